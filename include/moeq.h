@@ -15,6 +15,11 @@
  *   moe_nvfp4_repack        one-shot NVFP4 weight layout conversion
  *   moe_cast_bf16_to_f16    activations for the binary16 NVFP4 form
  *   moe_route_prep_noalloc  route prep for callers that cannot allocate
+ * and, for training and for adapters beside the quantized projections:
+ *   moe_permute, moe_permute_backward  token rows to sorted rows, gradient
+ *   moe_scatter_combine_backward       gradients of the combine
+ *   grouped_lora, grouped_lora_backward  low-rank adapters of the experts,
+ *                           or of the requests of a batch, and gradients
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer (memory the caller allocated
@@ -71,7 +76,8 @@ typedef enum {
   MOEQ_EHIP = 4          /* a HIP launch failed */
 } moeq_status;
 
-typedef enum { MOEQ_F16 = 1, MOEQ_BF16 = 2, MOEQ_F32 = 3, MOEQ_I32 = 4 } moeq_dtype;
+/* U8: moe_permute only (rows of quantized codes). */
+typedef enum { MOEQ_F16 = 1, MOEQ_BF16 = 2, MOEQ_F32 = 3, MOEQ_I32 = 4, MOEQ_U8 = 5 } moeq_dtype;
 
 /* MOEQ_ACT_SILU_MUL: the GEMM's N = 2I columns are [gate | up]
  * (columns [0, I) gate, [I, 2I) up); the call writes I columns
@@ -82,6 +88,12 @@ typedef enum { MOEQ_F16 = 1, MOEQ_BF16 = 2, MOEQ_F32 = 3, MOEQ_I32 = 4 } moeq_dt
 typedef enum { MOEQ_ACT_NONE = 0, MOEQ_ACT_SILU_MUL = 1, MOEQ_ACT_SILU_MUL_LIMIT = 2 } moeq_act;
 
 typedef enum { MOEQ_AROW_TOKEN = 0, MOEQ_AROW_SORTED = 1 } moeq_arow;
+
+/* Row order of grouped_lora's output (and base) and of its gradient dy:
+ *   MOEQ_OROW_SORTED: row s, the order of a grouped GEMM's output
+ *   MOEQ_OROW_PAIR  : row sorted_pair_ids[s], the order of the batch (with
+ *                     topk = 1 a token's own row) */
+typedef enum { MOEQ_OROW_SORTED = 0, MOEQ_OROW_PAIR = 1 } moeq_orow;
 
 /* Layout of NVFP4 block scales (C = K/16 per row).
  * MOEQ_SF_ROWS   [E][N][C] row-major, the layout of [TLK].
@@ -366,6 +378,124 @@ moeq_status moe_scatter_combine(const void* y, moeq_dtype y_dtype, const int32_t
  * ---------------------------------------------------------------------- */
 moeq_status moe_sum_pairs(const void* y_pairs, moeq_dtype y_dtype, const int32_t* pair_to_sorted, int64_t T,
                           int32_t topk, int64_t N, moeq_dtype out_dtype, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_permute - token rows copied to rows sorted by expert: the input of
+ * work that wants its rows contiguous per expert (an exchange between
+ * ranks, per-expert statistics, MOEQ_AROW_SORTED operands).
+ *
+ *   x   [T][N] dtype (F16 | BF16 | F32 | U8: rows of codes)
+ *   xs  [T*topk][N] dtype: xs[pair_to_sorted[t*topk+j]][:] = x[t][:] for
+ *       every pair that has an expert; the other rows (those past
+ *       expert_offsets[E]) are not written
+ * Requires N % 8 == 0 (U8: N % 16 == 0; else MOEQ_EALIGN), 16-byte aligned
+ * x and xs, xs disjoint from x (else MOEQ_EINVAL), 1 <= topk <= 64,
+ * T*topk < 2^31.
+ * ---------------------------------------------------------------------- */
+moeq_status moe_permute(const void* x, moeq_dtype dtype, const int32_t* pair_to_sorted, int64_t T, int32_t topk,
+                        int64_t N, void* xs, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_permute_backward - gradient of moe_permute (and of any call that reads
+ * token rows per pair, such as a grouped call with MOEQ_AROW_TOKEN):
+ *   dx[t][:] = sum_{j < topk, pair_to_sorted[t*topk+j] >= 0}
+ *                dxs[pair_to_sorted[t*topk+j]][:]
+ * accumulated in fp32 in slot order, rounded once; a token with no routed
+ * pair gets a zero row.
+ *
+ *   dxs  [T*topk][N] dxs_dtype (F16 | BF16 | F32), rows in sorted order
+ *   dx   [T][N] dx_dtype (F16 | BF16 | F32)
+ * Requires as moe_permute, dx disjoint from dxs.
+ * ---------------------------------------------------------------------- */
+moeq_status moe_permute_backward(const void* dxs, moeq_dtype dxs_dtype, const int32_t* pair_to_sorted, int64_t T,
+                                 int32_t topk, int64_t N, moeq_dtype dx_dtype, void* dx, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_scatter_combine_backward - gradients of moe_scatter_combine with
+ * respect to the expert rows and the top-k weights, for every pair
+ * p = t*topk + j with s = pair_to_sorted[p] >= 0:
+ *   dy[s][:]   = topk_weights[t][j] * dout[t][:]        (fp32, rounded once)
+ *   dw[t][j]   = sum_n dout[t][n] * y[s][n]             (fp32 sums)
+ * dw is 0 for pairs without an expert; rows of dy past expert_offsets[E] are
+ * not written.
+ *
+ *   dout  [T][N] dout_dtype, y [T*topk][N] y_dtype (each F16 | BF16 | F32)
+ *   dy    [T*topk][N] y_dtype;  dw f32 [T][topk]
+ * The sums are taken in a fixed order: equal inputs give equal bits.
+ * Requires N % 8 == 0, 16-byte aligned dout, y and dy, 1 <= topk <= 64,
+ * outputs disjoint from the inputs and from each other (else MOEQ_EINVAL).
+ * ---------------------------------------------------------------------- */
+moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype, const void* y, moeq_dtype y_dtype,
+                                         const int32_t* pair_to_sorted, const float* topk_weights, int64_t T,
+                                         int32_t topk, int64_t N, void* dy, float* dw, void* stream);
+
+/* ------------------------------------------------------------------------
+ * grouped_lora - low-rank adapters of E groups at once, added beside a
+ * projection.  The groups are the experts of a grouped GEMM (the tables of
+ * its moe_route_prep, rows in sorted order), or the adapters of the requests
+ * of a batch beside a shared projection (moe_route_prep over one adapter id
+ * per token with topk = 1, -1 = no adapter; MOEQ_OROW_PAIR keeps the rows in
+ * the order of the batch).  For every sorted row s < expert_offsets[E] of
+ * group e, with p = sorted_pair_ids[s]:
+ *   h[s][:]   = x[row][:] . A[e]^T            row = p / topk (TOKEN), s (SORTED)
+ *   out[o][:] = base[o][:] + scale[e] * h[s][:] . B[e]^T      o = s or p
+ * h is kept in fp32; sums in fp32; one rounding to the element type.
+ *
+ *   dtype  F16 | BF16: the type of x, a, b, base and out
+ *   x      [rows_x][K];  a [E][R][K];  b [E][N][R];  scale f32 [E] or NULL (1)
+ *   sorted_pair_ids  may be NULL with AROW_SORTED and OROW_SORTED; a row
+ *                    whose id is outside [0, P) is skipped
+ *   base   [P][N], or NULL (zero), or out itself (in place)
+ *   out    [P][N].  In place, rows without a group keep their value.  Out of
+ *          place, SORTED rows past expert_offsets[E] are not written, and
+ *          PAIR rows without a group become base (or zero), which needs
+ *   pair_to_sorted  int32 [P] (else NULL, not read)
+ *   h      NULL, or f32 [P][R] that receives h (rows past expert_offsets[E]
+ *          not written): what grouped_lora_backward reads
+ *   workspace  grouped_lora_workspace_bytes(P, E, N, K, R) bytes, contents
+ *          on entry ignored.  Calls that may overlap in time need their own.
+ * A group's rank may be below R: pad its A and B with zeros.  An infinity or
+ * NaN in an operand makes the outputs it enters infinite or NaN, without
+ * promise which of the two.
+ * Requires N, K and R multiples of 8 (else MOEQ_EALIGN), R <= 256,
+ * N, K <= 2^20, 1 <= E <= 1024, P < 2^31, 1 <= topk <= 64, rows_x * topk >= P
+ * (TOKEN) or rows_x >= P (SORTED), 16-byte aligned pointers (4-byte for the
+ * int32 tables and scale), and out, h and workspace disjoint from each other
+ * and the inputs (else MOEQ_EINVAL).  The workspace size of arguments
+ * outside these ranges is 0.
+ * ---------------------------------------------------------------------- */
+size_t grouped_lora_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R); /* host */
+
+moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_arow a_row, const void* a,
+                         const void* b, const float* scale, const int32_t* expert_offsets,
+                         const int32_t* sorted_pair_ids, const int32_t* pair_to_sorted, int64_t P, int32_t topk,
+                         int32_t E, int64_t N, int64_t K, int32_t R, const void* base, moeq_orow out_row, void* out,
+                         float* h, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * grouped_lora_backward - gradients of grouped_lora (base's is dy itself):
+ *   dh[s][:] = scale[e] * dy[o][:] . B[e]        (fp32, in the workspace)
+ *   dx[s][:] = dh[s][:] . A[e]
+ *   da[e]    = sum_{s of e} dh[s]^T x[row]       [R][K]
+ *   db[e]    = scale[e] * sum_{s of e} dy[o]^T h[s]   [N][R]
+ * sums in fp32, one rounding, in a fixed order: equal inputs give equal bits.
+ *
+ *   dy   [P][N] in out_row's order; x, a, b, scale and the tables as in the
+ *        forward call; h f32 [P][R] as it wrote it
+ *   dx   [P][K] in SORTED order, whatever a_row is (moe_permute_backward
+ *        sums TOKEN rows; rows past expert_offsets[E] are not written), or
+ *        NULL: not computed
+ *   da   [E][R][K], db [E][N][R]: written whole, zero for groups without rows
+ *   workspace  grouped_lora_backward_workspace_bytes(P, E, N, K, R) bytes
+ * Requires as grouped_lora; P == 0 writes zero da and db.
+ * ---------------------------------------------------------------------- */
+size_t grouped_lora_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R); /* host */
+
+moeq_status grouped_lora_backward(const void* dy, moeq_dtype dtype, moeq_orow out_row, const void* x, int64_t rows_x,
+                                  moeq_arow a_row, const void* a, const void* b, const float* scale, const float* h,
+                                  const int32_t* expert_offsets, const int32_t* sorted_pair_ids, int64_t P,
+                                  int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, void* dx, void* da,
+                                  void* db, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * moe_nvfp4_repack - convert NVFP4 expert weights from the layout [MMRM]

@@ -37,6 +37,8 @@ from .gemm import (grouped_gemm_qint4, grouped_gemm_qfp8_block, grouped_gemm_qnv
 from .combine import scatter_combine, pair_rows, sum_pairs
 from .layer import int4_layer, int4_ffn_layer, nvfp4_layer, fp8_dense, token_rows, combine_tokens
 from .quant import quantize_int4_rows
+from .permute import permute, permute_backward, scatter_combine_backward
+from .lora import grouped_lora, grouped_lora_backward
 from .layouts import (scale_swizzle_offset, unswizzle_scales, swizzle_scales, repack_nvfp4,
                       quads_from_rows, rows_from_quads, tiles_from_rows, rows_from_tiles)
 

@@ -21,20 +21,25 @@ LIB_PATH = os.path.join(_HERE, "libmoeq.so")
 
 # Status codes and enums of include/moeq.h.
 OK, EINVAL, EALIGN, EUNSUPPORTED, EHIP = 0, 1, 2, 3, 4
-F16, BF16, F32, I32 = 1, 2, 3, 4
+F16, BF16, F32, I32, U8 = 1, 2, 3, 4, 5
 ACT = {"none": 0, "silu_mul": 1}
 ACT_SILU_MUL_LIMIT = 2
 AROW = {"token": 0, "sorted": 1}
+OROW = {"sorted": 0, "pair": 1}
 SCHED = {"auto": 0, "decode": 1, "prefill": 2}
 SF_LAYOUT = {"rows": 0, "quads": 1}
 W_LAYOUT = {"rows": 0, "tiled": 1}
 
-_DTYPE_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32, torch.int32: I32}
+_DTYPE_CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32, torch.int32: I32,
+               torch.uint8: U8}
 
 EXPORTS = ("moeq_last_error", "moeq_abi_version", "moe_route_prep_workspace_bytes",
            "moe_route_prep", "grouped_gemm_qint4", "grouped_gemm_qfp8_block",
            "grouped_gemm_qnvfp4", "moe_scatter_combine", "moe_quantize_int4",
-           "moe_nvfp4_repack", "moe_sum_pairs", "moe_cast_bf16_to_f16", "moe_route_prep_noalloc")
+           "moe_nvfp4_repack", "moe_sum_pairs", "moe_cast_bf16_to_f16", "moe_route_prep_noalloc",
+           "moe_permute", "moe_permute_backward", "moe_scatter_combine_backward",
+           "grouped_lora_workspace_bytes", "grouped_lora", "grouped_lora_backward_workspace_bytes",
+           "grouped_lora_backward")
 
 # Fixed device scratch of moe_route_prep_noalloc per GPU (include/moeq.h).
 ROUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
@@ -83,6 +88,15 @@ def lib():
         "moe_nvfp4_repack": (i32, [vp, vp, i64, i64, i64, i32, i32, i32, vp, vp, vp]),
         "moe_sum_pairs": (i32, [vp, i32, vp, i64, i32, i64, i32, vp, vp]),
         "moe_cast_bf16_to_f16": (i32, [vp, i64, vp, vp]),
+        "moe_permute": (i32, [vp, i32, vp, i64, i32, i64, vp, vp]),
+        "moe_permute_backward": (i32, [vp, i32, vp, i64, i32, i64, i32, vp, vp]),
+        "moe_scatter_combine_backward": (i32, [vp, i32, vp, i32, vp, vp, i64, i32, i64, vp, vp, vp]),
+        "grouped_lora_workspace_bytes": (sz, [i64, i32, i64, i64, i32]),
+        "grouped_lora": (i32, [vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64, i64, i32, vp, i32,
+                               vp, vp, vp, sz, vp]),
+        "grouped_lora_backward_workspace_bytes": (sz, [i64, i32, i64, i64, i32]),
+        "grouped_lora_backward": (i32, [vp, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64,
+                                        i64, i32, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -122,6 +136,16 @@ def _gpu(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be on the GPU")
+
+
+def _here(**tensors):
+    """Every tensor argument (None: absent) must be in the current GPU's
+    memory: the kernels run on the current device's current stream."""
+    _gpu(**tensors)
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{cur}")
 
 
 def route_workspace_bytes(T: int, topk: int, E: int) -> int:
@@ -432,3 +456,183 @@ def nvfp4_repack(w, sf_swizzled, *, swap_halves: bool, sf_layout="rows", w_layou
                                 _stream())
     _check("moe_nvfp4_repack", st)
     return w_out, sf_out
+
+
+def _pairs(pair_to_sorted, topk):
+    """Tokens of a pair table."""
+    _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
+    if topk < 1 or pair_to_sorted.numel() % topk:
+        raise ValueError("pair_to_sorted must have T*topk entries")
+    return pair_to_sorted.numel() // topk
+
+
+def _fit(t, name, shape, dtype, device):
+    """The given output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def moe_permute(x, pair_to_sorted, topk: int, *, out=None):
+    """Token rows x [T][N] (f16, bf16, f32, or uint8 codes) copied to rows
+    sorted by expert: out[pair_to_sorted[t*topk+j]] = x[t].  Returns out
+    [T*topk][N]; rows past expert_offsets[E] are not written."""
+    _need(x, "x", (torch.float16, torch.bfloat16, torch.float32, torch.uint8), 2)
+    T = _pairs(pair_to_sorted, topk)
+    N = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x must have {T} rows, one per token of pair_to_sorted")
+    out = _fit(out, "out", (T * topk, N), x.dtype, x.device)
+    _here(x=x, pair_to_sorted=pair_to_sorted, out=out)
+    st = lib().moe_permute(_ptr(x), _DTYPE_CODE[x.dtype], _ptr(pair_to_sorted), T, topk, N, _ptr(out), _stream())
+    _check("moe_permute", st)
+    return out
+
+
+def moe_permute_backward(dxs, pair_to_sorted, topk: int, *, out_dtype=None, out=None):
+    """Gradient of moe_permute: dx[t] = sum over the routed slots of token t
+    of dxs[pair_to_sorted[t*topk+j]], fp32 in slot order, one rounding.
+    dxs [T*topk][N] in sorted order; returns dx [T][N]."""
+    _need(dxs, "dxs", (torch.float16, torch.bfloat16, torch.float32), 2)
+    T = _pairs(pair_to_sorted, topk)
+    N = dxs.shape[1]
+    if dxs.shape[0] < T * topk:
+        raise ValueError("dxs must have at least T*topk rows (sorted positions index into it)")
+    out_dtype = out_dtype or dxs.dtype
+    if out_dtype not in (torch.float16, torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype {out_dtype} is not a floating type of the library")
+    out = _fit(out, "out", (T, N), out_dtype, dxs.device)
+    _here(dxs=dxs, pair_to_sorted=pair_to_sorted, out=out)
+    st = lib().moe_permute_backward(_ptr(dxs), _DTYPE_CODE[dxs.dtype], _ptr(pair_to_sorted), T, topk, N,
+                                    _DTYPE_CODE[out_dtype], _ptr(out), _stream())
+    _check("moe_permute_backward", st)
+    return out
+
+
+def moe_scatter_combine_backward(dout, y, pair_to_sorted, topk_weights, *, dy=None, dw=None):
+    """Gradients of moe_scatter_combine: dy[s] = topk_weights[t, j] * dout[t]
+    (y's type) and dw[t, j] = <dout[t], y[s]> (f32; 0 for slots without an
+    expert), s = pair_to_sorted[t*topk+j].  Returns (dy, dw); rows of dy past
+    expert_offsets[E] are not written."""
+    floats = (torch.float16, torch.bfloat16, torch.float32)
+    _need(dout, "dout", floats, 2)
+    _need(y, "y", floats, 2)
+    _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
+    _need(topk_weights, "topk_weights", torch.float32, 2)
+    T, k = topk_weights.shape
+    N = y.shape[1]
+    if tuple(dout.shape) != (T, N):
+        raise ValueError(f"dout must be [{T}][{N}], got {tuple(dout.shape)}")
+    if pair_to_sorted.numel() != T * k or y.shape[0] != T * k:
+        raise ValueError("pair_to_sorted needs T*topk entries and y T*topk rows")
+    dy = _fit(dy, "dy", (T * k, N), y.dtype, y.device)
+    dw = _fit(dw, "dw", (T, k), torch.float32, y.device)
+    _here(dout=dout, y=y, pair_to_sorted=pair_to_sorted, topk_weights=topk_weights, dy=dy, dw=dw)
+    st = lib().moe_scatter_combine_backward(_ptr(dout), _DTYPE_CODE[dout.dtype], _ptr(y), _DTYPE_CODE[y.dtype],
+                                            _ptr(pair_to_sorted), _ptr(topk_weights), T, k, N, _ptr(dy), _ptr(dw),
+                                            _stream())
+    _check("moe_scatter_combine_backward", st)
+    return dy, dw
+
+
+def lora_workspace_bytes(P: int, E: int, N: int, K: int, R: int, *, backward=False) -> int:
+    f = lib().grouped_lora_backward_workspace_bytes if backward else lib().grouped_lora_workspace_bytes
+    return int(f(P, E, N, K, R))
+
+
+def _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids, a_row, rows):
+    _need(x, "x", (torch.float16, torch.bfloat16), 2)
+    _need(a, "a", x.dtype, 3)
+    _need(b, "b", x.dtype, 3)
+    _need(expert_offsets, "expert_offsets", torch.int32, 1)
+    if sorted_pair_ids is not None:
+        _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, 1)
+    E, R, K = a.shape
+    N = b.shape[1]
+    if tuple(b.shape) != (E, N, R) or x.shape[1] != K or expert_offsets.numel() != E + 1:
+        raise ValueError("inconsistent adapter shapes: x [rows][K], a [E][R][K], b [E][N][R], expert_offsets [E+1]")
+    if scale is not None:
+        _need(scale, "scale", torch.float32, 1)
+        if scale.numel() != E:
+            raise ValueError(f"scale must have {E} values")
+    P = sorted_pair_ids.numel() if sorted_pair_ids is not None else rows
+    return E, R, K, N, P
+
+
+def _lora_ws(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _need(workspace, "workspace")
+    return workspace
+
+
+def grouped_lora(x, a, b, expert_offsets, sorted_pair_ids, topk: int, *, base=None, scale=None, a_row="token",
+                 out_row="sorted", pair_to_sorted=None, out=None, h=None, workspace=None):
+    """Low-rank adapters beside a projection: out[o] = base[o] + scale[e] *
+    (x[row] a[e]^T) b[e]^T for every sorted row s of group e.
+
+    x f16 or bf16 [rows][K], a [E][R][K], b [E][N][R] and base [P][N] of the
+    same type; scale f32 [E] (None: 1).  The groups are experts (the tables of
+    their route prep), or the adapters of a batch's requests (route prep over
+    one adapter id per token, topk 1, -1 for none).  row: sorted_pair_ids[s]
+    // topk ('token') or s ('sorted'); o: s ('sorted') or sorted_pair_ids[s]
+    ('pair', the order of the batch).  base None: zero; base the same tensor
+    as out: in place, rows without a group keep their value.  Out of place,
+    'pair' rows without a group become base and need pair_to_sorted; 'sorted'
+    rows past expert_offsets[E] are not written.  h (f32 [P][R]) receives
+    x[row] a[e]^T for grouped_lora_backward.  workspace: uint8,
+    lora_workspace_bytes(P, E, N, K, R).  Returns out [P][N]."""
+    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+    E, R, K, N, P = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids, a_row, rows)
+    if base is not None:
+        base = _fit(base, "base", (P, N), x.dtype, x.device)
+    if pair_to_sorted is not None:
+        _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
+        if pair_to_sorted.numel() != P:
+            raise ValueError(f"pair_to_sorted must have {P} entries")
+    out = _fit(out, "out", (P, N), x.dtype, x.device)
+    if h is not None:
+        h = _fit(h, "h", (P, R), torch.float32, x.device)
+    workspace = _lora_ws(workspace, lora_workspace_bytes(P, E, N, K, R), x.device)
+    _here(x=x, a=a, b=b, scale=scale, expert_offsets=expert_offsets, sorted_pair_ids=sorted_pair_ids,
+          pair_to_sorted=pair_to_sorted, base=base, out=out, h=h, workspace=workspace)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().grouped_lora(_ptr(x), _DTYPE_CODE[x.dtype], x.shape[0], AROW[a_row], _ptr(a), _ptr(b), _ptr(scale),
+                            _ptr(expert_offsets), _ptr(sorted_pair_ids), _ptr(pair_to_sorted), P, topk, E, N, K, R,
+                            _ptr(base), OROW[out_row], _ptr(out), _ptr(h), _ptr(workspace), wsb, _stream())
+    _check("grouped_lora", st)
+    return out
+
+
+def grouped_lora_backward(dy, x, a, b, h, expert_offsets, sorted_pair_ids, topk: int, *, scale=None, a_row="token",
+                          out_row="sorted", need_dx=True, dx=None, da=None, db=None, workspace=None):
+    """Gradients of grouped_lora: dy [P][N] in out_row's order, h f32 [P][R]
+    as the forward call wrote it, the other arguments as there.  Returns
+    (dx [P][K] in sorted order, or None without need_dx; da [E][R][K];
+    db [E][N][R]), all of x's type: da and db are written whole, rows of dx
+    past expert_offsets[E] are not.  With a_row 'token', moe_permute_backward
+    sums dx over each token's slots.  workspace: uint8,
+    lora_workspace_bytes(P, E, N, K, R, backward=True)."""
+    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
+    E, R, K, N, P = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids, a_row, rows)
+    dy = _fit(dy, "dy", (P, N), x.dtype, x.device) if dy is not None else _need(dy, "dy")
+    h = _fit(h, "h", (P, R), torch.float32, x.device) if h is not None else _need(h, "h")
+    if need_dx:
+        dx = _fit(dx, "dx", (P, K), x.dtype, x.device)
+    elif dx is not None:
+        raise ValueError("dx is given, but need_dx is false")
+    da = _fit(da, "da", (E, R, K), x.dtype, x.device)
+    db = _fit(db, "db", (E, N, R), x.dtype, x.device)
+    workspace = _lora_ws(workspace, lora_workspace_bytes(P, E, N, K, R, backward=True), x.device)
+    _here(dy=dy, x=x, a=a, b=b, h=h, scale=scale, expert_offsets=expert_offsets, sorted_pair_ids=sorted_pair_ids,
+          dx=dx, da=da, db=db, workspace=workspace)
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().grouped_lora_backward(_ptr(dy), _DTYPE_CODE[x.dtype], OROW[out_row], _ptr(x), x.shape[0], AROW[a_row],
+                                     _ptr(a), _ptr(b), _ptr(scale), _ptr(h), _ptr(expert_offsets),
+                                     _ptr(sorted_pair_ids), P, topk, E, N, K, R, _ptr(dx), _ptr(da), _ptr(db),
+                                     _ptr(workspace), wsb, _stream())
+    _check("grouped_lora_backward", st)
+    return dx, da, db

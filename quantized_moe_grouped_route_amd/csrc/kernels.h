@@ -24,7 +24,22 @@ hipError_t launch_route_noalloc(const int* ids, int P, int E, int* offsets, int*
 // Combine.  y_kind / out_kind are OutKind values.  tw == null: y holds
 // pre-weighted rows in pair order (row t*topk + j), summed unweighted.
 hipError_t launch_combine(const void* y, int y_kind, const int* p2s, const float* tw, int T,
-                          int topk, int N, int64_t P, int out_kind, void* out, hipStream_t stream);
+                          int topk, int N, int out_kind, void* out, hipStream_t stream);
+
+// Workgroups of 256 threads one launch may have: a grid's size in threads is
+// a 32-bit field of the dispatch packet.
+constexpr int kMaxBlocks = 1 << 23;
+
+// Token rows to sorted rows (row_bytes % 16 == 0), and its gradient: the
+// unweighted sum of each token's sorted rows.
+hipError_t launch_permute(const void* x, const int* p2s, int T, int topk, int64_t row_bytes, void* xs, int num_cus,
+                          hipStream_t stream);
+hipError_t launch_permute_bwd(const void* dxs, int dxs_kind, const int* p2s, int T, int topk, int N, int out_kind,
+                              void* dx, hipStream_t stream);
+// Gradients of the weighted combine.
+hipError_t launch_combine_bwd(const void* dout, int dout_kind, const void* y, int y_kind, const int* p2s,
+                              const float* tw, int T, int topk, int N, void* dy, float* dw, int num_cus,
+                              hipStream_t stream);
 
 // Per-row symmetric INT4 quantization (x_kind: OutKind of the input).
 hipError_t launch_quant_int4(const void* x, int x_kind, int64_t rows, int K, uint8_t* q, float* scale,
@@ -60,6 +75,31 @@ hipError_t launch_gemm_fp8(const GroupedArgs& g, const uint8_t* a, const float* 
                            const uint8_t* w, const float* w_scale, hipStream_t stream);
 hipError_t launch_gemm_nvfp4(const GroupedArgs& g, const uint16_t* x, const uint8_t* w,
                              const uint8_t* w_sf, const float* w_gscale, hipStream_t stream);
+
+// Low-rank adapters beside a projection, rows grouped by adapter.
+struct LoraArgs {
+  const int* offsets;       // [E+1]
+  const int* sorted_ids;    // [P] or null (identity rows)
+  const int* p2s;           // [P] or null (pair-ordered output only)
+  int64_t P;                // rows
+  int E;                    // adapters
+  int x_div;                // row of x: sorted_ids[s] / x_div, or s where 0
+  int out_pair;             // 1: row of out / base / dy is sorted_ids[s], 0: s
+  int N;
+  int K;
+  int R;
+  int f16;                  // element type: binary16 (else bf16)
+  const float* scale;       // [E] or null (1)
+};
+size_t lora_workspace_bytes(int64_t P, int E, int N, int K, int R);
+size_t lora_bwd_workspace_bytes(int64_t P, int E, int N, int K, int R);
+// h: null, or [P][R] that receives the shrunk rows.
+hipError_t launch_lora(const LoraArgs& g, const uint16_t* x, const uint16_t* a, const uint16_t* b,
+                       const uint16_t* base, uint16_t* out, float* h, void* ws, hipStream_t stream);
+// dx: null where it is not wanted.
+hipError_t launch_lora_bwd(const LoraArgs& g, const uint16_t* dy, const uint16_t* x, const uint16_t* a,
+                           const uint16_t* b, const float* h, uint16_t* dx, uint16_t* da, uint16_t* db, void* ws,
+                           hipStream_t stream);
 
 // bf16 -> binary16 (round to nearest even), n values, n % 8 == 0.
 hipError_t launch_cast_bf16_f16(const uint16_t* x, int64_t n, uint16_t* y, int num_cus, hipStream_t stream);

@@ -33,6 +33,7 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxTopk = 64;
+constexpr int kMaxRank = 256;
 
 // Compute units of the current device, looked up once per device.  Calls
 // may come from several host threads at once; each stores the same value.
@@ -103,6 +104,78 @@ moeq::GroupedArgs make_args(const int32_t* offsets, const int32_t* sorted, int64
   g.sched = (int)sched;
   g.queue = nullptr;
   g.num_cus = device_cus();
+  return g;
+}
+
+// [a, a + na) and [b, b + nb) share a byte; null or empty ranges never do.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+bool float_dtype(moeq_dtype d) { return d == MOEQ_F16 || d == MOEQ_BF16 || d == MOEQ_F32; }
+int64_t float_bytes(moeq_dtype d) { return d == MOEQ_F32 ? 4 : 2; }
+
+// Sizes shared by the calls over token rows and the rows of their pairs.
+moeq_status check_tokens(const char* fn, int64_t T, int32_t topk, int64_t N, int64_t n_align) {
+  if (T < 0 || T >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: T=%lld outside [0, 2^31)", fn, (long long)T);
+  if (topk < 1 || topk > kMaxTopk) return fail(MOEQ_EINVAL, "%s: topk=%d outside [1, %d]", fn, topk, kMaxTopk);
+  if (N <= 0 || N > (1 << 24)) return fail(MOEQ_EINVAL, "%s: N=%lld out of range", fn, (long long)N);
+  if (N % n_align != 0)
+    return fail(MOEQ_EALIGN, "%s: N=%lld must be a multiple of %lld", fn, (long long)N, (long long)n_align);
+  if (T * (int64_t)topk >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: T*topk too large", fn);
+  return MOEQ_OK;
+}
+
+bool lora_sizes_ok(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
+  return P >= 0 && P < (int64_t(1) << 31) && E >= 1 && E <= kMaxE && N >= 8 && N <= (1 << 20) && N % 8 == 0 &&
+         K >= 8 && K <= (1 << 20) && K % 8 == 0 && R >= 8 && R <= kMaxRank && R % 8 == 0;
+}
+
+// Checks shared by grouped_lora and its gradient.
+moeq_status check_lora(const char* fn, moeq_dtype dtype, const void* x, int64_t rows_x, int a_row, const void* a,
+                       const void* b, const float* scale, const int32_t* offsets, const int32_t* sorted, int64_t P,
+                       int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, int out_row) {
+  if (dtype != MOEQ_F16 && dtype != MOEQ_BF16) return fail(MOEQ_EUNSUPPORTED, "%s: dtype %d", fn, dtype);
+  if (E < 1 || E > kMaxE) return fail(MOEQ_EINVAL, "%s: E=%d outside [1, %d]", fn, E, kMaxE);
+  if (topk < 1 || topk > kMaxTopk) return fail(MOEQ_EINVAL, "%s: topk=%d outside [1, %d]", fn, topk, kMaxTopk);
+  if (P < 0 || P >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: P=%lld out of range", fn, (long long)P);
+  if (N <= 0 || K <= 0 || N > (1 << 20) || K > (1 << 20))
+    return fail(MOEQ_EINVAL, "%s: N=%lld K=%lld out of range", fn, (long long)N, (long long)K);
+  if (R < 1 || R > kMaxRank) return fail(MOEQ_EINVAL, "%s: R=%d outside [1, %d]", fn, R, kMaxRank);
+  if (N % 8 != 0 || K % 8 != 0 || R % 8 != 0)
+    return fail(MOEQ_EALIGN, "%s: N=%lld, K=%lld and R=%d must be multiples of 8", fn, (long long)N, (long long)K, R);
+  if (a_row != MOEQ_AROW_TOKEN && a_row != MOEQ_AROW_SORTED) return fail(MOEQ_EINVAL, "%s: bad a_row %d", fn, a_row);
+  if (out_row != MOEQ_OROW_SORTED && out_row != MOEQ_OROW_PAIR)
+    return fail(MOEQ_EINVAL, "%s: bad out_row %d", fn, out_row);
+  if (rows_x < 0 || rows_x >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: rows_x=%lld out of range", fn, (long long)rows_x);
+  if (a_row == MOEQ_AROW_TOKEN ? rows_x * topk < P : rows_x < P)
+    return fail(MOEQ_EINVAL, "%s: rows_x=%lld is too few for P=%lld", fn, (long long)rows_x, (long long)P);
+  if (!a || !b || !offsets || (P > 0 && !x)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (P > 0 && !sorted && (a_row != MOEQ_AROW_SORTED || out_row != MOEQ_OROW_SORTED))
+    return fail(MOEQ_EINVAL, "%s: token rows and pair-ordered rows need sorted_pair_ids", fn);
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) || !aligned(offsets, 4) ||
+      !aligned(sorted, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  return MOEQ_OK;
+}
+
+moeq::LoraArgs lora_args(moeq_dtype dtype, int a_row, const float* scale, const int32_t* offsets,
+                         const int32_t* sorted, const int32_t* p2s, int64_t P, int32_t topk, int32_t E, int64_t N,
+                         int64_t K, int32_t R, int out_row) {
+  moeq::LoraArgs g;
+  g.offsets = offsets;
+  g.sorted_ids = sorted;
+  g.p2s = p2s;
+  g.P = P;
+  g.E = E;
+  g.x_div = a_row == MOEQ_AROW_TOKEN ? topk : 0;
+  g.out_pair = out_row == MOEQ_OROW_PAIR ? 1 : 0;
+  g.N = (int)N;
+  g.K = (int)K;
+  g.R = R;
+  g.f16 = dtype == MOEQ_F16 ? 1 : 0;
+  g.scale = scale;
   return g;
 }
 
@@ -283,8 +356,7 @@ moeq_status moe_scatter_combine(const void* y, moeq_dtype y_dtype, const int32_t
   if (!aligned(y, 16) || !aligned(out, 16) || !aligned(pair_to_sorted, 4) || !aligned(topk_weights, 4))
     return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
   return hip_status(moeq::launch_combine(y, (int)y_dtype, pair_to_sorted, topk_weights, (int)T, topk,
-                                         (int)N, T * (int64_t)topk, (int)out_dtype, out,
-                                         (hipStream_t)stream),
+                                         (int)N, (int)out_dtype, out, (hipStream_t)stream),
                     fn);
 }
 
@@ -304,7 +376,147 @@ moeq_status moe_sum_pairs(const void* y_pairs, moeq_dtype y_dtype, const int32_t
   if (!aligned(y_pairs, 16) || !aligned(out, 16) || !aligned(pair_to_sorted, 4))
     return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
   return hip_status(moeq::launch_combine(y_pairs, (int)y_dtype, pair_to_sorted, nullptr, (int)T, topk, (int)N,
-                                         T * (int64_t)topk, (int)out_dtype, out, (hipStream_t)stream),
+                                         (int)out_dtype, out, (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status moe_permute(const void* x, moeq_dtype dtype, const int32_t* pair_to_sorted, int64_t T, int32_t topk,
+                        int64_t N, void* xs, void* stream) {
+  const char* fn = "moe_permute";
+  int64_t elem = 0, unit = 8;
+  switch (dtype) {
+    case MOEQ_F16: case MOEQ_BF16: elem = 2; break;
+    case MOEQ_F32: elem = 4; break;
+    case MOEQ_U8: elem = 1; unit = 16; break;
+    default: return fail(MOEQ_EUNSUPPORTED, "%s: dtype %d", fn, dtype);
+  }
+  moeq_status st = check_tokens(fn, T, topk, N, unit);
+  if (st != MOEQ_OK) return st;
+  if (T > 0 && (!x || !pair_to_sorted || !xs)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(pair_to_sorted, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  if (overlap(xs, T * topk * N * elem, x, T * N * elem)) return fail(MOEQ_EINVAL, "%s: xs overlaps x", fn);
+  return hip_status(moeq::launch_permute(x, pair_to_sorted, (int)T, topk, N * elem, xs, device_cus(),
+                                         (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status moe_permute_backward(const void* dxs, moeq_dtype dxs_dtype, const int32_t* pair_to_sorted, int64_t T,
+                                 int32_t topk, int64_t N, moeq_dtype dx_dtype, void* dx, void* stream) {
+  const char* fn = "moe_permute_backward";
+  moeq_status st = check_tokens(fn, T, topk, N, 8);
+  if (st != MOEQ_OK) return st;
+  if (!float_dtype(dxs_dtype)) return fail(MOEQ_EUNSUPPORTED, "%s: dxs dtype %d", fn, dxs_dtype);
+  if (!float_dtype(dx_dtype)) return fail(MOEQ_EUNSUPPORTED, "%s: dx dtype %d", fn, dx_dtype);
+  if (T > 0 && (!dxs || !pair_to_sorted || !dx)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(dxs, 16) || !aligned(dx, 16) || !aligned(pair_to_sorted, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  if (overlap(dx, T * N * float_bytes(dx_dtype), dxs, T * topk * N * float_bytes(dxs_dtype)))
+    return fail(MOEQ_EINVAL, "%s: dx overlaps dxs", fn);
+  return hip_status(moeq::launch_permute_bwd(dxs, (int)dxs_dtype, pair_to_sorted, (int)T, topk, (int)N,
+                                             (int)dx_dtype, dx, (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype, const void* y, moeq_dtype y_dtype,
+                                         const int32_t* pair_to_sorted, const float* topk_weights, int64_t T,
+                                         int32_t topk, int64_t N, void* dy, float* dw, void* stream) {
+  const char* fn = "moe_scatter_combine_backward";
+  moeq_status st = check_tokens(fn, T, topk, N, 8);
+  if (st != MOEQ_OK) return st;
+  if (!float_dtype(dout_dtype)) return fail(MOEQ_EUNSUPPORTED, "%s: dout dtype %d", fn, dout_dtype);
+  if (!float_dtype(y_dtype)) return fail(MOEQ_EUNSUPPORTED, "%s: y dtype %d", fn, y_dtype);
+  if (T > 0 && (!dout || !y || !pair_to_sorted || !topk_weights || !dy || !dw))
+    return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(pair_to_sorted, 4) ||
+      !aligned(topk_weights, 4) || !aligned(dw, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  const int64_t db = T * N * float_bytes(dout_dtype), yb = T * topk * N * float_bytes(y_dtype), wb = T * topk * 4;
+  if (overlap(dy, yb, dout, db) || overlap(dy, yb, y, yb) || overlap(dy, yb, topk_weights, wb) ||
+      overlap(dw, wb, topk_weights, wb) || overlap(dw, wb, dy, yb) || overlap(dw, wb, y, yb) ||
+      overlap(dw, wb, dout, db))
+    return fail(MOEQ_EINVAL, "%s: an output overlaps an input or the other output", fn);
+  return hip_status(moeq::launch_combine_bwd(dout, (int)dout_dtype, y, (int)y_dtype, pair_to_sorted, topk_weights,
+                                             (int)T, topk, (int)N, dy, dw, device_cus(), (hipStream_t)stream),
+                    fn);
+}
+
+size_t grouped_lora_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
+  return lora_sizes_ok(P, E, N, K, R) ? moeq::lora_workspace_bytes(P, E, (int)N, (int)K, R) : 0;
+}
+
+size_t grouped_lora_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
+  return lora_sizes_ok(P, E, N, K, R) ? moeq::lora_bwd_workspace_bytes(P, E, (int)N, (int)K, R) : 0;
+}
+
+moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_arow a_row, const void* a,
+                         const void* b, const float* scale, const int32_t* expert_offsets,
+                         const int32_t* sorted_pair_ids, const int32_t* pair_to_sorted, int64_t P, int32_t topk,
+                         int32_t E, int64_t N, int64_t K, int32_t R, const void* base, moeq_orow out_row, void* out,
+                         float* h, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "grouped_lora";
+  moeq_status st = check_lora(fn, dtype, x, rows_x, a_row, a, b, scale, expert_offsets, sorted_pair_ids, P, topk, E,
+                              N, K, R, out_row);
+  if (st != MOEQ_OK) return st;
+  if (P > 0 && !out) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(out, 16) || !aligned(base, 16) || !aligned(h, 16) || !aligned(workspace, 16) ||
+      !aligned(pair_to_sorted, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  if (P > 0 && out_row == MOEQ_OROW_PAIR && base != out && !pair_to_sorted)
+    return fail(MOEQ_EINVAL, "%s: pair-ordered rows out of place need pair_to_sorted", fn);
+  const int64_t ob = P * N * 2, hb = P * R * 4;
+  if ((base != out && overlap(out, ob, base, ob)) || overlap(out, ob, x, rows_x * K * 2) ||
+      overlap(out, ob, a, E * K * R * 2) || overlap(out, ob, b, E * N * R * 2))
+    return fail(MOEQ_EINVAL, "%s: out overlaps an input (base may be out itself)", fn);
+  if (overlap(h, hb, out, ob) || overlap(h, hb, base, ob) || overlap(h, hb, x, rows_x * K * 2))
+    return fail(MOEQ_EINVAL, "%s: h overlaps another argument", fn);
+  const size_t need = moeq::lora_workspace_bytes(P, E, (int)N, (int)K, R);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
+  if (overlap(workspace, (int64_t)need, out, ob) || overlap(workspace, (int64_t)need, base, ob) ||
+      overlap(workspace, (int64_t)need, x, rows_x * K * 2) || overlap(workspace, (int64_t)need, h, hb))
+    return fail(MOEQ_EINVAL, "%s: workspace overlaps another argument", fn);
+  const moeq::LoraArgs g = lora_args(dtype, a_row, scale, expert_offsets, sorted_pair_ids, pair_to_sorted, P, topk, E,
+                                     N, K, R, out_row);
+  return hip_status(moeq::launch_lora(g, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(a),
+                                      static_cast<const uint16_t*>(b), static_cast<const uint16_t*>(base),
+                                      static_cast<uint16_t*>(out), h, workspace, (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status grouped_lora_backward(const void* dy, moeq_dtype dtype, moeq_orow out_row, const void* x, int64_t rows_x,
+                                  moeq_arow a_row, const void* a, const void* b, const float* scale, const float* h,
+                                  const int32_t* expert_offsets, const int32_t* sorted_pair_ids, int64_t P,
+                                  int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, void* dx, void* da,
+                                  void* db, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "grouped_lora_backward";
+  moeq_status st = check_lora(fn, dtype, x, rows_x, a_row, a, b, scale, expert_offsets, sorted_pair_ids, P, topk, E,
+                              N, K, R, out_row);
+  if (st != MOEQ_OK) return st;
+  if (!da || !db || (P > 0 && (!dy || !h))) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(dx, 16) || !aligned(da, 16) || !aligned(db, 16) ||
+      !aligned(workspace, 16))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  const size_t need = moeq::lora_bwd_workspace_bytes(P, E, (int)N, (int)K, R);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
+  const struct { const void* p; int64_t n; } outs[4] = {{dx, P * K * 2}, {da, E * K * R * 2}, {db, E * N * R * 2},
+                                                        {workspace, (int64_t)need}},
+      ins[5] = {{dy, P * N * 2}, {x, rows_x * K * 2}, {a, E * K * R * 2}, {b, E * N * R * 2}, {h, P * R * 4}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 5; ++j)
+      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
+        return fail(MOEQ_EINVAL, "%s: an output or the workspace overlaps an input", fn);
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return fail(MOEQ_EINVAL, "%s: two outputs, or an output and the workspace, overlap", fn);
+  }
+  const moeq::LoraArgs g = lora_args(dtype, a_row, scale, expert_offsets, sorted_pair_ids, nullptr, P, topk, E, N, K,
+                                     R, out_row);
+  return hip_status(moeq::launch_lora_bwd(g, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
+                                          static_cast<const uint16_t*>(a), static_cast<const uint16_t*>(b), h,
+                                          static_cast<uint16_t*>(dx), static_cast<uint16_t*>(da),
+                                          static_cast<uint16_t*>(db), workspace, (hipStream_t)stream),
                     fn);
 }
 
@@ -353,11 +565,7 @@ moeq_status moe_nvfp4_repack(const uint8_t* w_in, const uint8_t* sf_in, int64_t 
   if (!w_in || !sf_in || !w_out || !sf_out) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(w_in, 16) || !aligned(sf_in, 16) || !aligned(w_out, 16) || !aligned(sf_out, 16))
     return fail(MOEQ_EALIGN, "%s: pointers must be 16-byte aligned", fn);
-  const uintptr_t wb = (uintptr_t)(E * N * (K / 2)), sb = (uintptr_t)(E * N * (K / 16));
-  auto overlap = [](const void* a, uintptr_t na, const void* b, uintptr_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
-  };
+  const int64_t wb = E * N * (K / 2), sb = E * N * (K / 16);
   if (overlap(w_out, wb, w_in, wb) || overlap(w_out, wb, sf_in, sb) || overlap(w_out, wb, sf_out, sb) ||
       overlap(sf_out, sb, w_in, wb) || overlap(sf_out, sb, sf_in, sb))
     return fail(MOEQ_EINVAL, "%s: an output overlaps an input or the other output (no in-place repack)", fn);
