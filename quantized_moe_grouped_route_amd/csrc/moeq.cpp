@@ -129,7 +129,8 @@ moeq_status check_tokens(const char* fn, int64_t T, int32_t topk, int64_t N, int
 
 bool lora_sizes_ok(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
   return P >= 0 && P < (int64_t(1) << 31) && E >= 1 && E <= kMaxE && N >= 8 && N <= (1 << 20) && N % 8 == 0 &&
-         K >= 8 && K <= (1 << 20) && K % 8 == 0 && R >= 8 && R <= kMaxRank && R % 8 == 0;
+         K >= 8 && K <= (1 << 20) && K % 8 == 0 && R >= 8 && R <= kMaxRank && R % 8 == 0 &&
+         moeq::lora_fits(P, E, (int)N, (int)K, R);
 }
 
 // Checks shared by grouped_lora and its gradient.
@@ -145,6 +146,9 @@ moeq_status check_lora(const char* fn, moeq_dtype dtype, const void* x, int64_t 
   if (R < 1 || R > kMaxRank) return fail(MOEQ_EINVAL, "%s: R=%d outside [1, %d]", fn, R, kMaxRank);
   if (N % 8 != 0 || K % 8 != 0 || R % 8 != 0)
     return fail(MOEQ_EALIGN, "%s: N=%lld, K=%lld and R=%d must be multiples of 8", fn, (long long)N, (long long)K, R);
+  if (!moeq::lora_fits(P, E, (int)N, (int)K, R))
+    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld, R=%d are too large for one launch", fn, (long long)P, E,
+                (long long)N, (long long)K, R);
   if (a_row != MOEQ_AROW_TOKEN && a_row != MOEQ_AROW_SORTED) return fail(MOEQ_EINVAL, "%s: bad a_row %d", fn, a_row);
   if (out_row != MOEQ_OROW_SORTED && out_row != MOEQ_OROW_PAIR)
     return fail(MOEQ_EINVAL, "%s: bad out_row %d", fn, out_row);
