@@ -93,6 +93,17 @@ __device__ __forceinline__ u32x4 column_of(const u32x4 rows[8], int j) {
   return v;
 }
 
+// Two transposing LDS reads: lane i of each 16 gets column i of the 4 x 16
+// block whose row j/4, columns 4 (j % 4) .. +3 its lane j points at.
+__device__ __forceinline__ u32x4 transposed8(const uint16_t* a, const uint16_t* b) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds4;
+  typedef u32 u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)a));
+  const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)b));
+  return u32x4{x[0], x[1], y[0], y[1]};
+}
+
 // Exponent of the power of two that brings m (finite, >= 0) to [2^8, 2^9):
 // far from both ends of binary16, with 2^6 of room before 2^15.
 __device__ __forceinline__ int half_exp(float m) { return 135 - max(1, __float_as_int(m) >> 23); }
@@ -102,16 +113,20 @@ __device__ __forceinline__ float ldexp2(float v, int e) { return __builtin_amdgc
 constexpr int kShrinkWaves = 8;
 constexpr int kShrinkThreads = 64 * kShrinkWaves;
 
-// part[split][s][r] = sum over the split's columns of X[row(s)][k] W[e][r][k].
-// One workgroup: 16 RT rows of one group, 16 NR ranks, one split of the
+// part[split][s][r] = sum over the split's columns of X[row(s)][k] W[e][r][k]
+// (W [E][R][C]; C_MAJOR: W [E][C][R], as B is stored for dh).  One workgroup: 16 RT rows of one group, 16 NR ranks, one split of the
 // columns, dealt to its 8 waves in steps of 128.  Rows past the tile and ranks
 // past R repeat valid ones: they only reach results that are not stored.
-template <int KIND, int RT, int NR>
+// C_MAJOR weights pass through the wave's own piece of LDS, 32 columns at a
+// time, and come back through the transposing read (lane i of 16 gets column
+// i of a 4 x 16 block), so that B needs no transposed copy in memory.
+template <int KIND, int RT, int NR, bool C_MAJOR>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm,
                                                                 int C, const uint16_t* __restrict__ W,
                                                                 float* __restrict__ part, int splits, int rchunks) {
   constexpr int BM = 16 * RT, RW = 16 * NR + 4;
   __shared__ __align__(16) int sm[cmax(kTableInts, kShrinkWaves * BM * RW)];
+  __shared__ __align__(16) uint16_t turn[C_MAJOR ? kShrinkWaves : 1][32 * 16 * NR];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, c = lane & 15, q = lane >> 4;
   const int rc = blockIdx.x % rchunks, sp = blockIdx.x / rchunks % splits, w = blockIdx.x / rchunks / splits;
   sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, BM, 1);
@@ -126,8 +141,14 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
   }
   const uint16_t* wp[NR];
 #pragma unroll
-  for (int n = 0; n < NR; ++n)
-    wp[n] = W + ((int64_t)t.e * g.R + min(rc * 64 + n * 16 + c, g.R - 1)) * C;
+  for (int n = 0; n < NR; ++n) {
+    if (C_MAJOR) {  // piece p of 32 columns: row p / 2NR, 8 ranks
+      const int p = lane + 64 * n, row = p / (2 * NR), o = min(rc * 8 + p % (2 * NR), g.R / 8 - 1);
+      wp[n] = W + ((int64_t)t.e * C + (row / 8) * 32 + row % 8) * g.R + o * 8;
+    } else {
+      wp[n] = W + ((int64_t)t.e * g.R + min(rc * 64 + n * 16 + c, g.R - 1)) * C;
+    }
+  }
 
   v4f acc[RT][NR];
 #pragma unroll
@@ -146,7 +167,14 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) xv[rt][i] = in ? ld16(xp[rt] + k + i * 8) : u32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int n = 0; n < NR; ++n) wv[n][i] = in ? ld16(wp[n] + k + i * 8) : u32x4{0, 0, 0, 0};
+      for (int n = 0; n < NR; ++n) {
+        if (C_MAJOR) {
+          const int row = (lane + 64 * n) / (2 * NR), col = st * 128 + (row / 8) * 32 + i * 8 + row % 8;
+          wv[n][i] = col < C ? ld16(wp[n] + (int64_t)(st * 128 + i * 8) * g.R) : u32x4{0, 0, 0, 0};
+        } else {
+          wv[n][i] = in ? ld16(wp[n] + k + i * 8) : u32x4{0, 0, 0, 0};
+        }
+      }
     }
   };
   if (st0 < st1) load(st0, xb, wb);
@@ -155,11 +183,26 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
     u32x4 xn[RT][4], wn[NR][4];
     if (st + 1 < st1) load(st + 1, xn, wn);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
+      u32x4 wf[NR];
+      if (C_MAJOR) {
+        uint16_t* tw = turn[wid];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) *reinterpret_cast<u32x4*>(tw + (lane + 64 * n) * 8) = wb[n][i];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+          const uint16_t* p = tw + (q * 8 + c / 4) * (16 * NR) + n * 16 + (c & 3) * 4;
+          wf[n] = transposed8(p, p + 4 * 16 * NR);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NR; ++n) wf[n] = wb[n][i];
+      }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) acc[rt][n] = mfma16<KIND>(wb[n][i], xb[rt][i], acc[rt][n]);
+        for (int n = 0; n < NR; ++n) acc[rt][n] = mfma16<KIND>(wf[n], xb[rt][i], acc[rt][n]);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -360,9 +403,20 @@ __global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(Dev g, Expand
 }
 
 // ------------------------------------------------------------------- outer
-constexpr int kOuterWaves = 8;
+constexpr int kOuterWaves = 4;
 constexpr int kOuterThreads = 64 * kOuterWaves;
-constexpr int kOuterRows = 1024;  // rows a workgroup sums; longer groups are cut and joined
+
+// What outer's waves read of a tile of 32 rows of one group, made once by
+// split_kernel: the low-rank operands of both weight gradients as MFMA
+// fragments, fr[side][tile][part][16 ranks][lane][8 rows], the exponents of
+// their scales (F16), and the rows of the wide operands (-1: none).
+struct Tiles {
+  uint16_t* fr;
+  int* exps;       // [side][tile]
+  int* rows;       // [side][tile][32]
+  int64_t tiles;   // allocated
+  int rank_tiles;
+};
 
 struct Side {
   const float* L;      // [splits][P][R], summed here; times the group's scale
@@ -373,64 +427,148 @@ struct Side {
   uint16_t* out;       // [E][R][C], or col_major: [E][C][R]
   int col_major;
   float* part;         // [slots][R][C] of the cut groups
-  int slabs;           // 128-column slabs
+  int slabs;           // 128 columns each
 };
+
+// Exponent of a 32-row tile's scale, a multiple of 16 so that neighbours
+// rarely differ: brings m to [2^-2, 2^14).
+__device__ __forceinline__ int tile_exp(float m) {
+  return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~15) - 128;
+}
+
+template <int KIND>
+__global__ __launch_bounds__(256) void split_kernel(Dev g, Side sa, Side sb, Tiles tl) {
+  constexpr int NP = kParts<KIND>;
+  __shared__ int sm[kTableInts];
+  __shared__ u32 tmax[2];
+  const int tid = threadIdx.x;
+  sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, 32, 1);
+  const int w = blockIdx.x;
+  if (w >= sm[g.E]) return;
+  const Tile t = sched_tile<1>(sm, g.offsets, g.E, g.P, 32, 1, w);
+  const float sc = scale_of(g, t.e);
+  if (tid < 64) {
+    const int side = tid >> 5, i = tid & 31;
+    const int pair = i < t.rows ? pair_of(g, t.row0 + i) : -1;
+    tl.rows[(side * tl.tiles + w) * 32 + i] = pair < 0 ? -1 : map_row(side ? sb.xm : sa.xm, t.row0 + i, pair);
+  }
+  if (tid < 2) tmax[tid] = 0;
+  __syncthreads();
+  // task: 8 rows (slice q) of one rank of one side
+  const int per = 64 * tl.rank_tiles;
+  const auto low = [&](int i, float (&v)[8]) {
+    const int side = i >= per, k = i - side * per, rank = (k >> 6) * 16 + (k & 15), q = k >> 4 & 3;
+    const Side& d = side ? sb : sa;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = 0.f;
+      const int s = t.row0 + q * 8 + j;
+      if (rank < g.R && q * 8 + j < t.rows && pair_of(g, s) >= 0)
+        for (int sp = 0; sp < d.splits; ++sp) v[j] += d.L[((int64_t)sp * g.P + s) * g.R + rank];
+      v[j] *= sc;
+    }
+  };
+  if (KIND == OUT_F16) {
+    for (int i = tid; i < 2 * per; i += 256) {
+      float v[8], big = 0.f;
+      low(i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = __builtin_fabsf(v[j]);
+        big = u < __builtin_inff() ? fmaxf(big, u) : big;
+      }
+      atomicMax(&tmax[i >= per], __float_as_uint(big));
+    }
+    __syncthreads();
+    if (tid < 2) tl.exps[tid * tl.tiles + w] = tile_exp(__uint_as_float(tmax[tid]));
+  }
+  for (int i = tid; i < 2 * per; i += 256) {
+    const int side = i >= per, k = i - side * per;
+    float v[8];
+    low(i, v);
+    const int f = KIND == OUT_F16 ? tile_exp(__uint_as_float(tmax[side])) : 0;
+    u32x4 pk[NP];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      uint16_t u0[NP], u1[NP];
+      split<KIND>(KIND == OUT_F16 ? ldexp2(v[j], f) : v[j], u0);
+      split<KIND>(KIND == OUT_F16 ? ldexp2(v[j + 1], f) : v[j + 1], u1);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)u0[p] | ((u32)u1[p] << 16);
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) st16(tl.fr + (((side * tl.tiles + w) * NP + p) * per + k) * 8, pk[p]);
+  }
+}
 
 // Slot of the partial sums of the chunk that starts at sorted row s: at most
 // one first and one later chunk of the groups longer than a chunk start in
-// the same kOuterRows rows.
-__host__ __device__ constexpr int outer_slot(int s, bool first) { return 2 * (s / kOuterRows) + (first ? 1 : 0); }
-__host__ __device__ constexpr int64_t outer_slots(int64_t P) { return P > kOuterRows ? 2 * ((P - 1) / kOuterRows + 1) : 0; }
+// the same `chunk` rows.
+__host__ __device__ constexpr int outer_slot(int s, bool first, int chunk) { return 2 * (s / chunk) + (first ? 1 : 0); }
+__host__ __device__ constexpr int64_t outer_slots(int64_t P, int chunk) { return P > chunk ? 2 * ((P - 1) / chunk + 1) : 0; }
 
 // Chunks of a group of m rows; a group without rows has one that writes zeros.
-__device__ __forceinline__ int chunks_of(int m) { return max(1, (m + kOuterRows - 1) / kOuterRows); }
+__device__ __forceinline__ int chunks_of(int m, int chunk) { return max(1, (m + chunk - 1) / chunk); }
 
-// dW[r][n] = sum_s (scale L[s][r]) X[row(s)][n] for one chunk of a group's
-// rows, 128 columns and 16 NR ranks.  The 8 waves deal the rows in steps of
-// 32 (the MFMA's contraction) and meet in LDS.
+// dW[r][n] = sum_s (scale L[s][r]) X[row(s)][n]: each wave by itself takes one
+// chunk of a group's rows, 128 columns and 16 NR ranks, and walks the chunk's
+// tiles of 32 rows (the MFMA's contraction) with the next tile's 8 KB in
+// flight.  Waves of the same columns and other ranks sit side by side, where
+// the second finds the wide operand in the L1.
 template <int KIND, int NR>
-__global__ __launch_bounds__(kOuterThreads) void outer_kernel(Dev g, Side sa, Side sb, int rchunks) {
-  constexpr int NP = kParts<KIND>, CW = 132;
-  __shared__ __align__(16) int sm[kOuterWaves * 16 * CW];
-  static_assert(kOuterWaves * 16 * CW >= kTableInts, "the schedule fits under the sums");
-  __shared__ int rows[kOuterRows];
+__global__ __launch_bounds__(kOuterThreads, 2) void outer_kernel(Dev g, Side sa, Side sb, Tiles tl, int rchunks,
+                                                                 int chunk) {
+  constexpr int NP = kParts<KIND>;
+  __shared__ int tab[1025], tiles[1025], scratch[2 * kOuterWaves];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, c = lane & 15, q = lane >> 4;
-  const int slabs = sa.slabs + sb.slabs;
-  const int rc = blockIdx.x % rchunks;
-  int slab = blockIdx.x / rchunks % slabs, w = blockIdx.x / rchunks / slabs;
-  const Side& d = slab < sa.slabs ? sa : sb;
-  if (slab >= sa.slabs) slab -= sa.slabs;
 
-  // Work item w: chunk `ch` of group e, the groups' chunks in order.
-  int* tab = sm;
+  // Tables of the groups' chunks and 32-row tiles: one scan of both counts.
   {
-    int* scratch = tab + g.E + 1;
     const int per = (g.E + kOuterThreads - 1) / kOuterThreads;
     const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
-    int local = 0, lo, hi;
+    int nc = 0, nt = 0, lo, hi;
     for (int e = e0; e < e1; ++e) {
       expert_range(g.offsets, e, g.P, lo, hi);
-      local += chunks_of(hi - lo);
+      nc += chunks_of(hi - lo, chunk);
+      nt += (hi - lo + 31) / 32;
     }
-    int incl = local;
+    int ic = nc, it = nt;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
+      const int vc = __shfl_up(ic, o, 64), vt = __shfl_up(it, o, 64);
+      if (lane >= o) {
+        ic += vc;
+        it += vt;
+      }
     }
-    if (lane == 63) scratch[wid] = incl;
+    if (lane == 63) {
+      scratch[wid] = ic;
+      scratch[kOuterWaves + wid] = it;
+    }
     __syncthreads();
-    int run = incl - local;
-    for (int v = 0; v < wid; ++v) run += scratch[v];
-    for (int e = e0; e < e1; ++e) {
-      tab[e] = run;
-      expert_range(g.offsets, e, g.P, lo, hi);
-      run += chunks_of(hi - lo);
+    int rc = ic - nc, rt = it - nt;
+    for (int v = 0; v < wid; ++v) {
+      rc += scratch[v];
+      rt += scratch[kOuterWaves + v];
     }
-    if (tid == kOuterThreads - 1) tab[g.E] = run;
+    for (int e = e0; e < e1; ++e) {
+      tab[e] = rc;
+      tiles[e] = rt;
+      expert_range(g.offsets, e, g.P, lo, hi);
+      rc += chunks_of(hi - lo, chunk);
+      rt += (hi - lo + 31) / 32;
+    }
+    if (tid == kOuterThreads - 1) tab[g.E] = rc;
     __syncthreads();
   }
+  const int slabs = sa.slabs + sb.slabs;
+  const int task = blockIdx.x * kOuterWaves + wid;
+  const int rc = task % rchunks, w = task / rchunks / slabs;
+  int slab = task / rchunks % slabs;
   if (w >= tab[g.E]) return;
+  const int side = slab >= sa.slabs;
+  const Side& d = side ? sb : sa;
+  if (side) slab -= sa.slabs;
   int bl = 0, bh = g.E - 1;
   while (bl < bh) {
     const int mid = (bl + bh + 1) >> 1;
@@ -439,130 +577,119 @@ __global__ __launch_bounds__(kOuterThreads) void outer_kernel(Dev g, Side sa, Si
   const int e = bl, ch = w - tab[e];
   int lo, hi;
   expert_range(g.offsets, e, g.P, lo, hi);
-  const int s0 = lo + ch * kOuterRows, m = min(kOuterRows, hi - s0);
-  for (int i = tid; i < (m + 31) / 32 * 32; i += kOuterThreads) {
-    const int pair = i < m ? pair_of(g, s0 + i) : -1;
-    rows[i] = pair < 0 ? -1 : map_row(d.xm, s0 + i, pair);
-  }
-  __syncthreads();
+  const int s0 = lo + ch * chunk, first = tiles[e] + ch * (chunk / 32);
+  // (a malformed offsets table may count more tiles than there can be)
+  const int nt = min((min(chunk, hi - s0) + 31) / 32, (int)max<int64_t>(0, tl.tiles - first));
+  const int64_t t0 = side * tl.tiles + first;
 
-  const float sc = scale_of(g, e);
   const int col = min(slab * 128 + c * 8, d.C - 8);
-  int rank[NR];
+  const uint16_t* X = d.X + col;
+  const int* rowp = tl.rows + t0 * 32 + q * 8;
+  // ranks past R: results that are not stored
+  const uint16_t* fp[NR];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) rank[n] = min(rc * 64 + n * 16 + c, g.R - 1);
+  for (int n = 0; n < NR; ++n)
+    fp[n] = tl.fr + t0 * NP * tl.rank_tiles * 512 + min(rc * NR + n, tl.rank_tiles - 1) * 512 + lane * 8;
+
   v4f acc[NR][8];
 #pragma unroll
   for (int n = 0; n < NR; ++n)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[n][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  int f = 0;  // F16: exponent of the wave's scale of L
-  bool first = true;
-  for (int st = wid * 32; st < m; st += kOuterWaves * 32) {
-    u32x4 raw[8];
-    float l[NR][8];
+  u32x4 raw[8], fr[NR][NP];
+  int row[8];
+  const auto load_rows = [&](int k) {
+    const v4i r0 = *reinterpret_cast<const v4i*>(rowp + k * 32), r1 = *reinterpret_cast<const v4i*>(rowp + k * 32 + 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = st + q * 8 + i, row = rows[k];
-      raw[i] = row >= 0 ? ld16(d.X + (int64_t)row * d.C + col) : u32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int n = 0; n < NR; ++n) {
-        float v = 0.f;
-        if (row >= 0)
-          for (int sp = 0; sp < d.splits; ++sp) v += d.L[((int64_t)sp * g.P + s0 + k) * g.R + rank[n]];
-        l[n][i] = sc * v;
-      }
+    for (int i = 0; i < 4; ++i) {
+      row[i] = r0[i];
+      row[4 + i] = r1[i];
     }
-    if (KIND == OUT_F16) {
-      float big = 0.f;
+  };
+  const auto load_x = [&]() {
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float u = __builtin_fabsf(l[n][i]);
-          big = u < __builtin_inff() ? fmaxf(big, u) : big;
-        }
-      if (first || __any(ldexp2(big, f) > 32768.f)) {
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
-        const int nf = half_exp(big);
-        if (!first) {
-#pragma unroll
-          for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[n][j][i] = ldexp2(acc[n][j][i], nf - f);
-        }
-        f = nf;
-        first = false;
-      }
-    }
-    u32x4 lp[NR][NP];
+    for (int i = 0; i < 8; ++i) raw[i] = row[i] >= 0 ? ld16(X + (int64_t)row[i] * d.C) : u32x4{0, 0, 0, 0};
+  };
+  const auto load_fr = [&](int k) {
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        uint16_t u0[NP], u1[NP];
-        split<KIND>(KIND == OUT_F16 ? ldexp2(l[n][i], f) : l[n][i], u0);
-        split<KIND>(KIND == OUT_F16 ? ldexp2(l[n][i + 1], f) : l[n][i + 1], u1);
+      for (int p = 0; p < NP; ++p) fr[n][p] = ld16(fp[n] + ((int64_t)k * NP + p) * tl.rank_tiles * 512);
+  };
+  int f = 0;
+  if (nt > 0) {
+    load_rows(0);
+    load_x();
+    load_fr(0);
+    if (nt > 1) load_rows(1);
+    f = KIND == OUT_F16 ? tl.exps[t0] : 0;
+  }
+  for (int k = 0; k < nt; ++k) {
+    if (KIND == OUT_F16) {
+      // The sums keep the smallest scale so far; a tile with a larger one is
+      // brought down to it (what that drops is below 2^-22 of the largest).
+      const int ft = tl.exps[t0 + k];
+      if (ft < f) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) lp[n][p][i / 2] = (u32)u0[p] | ((u32)u1[p] << 16);
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][j][i] = ldexp2(acc[n][j][i], ft - f);
+        f = ft;
+      } else if (ft > f) {
+        const _Float16 down = (_Float16)ldexp2(1.f, f - ft);
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) fr[n][p] = __builtin_bit_cast(u32x4, __builtin_bit_cast(v8h, fr[n][p]) * down);
       }
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const u32x4 x = column_of(raw, j);
+    for (int jh = 0; jh < 8; jh += 4) {  // half of the columns at a time: fewer live registers
+      u32x4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = column_of(raw, jh + j);
+      if (jh == 4 && k + 1 < nt) {
+        load_x();
+        if (k + 2 < nt) load_rows(k + 2);
+      }
 #pragma unroll
       for (int n = 0; n < NR; ++n)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) acc[n][j] = mfma16<KIND>(lp[n][p], x, acc[n][j]);
+        for (int p = 0; p < NP; ++p)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[n][jh + j] = mfma16<KIND>(fr[n][p], x[j], acc[n][jh + j]);
     }
+    if (k + 1 < nt) load_fr(k + 1);
   }
 
-  // Join the waves 16 ranks at a time: red[wave][rank][column].
-  const bool cut = hi - lo > kOuterRows;
-  float* red = reinterpret_cast<float*>(sm);
+  // Lane: ranks 4q .. 4q+3 of each tile, columns col .. col+7.
+  if (slab * 128 + c * 8 >= d.C) return;
+  const bool cut = hi - lo > chunk;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
-    __syncthreads();
+    const int r0 = (rc * NR + n) * 16 + 4 * q;
+    if (r0 >= g.R) continue;
+    float v[4][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float* p = red + (wid * 16 + 4 * q + i) * CW + c * 8;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = KIND == OUT_F16 ? ldexp2(acc[n][j][i], -f) : acc[n][j][i];
-    }
-    __syncthreads();
-    // thread: 4 columns of one rank
-    const int r = tid >> 5, x = (tid & 31) * 4;
-    v4f sum = *reinterpret_cast<v4f*>(red + r * CW + x);
+      for (int j = 0; j < 8; ++j) v[i][j] = KIND == OUT_F16 ? ldexp2(acc[n][j][i], -f) : acc[n][j][i];
+    if (cut) {
 #pragma unroll
-    for (int v = 1; v < kOuterWaves; ++v) {
-      const v4f o = *reinterpret_cast<v4f*>(red + (v * 16 + r) * CW + x);
+      for (int i = 0; i < 4; ++i)
+        store8<OUT_F32, false>(d.part, ((int64_t)outer_slot(s0, ch == 0, chunk) * g.R + r0 + i) * d.C + col, v[i]);
+    } else if (d.col_major) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += o[j];
-    }
-    const int rr = rc * 64 + n * 16 + r, cc = slab * 128 + x;
-    if (!cut && d.col_major) {  // transposed through wave 0's part of red
-      __syncthreads();
-      *reinterpret_cast<v4f*>(red + r * CW + x) = sum;
-      __syncthreads();
-      const int n4 = (tid & 3) * 4, y = tid >> 2, rb = rc * 64 + n * 16 + n4, yc = slab * 128 + y;
-      if (rb < g.R && yc < d.C) {
-        u32 o[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          o[j] = (u32)OutT<KIND>::from(red[(n4 + 2 * j) * CW + y]) |
-                 ((u32)OutT<KIND>::from(red[(n4 + 2 * j + 1) * CW + y]) << 16);
-        *reinterpret_cast<uint2*>(d.out + ((int64_t)e * d.C + yc) * g.R + rb) = make_uint2(o[0], o[1]);
+      for (int j = 0; j < 8; ++j) {
+        const u32 o0 = (u32)OutT<KIND>::from(v[0][j]) | ((u32)OutT<KIND>::from(v[1][j]) << 16);
+        const u32 o1 = (u32)OutT<KIND>::from(v[2][j]) | ((u32)OutT<KIND>::from(v[3][j]) << 16);
+        *reinterpret_cast<uint2*>(d.out + ((int64_t)e * d.C + col + j) * g.R + r0) = make_uint2(o0, o1);
       }
-    } else if (rr < g.R && cc < d.C) {
-      if (cut) {
-        *reinterpret_cast<v4f*>(d.part + ((int64_t)outer_slot(s0, ch == 0) * g.R + rr) * d.C + cc) = sum;
-      } else {
-        const u32 o0 = (u32)OutT<KIND>::from(sum[0]) | ((u32)OutT<KIND>::from(sum[1]) << 16);
-        const u32 o1 = (u32)OutT<KIND>::from(sum[2]) | ((u32)OutT<KIND>::from(sum[3]) << 16);
-        *reinterpret_cast<uint2*>(d.out + ((int64_t)e * g.R + rr) * d.C + cc) = make_uint2(o0, o1);
-      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store8<KIND, false>(d.out, ((int64_t)e * g.R + r0 + i) * d.C + col, v[i]);
     }
   }
 }
@@ -570,20 +697,21 @@ __global__ __launch_bounds__(kOuterThreads) void outer_kernel(Dev g, Side sa, Si
 // Joins the chunks of the groups longer than one: a thread takes 4 ranks of
 // one column, so that both output orders store 4 values at once or in runs.
 template <int KIND>
-__global__ __launch_bounds__(256) void join_kernel(Dev g, Side sa, Side sb, int blocks_a, int blocks_b) {
+__global__ __launch_bounds__(256) void join_kernel(Dev g, Side sa, Side sb, int blocks_a, int blocks_b,
+                                                  int chunk) {
   const int per = blocks_a + blocks_b, e = blockIdx.x / per;
   int b = blockIdx.x - e * per;
   const Side& d = b < blocks_a ? sa : sb;
   if (b >= blocks_a) b -= blocks_a;
   int lo, hi;
   expert_range(g.offsets, e, g.P, lo, hi);
-  if (hi - lo <= kOuterRows) return;
+  if (hi - lo <= chunk) return;
   const int64_t i = (int64_t)b * 256 + threadIdx.x;
   const int r = (int)(i / d.C) * 4, n = (int)(i % d.C);
   if (r >= g.R) return;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = lo; s < hi; s += kOuterRows) {
-    const float* p = d.part + ((int64_t)outer_slot(s, s == lo) * g.R + r) * d.C + n;
+  for (int s = lo; s < hi; s += chunk) {
+    const float* p = d.part + ((int64_t)outer_slot(s, s == lo, chunk) * g.R + r) * d.C + n;
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] += p[(int64_t)j * d.C];
   }
@@ -594,29 +722,6 @@ __global__ __launch_bounds__(256) void join_kernel(Dev g, Side sa, Side sb, int 
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) d.out[((int64_t)e * g.R + r + j) * d.C + n] = OutT<KIND>::from(sum[j]);
-  }
-}
-
-// --------------------------------------------------------------- transpose
-// bt[e][r][n] = b[e][n][r] of the groups with rows: 64 rows of b at a time.
-__global__ __launch_bounds__(256) void transpose_kernel(Dev g, const uint16_t* __restrict__ b, int N,
-                                                        uint16_t* __restrict__ bt) {
-  __shared__ uint16_t tile[64][66];
-  const int nblocks = (N + 63) / 64, rblocks = (g.R + 63) / 64;
-  const int e = blockIdx.x / (nblocks * rblocks), i = blockIdx.x - e * nblocks * rblocks;
-  const int n0 = i / rblocks * 64, r0 = i % rblocks * 64;
-  int lo, hi;
-  expert_range(g.offsets, e, g.P, lo, hi);
-  if (lo == hi) return;
-  const int rn = min(64, g.R - r0), nn = min(64, N - n0);
-  for (int k = threadIdx.x; k < nn * rn; k += 256) {
-    const int n = k / rn, r = k - n * rn;
-    tile[r][n] = b[((int64_t)e * N + n0 + n) * g.R + r0 + r];
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < 64 * rn; k += 256) {
-    const int r = k >> 6, n = k & 63;
-    if (n < nn) bt[((int64_t)e * g.R + r0 + r) * N + n0 + n] = tile[r][n];
   }
 }
 
@@ -658,27 +763,27 @@ int shrink_splits(int64_t P, int E, int C, int R) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, (steps + kShrinkWaves - 1) / kShrinkWaves, 8}));
 }
 
-template <int KIND, int RT, int NR>
+template <int KIND, int RT, int NR, bool CM>
 hipError_t shrink_launch(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint16_t* W, float* part, int splits,
                          hipStream_t stream) {
   const int rchunks = (d.R + 63) / 64;
   const int64_t grid = max_tiles(d.P, d.E, 16 * RT) * splits * rchunks;
-  hipLaunchKernelGGL((shrink_kernel<KIND, RT, NR>), dim3((unsigned)grid), dim3(kShrinkThreads), 0, stream, d, X, xm, C,
+  hipLaunchKernelGGL((shrink_kernel<KIND, RT, NR, CM>), dim3((unsigned)grid), dim3(kShrinkThreads), 0, stream, d, X, xm, C,
                      W, part, splits, rchunks);
   return hipGetLastError();
 }
 
-template <int KIND>
+template <int KIND, bool CM>
 hipError_t shrink(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint16_t* W, float* part, int splits,
                   hipStream_t stream) {
   const int nr = rank_tiles(d.R), rt = shrink_rt(d.P, d.E, nr);
-  if (nr == 1 && rt == 4) return shrink_launch<KIND, 4, 1>(d, X, xm, C, W, part, splits, stream);
-  if (nr == 1 && rt == 2) return shrink_launch<KIND, 2, 1>(d, X, xm, C, W, part, splits, stream);
-  if (nr == 1) return shrink_launch<KIND, 1, 1>(d, X, xm, C, W, part, splits, stream);
-  if (nr == 2 && rt == 2) return shrink_launch<KIND, 2, 2>(d, X, xm, C, W, part, splits, stream);
-  if (nr == 2) return shrink_launch<KIND, 1, 2>(d, X, xm, C, W, part, splits, stream);
-  if (rt == 2) return shrink_launch<KIND, 2, 4>(d, X, xm, C, W, part, splits, stream);
-  return shrink_launch<KIND, 1, 4>(d, X, xm, C, W, part, splits, stream);
+  if (nr == 1 && rt == 4) return shrink_launch<KIND, 4, 1, CM>(d, X, xm, C, W, part, splits, stream);
+  if (nr == 1 && rt == 2) return shrink_launch<KIND, 2, 1, CM>(d, X, xm, C, W, part, splits, stream);
+  if (nr == 1) return shrink_launch<KIND, 1, 1, CM>(d, X, xm, C, W, part, splits, stream);
+  if (nr == 2 && rt == 2) return shrink_launch<KIND, 2, 2, CM>(d, X, xm, C, W, part, splits, stream);
+  if (nr == 2) return shrink_launch<KIND, 1, 2, CM>(d, X, xm, C, W, part, splits, stream);
+  if (rt == 2) return shrink_launch<KIND, 2, 4, CM>(d, X, xm, C, W, part, splits, stream);
+  return shrink_launch<KIND, 1, 4, CM>(d, X, xm, C, W, part, splits, stream);
 }
 
 template <int KIND, int RT, bool TR>
@@ -705,12 +810,35 @@ hipError_t expand(const Dev& d, const ExpandArgs& a, bool copy, hipStream_t stre
   }
 }
 
-template <int KIND, int NR>
-hipError_t outer_launch(const Dev& d, const Side& sa, const Side& sb, hipStream_t stream) {
-  const int rchunks = (d.R + 63) / 64;
-  const int64_t grid = (d.P / kOuterRows + d.E) * (int64_t)(sa.slabs + sb.slabs) * rchunks;
-  hipLaunchKernelGGL((outer_kernel<KIND, NR>), dim3((unsigned)grid), dim3(kOuterThreads), 0, stream, d, sa, sb,
-                     rchunks);
+int outer_nr(int R) { return R <= 16 ? 1 : 2; }
+int64_t outer_tasks(int E, int N, int K, int R) {  // waves per chunk of rows
+  const int nr = outer_nr(R);
+  return (int64_t)((N + 127) / 128 + (K + 127) / 128) * ((R + 16 * nr - 1) / (16 * nr));
+}
+
+// Rows a wave sums before a longer group is cut: short enough for eight waves
+// on each of 256 compute units, where the rows allow it.
+int outer_chunk(int64_t P, int E, int N, int K, int R) {
+  for (int chunk = 1024; chunk > 128; chunk /= 2)
+    if (std::max<int64_t>(P / chunk, std::min<int64_t>(P, E)) * outer_tasks(E, N, K, R) >= 2048) return chunk;
+  return 128;
+}
+
+template <int KIND>
+hipError_t outer(const Dev& d, const Side& sa, const Side& sb, const Tiles& tl, int N, int K, hipStream_t stream) {
+  const int chunk = outer_chunk(d.P, d.E, N, K, d.R), nr = outer_nr(d.R);
+  const int64_t tasks = (d.P / chunk + d.E) * outer_tasks(d.E, N, K, d.R);
+  const dim3 grid((unsigned)((tasks + kOuterWaves - 1) / kOuterWaves));
+  const int rchunks = (d.R + 16 * nr - 1) / (16 * nr);
+  if (nr == 1)
+    hipLaunchKernelGGL((outer_kernel<KIND, 1>), grid, dim3(kOuterThreads), 0, stream, d, sa, sb, tl, rchunks, chunk);
+  else
+    hipLaunchKernelGGL((outer_kernel<KIND, 2>), grid, dim3(kOuterThreads), 0, stream, d, sa, sb, tl, rchunks, chunk);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || d.P <= chunk) return e;
+  const int ba = (int)(((int64_t)K * (d.R / 4) + 255) / 256), bb = (int)(((int64_t)N * (d.R / 4) + 255) / 256);
+  hipLaunchKernelGGL(join_kernel<KIND>, dim3((unsigned)(d.E * (ba + bb))), dim3(256), 0, stream, d, sa, sb, ba, bb,
+                     chunk);
   return hipGetLastError();
 }
 
@@ -720,24 +848,31 @@ hipError_t forward(const LoraArgs& g, const uint16_t* x, const uint16_t* a, cons
   const Dev d = dev_args(g);
   const int splits = shrink_splits(g.P, g.E, g.K, g.R);
   float* part = splits == 1 && h ? h : ws;
-  hipError_t e = shrink<KIND>(d, x, x_map(g), g.K, a, part, splits, stream);
+  hipError_t e = shrink<KIND, false>(d, x, x_map(g), g.K, a, part, splits, stream);
   if (e != hipSuccess) return e;
   ExpandArgs ea = {part, splits, part == h ? nullptr : h, b, g.N, base, out, g.out_pair, 0, 0, 0, g.p2s};
   return expand<KIND, false>(d, ea, g.out_pair && base != out, stream);
 }
 
-// Workspace of the gradients: dh's partial sums, B transposed, and the cut
-// groups' partial weight gradients, each at a multiple of 256 bytes.
+// Workspace of the gradients: dh's partial sums, the tiles of both low-rank
+// operands (exponents, rows, fragments), and the cut groups' partial weight
+// gradients, each at a multiple of 256 bytes.
 struct BwdLayout {
-  size_t bt, pa, pb, bytes;
+  int64_t tiles;
+  size_t exps, rows, fr, pa, pb, bytes;
 };
 BwdLayout bwd_layout(int64_t P, int E, int N, int K, int R) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-  BwdLayout l;
-  l.bt = up((size_t)P * R * sizeof(float) * (P ? shrink_splits(P, E, N, R) : 0));
-  l.pa = l.bt + (P ? up((size_t)E * N * R * 2) : 0);
-  l.pb = l.pa + up((size_t)outer_slots(P) * R * K * sizeof(float));
-  l.bytes = l.pb + up((size_t)outer_slots(P) * R * N * sizeof(float));
+  BwdLayout l = {};
+  if (P == 0) return l;
+  l.tiles = max_tiles(P, E, 32);
+  l.exps = up((size_t)P * R * sizeof(float) * shrink_splits(P, E, N, R));
+  l.rows = l.exps + up((size_t)l.tiles * 2 * sizeof(int));
+  l.fr = l.rows + up((size_t)l.tiles * 2 * 32 * sizeof(int));
+  l.pa = l.fr + up((size_t)l.tiles * 2 * kParts<OUT_BF16> * ((R + 15) / 16) * 1024);
+  const size_t slots = outer_slots(P, outer_chunk(P, E, N, K, R));
+  l.pb = l.pa + up(slots * R * K * sizeof(float));
+  l.bytes = l.pb + up(slots * R * N * sizeof(float));
   return l;
 }
 
@@ -745,34 +880,24 @@ template <int KIND>
 hipError_t backward(const LoraArgs& g, const uint16_t* dy, const uint16_t* x, const uint16_t* a, const uint16_t* b,
                     const float* h, uint16_t* dx, uint16_t* da, uint16_t* db, char* ws, hipStream_t stream) {
   const Dev d = dev_args(g);
-  Dev d1 = d;  // without the scale
-  d1.scale = nullptr;
   const BwdLayout l = bwd_layout(g.P, g.E, g.N, g.K, g.R);
   float* dh = reinterpret_cast<float*>(ws);
-  const int splits = g.P ? shrink_splits(g.P, g.E, g.N, g.R) : 1;
-  hipError_t e;
+  const int splits = shrink_splits(g.P, g.E, g.N, g.R);
+  const Side sa = {dh, splits, x, x_map(g), g.K, da, 0, reinterpret_cast<float*>(ws + l.pa), (g.K + 127) / 128};
+  const Side sb = {h, 1, dy, o_map(g), g.N, db, 1, reinterpret_cast<float*>(ws + l.pb), (g.N + 127) / 128};
+  const Tiles tl = {reinterpret_cast<uint16_t*>(ws + l.fr), reinterpret_cast<int*>(ws + l.exps),
+                    reinterpret_cast<int*>(ws + l.rows), l.tiles, (g.R + 15) / 16};
   if (g.P > 0) {
-    uint16_t* bt = reinterpret_cast<uint16_t*>(ws + l.bt);
-    hipLaunchKernelGGL(transpose_kernel, dim3(g.E * ((g.N + 63) / 64) * ((g.R + 63) / 64)), dim3(256), 0, stream, d, b,
-                       g.N, bt);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = shrink<KIND>(d1, dy, o_map(g), g.N, bt, dh, splits, stream)) != hipSuccess) return e;
+    hipError_t e = shrink<KIND, true>(d, dy, o_map(g), g.N, b, dh, splits, stream);
+    if (e != hipSuccess) return e;
     if (dx) {
       ExpandArgs ea = {dh, splits, nullptr, a, g.K, nullptr, dx, 0, 0, 0, 0, nullptr};
       if ((e = expand<KIND, true>(d, ea, false, stream)) != hipSuccess) return e;
     }
+    hipLaunchKernelGGL(split_kernel<KIND>, dim3((unsigned)l.tiles), dim3(256), 0, stream, d, sa, sb, tl);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const Side sa = {dh, splits, x, x_map(g), g.K, da, 0, reinterpret_cast<float*>(ws + l.pa), (g.K + 127) / 128};
-  const Side sb = {h, 1, dy, o_map(g), g.N, db, 1, reinterpret_cast<float*>(ws + l.pb), (g.N + 127) / 128};
-  switch (rank_tiles(g.R)) {
-    case 1: e = outer_launch<KIND, 1>(d, sa, sb, stream); break;
-    case 2: e = outer_launch<KIND, 2>(d, sa, sb, stream); break;
-    default: e = outer_launch<KIND, 4>(d, sa, sb, stream); break;
-  }
-  if (e != hipSuccess || g.P <= kOuterRows) return e;
-  const int ba = (int)(((int64_t)g.K * (g.R / 4) + 255) / 256), bb = (int)(((int64_t)g.N * (g.R / 4) + 255) / 256);
-  hipLaunchKernelGGL(join_kernel<KIND>, dim3((unsigned)(g.E * (ba + bb))), dim3(256), 0, stream, d, sa, sb, ba, bb);
-  return hipGetLastError();
+  return outer<KIND>(d, sa, sb, tl, g.N, g.K, stream);
 }
 
 }  // namespace
@@ -788,8 +913,8 @@ bool lora_fits(int64_t P, int E, int N, int K, int R) {
     const int blocks = (C + 511) / 512, iters = expand_iters(tiles, blocks);
     if (tiles * ((blocks + iters - 1) / iters) > kMaxBlocks) return false;
   }
-  const int64_t slabs = (N + 127) / 128 + (K + 127) / 128;
-  return (P / kOuterRows + E) * slabs * rchunks * kOuterThreads <= kThreadsMax &&
+  return max_tiles(P, E, 32) * 256 <= kThreadsMax &&
+         (P / outer_chunk(P, E, N, K, R) + E) * outer_tasks(E, N, K, R) * 64 <= kThreadsMax &&
          E * (((int64_t)N + K) * (R / 4) / 256 + 2) * 256 <= kThreadsMax;
 }
 
