@@ -115,12 +115,18 @@ def _ptr(t):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    # the raw handle of torch.cuda.current_stream(), without building the
+    # Stream object, which took 2.8 of a call's 10 us
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _need(t, name, dtype=None, ndim=None):
     """Type, dtype, rank and contiguity of one tensor argument (where it
-    lives is checked by _gpu, after every shape check)."""
+    lives is checked by _gpu or _here, after every shape check)."""
+    if type(t) is torch.Tensor and t.is_contiguous() and (ndim is None or t.dim() == ndim):  # the usual case, quickly
+        dt = t.dtype
+        if dtype is None or dt is dtype or (type(dtype) is tuple and dt in dtype):
+            return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
@@ -138,14 +144,18 @@ def _gpu(**tensors):
             raise ValueError(f"{name} must be on the GPU")
 
 
-def _here(**tensors):
+def _here(names, *tensors):
     """Every tensor argument (None: absent) must be in the current GPU's
-    memory: the kernels run on the current device's current stream."""
-    _gpu(**tensors)
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the current device is cuda:{cur}")
+    memory: the kernels run on the current device's current stream.  Returns
+    that stream; `names` (space-separated) is for the error."""
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != cur:
+            name = names.split()[i]
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be on the GPU")
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+    return torch._C._cuda_getCurrentRawStream(cur) if torch.cuda.is_initialized() else None
 
 
 def route_workspace_bytes(T: int, topk: int, E: int) -> int:
@@ -458,21 +468,26 @@ def nvfp4_repack(w, sf_swizzled, *, swap_halves: bool, sf_layout="rows", w_layou
     return w_out, sf_out
 
 
+_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
+
+
 def _pairs(pair_to_sorted, topk):
     """Tokens of a pair table."""
     _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
-    if topk < 1 or pair_to_sorted.numel() % topk:
+    P = pair_to_sorted.numel()
+    if topk < 1 or P % topk:
         raise ValueError("pair_to_sorted must have T*topk entries")
-    return pair_to_sorted.numel() // topk
+    return P // topk
 
 
-def _fit(t, name, shape, dtype, device):
-    """The given output tensor, checked, or a new one."""
+def _fit(t, name, shape, dtype, like):
+    """The given tensor, checked, or a new one on the device of `like`."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, len(shape))
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t
 
 
@@ -482,12 +497,13 @@ def moe_permute(x, pair_to_sorted, topk: int, *, out=None):
     [T*topk][N]; rows past expert_offsets[E] are not written."""
     _need(x, "x", (torch.float16, torch.bfloat16, torch.float32, torch.uint8), 2)
     T = _pairs(pair_to_sorted, topk)
-    N = x.shape[1]
-    if x.shape[0] != T:
+    rows, N = x.shape
+    if rows != T:
         raise ValueError(f"x must have {T} rows, one per token of pair_to_sorted")
-    out = _fit(out, "out", (T * topk, N), x.dtype, x.device)
-    _here(x=x, pair_to_sorted=pair_to_sorted, out=out)
-    st = lib().moe_permute(_ptr(x), _DTYPE_CODE[x.dtype], _ptr(pair_to_sorted), T, topk, N, _ptr(out), _stream())
+    out = _fit(out, "out", (T * topk, N), x.dtype, x)
+    stream = _here("x pair_to_sorted out", x, pair_to_sorted, out)
+    st = lib().moe_permute(x.data_ptr(), _DTYPE_CODE[x.dtype], pair_to_sorted.data_ptr(), T, topk, N, out.data_ptr(),
+                           stream)
     _check("moe_permute", st)
     return out
 
@@ -496,18 +512,18 @@ def moe_permute_backward(dxs, pair_to_sorted, topk: int, *, out_dtype=None, out=
     """Gradient of moe_permute: dx[t] = sum over the routed slots of token t
     of dxs[pair_to_sorted[t*topk+j]], fp32 in slot order, one rounding.
     dxs [T*topk][N] in sorted order; returns dx [T][N]."""
-    _need(dxs, "dxs", (torch.float16, torch.bfloat16, torch.float32), 2)
+    _need(dxs, "dxs", _FLOATS, 2)
     T = _pairs(pair_to_sorted, topk)
-    N = dxs.shape[1]
-    if dxs.shape[0] < T * topk:
+    rows, N = dxs.shape
+    if rows < T * topk:
         raise ValueError("dxs must have at least T*topk rows (sorted positions index into it)")
     out_dtype = out_dtype or dxs.dtype
-    if out_dtype not in (torch.float16, torch.bfloat16, torch.float32):
+    if out_dtype not in _FLOATS:
         raise TypeError(f"out_dtype {out_dtype} is not a floating type of the library")
-    out = _fit(out, "out", (T, N), out_dtype, dxs.device)
-    _here(dxs=dxs, pair_to_sorted=pair_to_sorted, out=out)
-    st = lib().moe_permute_backward(_ptr(dxs), _DTYPE_CODE[dxs.dtype], _ptr(pair_to_sorted), T, topk, N,
-                                    _DTYPE_CODE[out_dtype], _ptr(out), _stream())
+    out = _fit(out, "out", (T, N), out_dtype, dxs)
+    stream = _here("dxs pair_to_sorted out", dxs, pair_to_sorted, out)
+    st = lib().moe_permute_backward(dxs.data_ptr(), _DTYPE_CODE[dxs.dtype], pair_to_sorted.data_ptr(), T, topk, N,
+                                    _DTYPE_CODE[out_dtype], out.data_ptr(), stream)
     _check("moe_permute_backward", st)
     return out
 
@@ -517,23 +533,22 @@ def moe_scatter_combine_backward(dout, y, pair_to_sorted, topk_weights, *, dy=No
     (y's type) and dw[t, j] = <dout[t], y[s]> (f32; 0 for slots without an
     expert), s = pair_to_sorted[t*topk+j].  Returns (dy, dw); rows of dy past
     expert_offsets[E] are not written."""
-    floats = (torch.float16, torch.bfloat16, torch.float32)
-    _need(dout, "dout", floats, 2)
-    _need(y, "y", floats, 2)
+    _need(dout, "dout", _FLOATS, 2)
+    _need(y, "y", _FLOATS, 2)
     _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
     _need(topk_weights, "topk_weights", torch.float32, 2)
     T, k = topk_weights.shape
-    N = y.shape[1]
-    if tuple(dout.shape) != (T, N):
+    rows, N = y.shape
+    if dout.shape != (T, N):
         raise ValueError(f"dout must be [{T}][{N}], got {tuple(dout.shape)}")
-    if pair_to_sorted.numel() != T * k or y.shape[0] != T * k:
+    if pair_to_sorted.numel() != T * k or rows != T * k:
         raise ValueError("pair_to_sorted needs T*topk entries and y T*topk rows")
-    dy = _fit(dy, "dy", (T * k, N), y.dtype, y.device)
-    dw = _fit(dw, "dw", (T, k), torch.float32, y.device)
-    _here(dout=dout, y=y, pair_to_sorted=pair_to_sorted, topk_weights=topk_weights, dy=dy, dw=dw)
-    st = lib().moe_scatter_combine_backward(_ptr(dout), _DTYPE_CODE[dout.dtype], _ptr(y), _DTYPE_CODE[y.dtype],
-                                            _ptr(pair_to_sorted), _ptr(topk_weights), T, k, N, _ptr(dy), _ptr(dw),
-                                            _stream())
+    dy = _fit(dy, "dy", (T * k, N), y.dtype, y)
+    dw = _fit(dw, "dw", (T, k), torch.float32, y)
+    stream = _here("dout y pair_to_sorted topk_weights dy dw", dout, y, pair_to_sorted, topk_weights, dy, dw)
+    st = lib().moe_scatter_combine_backward(dout.data_ptr(), _DTYPE_CODE[dout.dtype], y.data_ptr(),
+                                            _DTYPE_CODE[y.dtype], pair_to_sorted.data_ptr(), topk_weights.data_ptr(),
+                                            T, k, N, dy.data_ptr(), dw.data_ptr(), stream)
     _check("moe_scatter_combine_backward", st)
     return dy, dw
 
@@ -543,30 +558,34 @@ def lora_workspace_bytes(P: int, E: int, N: int, K: int, R: int, *, backward=Fal
     return int(f(P, E, N, K, R))
 
 
-def _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids, a_row, rows):
+def _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids):
     _need(x, "x", (torch.float16, torch.bfloat16), 2)
-    _need(a, "a", x.dtype, 3)
-    _need(b, "b", x.dtype, 3)
+    dt = x.dtype
+    _need(a, "a", dt, 3)
+    _need(b, "b", dt, 3)
     _need(expert_offsets, "expert_offsets", torch.int32, 1)
-    if sorted_pair_ids is not None:
-        _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, 1)
     E, R, K = a.shape
-    N = b.shape[1]
-    if tuple(b.shape) != (E, N, R) or x.shape[1] != K or expert_offsets.numel() != E + 1:
+    rows, xk = x.shape
+    if b.shape[0] != E or b.shape[2] != R or xk != K or expert_offsets.numel() != E + 1:
         raise ValueError("inconsistent adapter shapes: x [rows][K], a [E][R][K], b [E][N][R], expert_offsets [E+1]")
     if scale is not None:
         _need(scale, "scale", torch.float32, 1)
         if scale.numel() != E:
             raise ValueError(f"scale must have {E} values")
-    P = sorted_pair_ids.numel() if sorted_pair_ids is not None else rows
-    return E, R, K, N, P
+    if sorted_pair_ids is not None:
+        _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, 1)
+        P = sorted_pair_ids.numel()
+    else:
+        P = rows
+    return E, R, K, b.shape[1], P, rows
 
 
-def _lora_ws(workspace, need, device):
+def _lora_ws(workspace, sizes, backward, like):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        need = lora_workspace_bytes(*sizes, backward=backward)
+        return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
     _need(workspace, "workspace")
-    return workspace
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def grouped_lora(x, a, b, expert_offsets, sorted_pair_ids, topk: int, *, base=None, scale=None, a_row="token",
@@ -585,24 +604,23 @@ def grouped_lora(x, a, b, expert_offsets, sorted_pair_ids, topk: int, *, base=No
     rows past expert_offsets[E] are not written.  h (f32 [P][R]) receives
     x[row] a[e]^T for grouped_lora_backward.  workspace: uint8,
     lora_workspace_bytes(P, E, N, K, R).  Returns out [P][N]."""
-    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
-    E, R, K, N, P = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids, a_row, rows)
+    E, R, K, N, P, rows = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids)
+    dt = x.dtype
     if base is not None:
-        base = _fit(base, "base", (P, N), x.dtype, x.device)
+        base = _fit(base, "base", (P, N), dt, x)
     if pair_to_sorted is not None:
         _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
         if pair_to_sorted.numel() != P:
             raise ValueError(f"pair_to_sorted must have {P} entries")
-    out = _fit(out, "out", (P, N), x.dtype, x.device)
+    out = _fit(out, "out", (P, N), dt, x)
     if h is not None:
-        h = _fit(h, "h", (P, R), torch.float32, x.device)
-    workspace = _lora_ws(workspace, lora_workspace_bytes(P, E, N, K, R), x.device)
-    _here(x=x, a=a, b=b, scale=scale, expert_offsets=expert_offsets, sorted_pair_ids=sorted_pair_ids,
-          pair_to_sorted=pair_to_sorted, base=base, out=out, h=h, workspace=workspace)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().grouped_lora(_ptr(x), _DTYPE_CODE[x.dtype], x.shape[0], AROW[a_row], _ptr(a), _ptr(b), _ptr(scale),
-                            _ptr(expert_offsets), _ptr(sorted_pair_ids), _ptr(pair_to_sorted), P, topk, E, N, K, R,
-                            _ptr(base), OROW[out_row], _ptr(out), _ptr(h), _ptr(workspace), wsb, _stream())
+        h = _fit(h, "h", (P, R), torch.float32, x)
+    workspace, wsb = _lora_ws(workspace, (P, E, N, K, R), False, x)
+    stream = _here("x a b scale expert_offsets sorted_pair_ids pair_to_sorted base out h workspace", x, a, b, scale,
+                   expert_offsets, sorted_pair_ids, pair_to_sorted, base, out, h, workspace)
+    st = lib().grouped_lora(x.data_ptr(), _DTYPE_CODE[dt], rows, AROW[a_row], a.data_ptr(), b.data_ptr(), _ptr(scale),
+                            expert_offsets.data_ptr(), _ptr(sorted_pair_ids), _ptr(pair_to_sorted), P, topk, E, N, K, R,
+                            _ptr(base), OROW[out_row], out.data_ptr(), _ptr(h), _ptr(workspace), wsb, stream)
     _check("grouped_lora", st)
     return out
 
@@ -616,23 +634,24 @@ def grouped_lora_backward(dy, x, a, b, h, expert_offsets, sorted_pair_ids, topk:
     past expert_offsets[E] are not.  With a_row 'token', moe_permute_backward
     sums dx over each token's slots.  workspace: uint8,
     lora_workspace_bytes(P, E, N, K, R, backward=True)."""
-    rows = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else 0
-    E, R, K, N, P = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids, a_row, rows)
-    dy = _fit(dy, "dy", (P, N), x.dtype, x.device) if dy is not None else _need(dy, "dy")
-    h = _fit(h, "h", (P, R), torch.float32, x.device) if h is not None else _need(h, "h")
+    E, R, K, N, P, rows = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids)
+    dt = x.dtype
+    if dy is None or h is None:
+        raise TypeError("dy and h must be torch.Tensor")
+    _fit(dy, "dy", (P, N), dt, x)
+    _fit(h, "h", (P, R), torch.float32, x)
     if need_dx:
-        dx = _fit(dx, "dx", (P, K), x.dtype, x.device)
+        dx = _fit(dx, "dx", (P, K), dt, x)
     elif dx is not None:
         raise ValueError("dx is given, but need_dx is false")
-    da = _fit(da, "da", (E, R, K), x.dtype, x.device)
-    db = _fit(db, "db", (E, N, R), x.dtype, x.device)
-    workspace = _lora_ws(workspace, lora_workspace_bytes(P, E, N, K, R, backward=True), x.device)
-    _here(dy=dy, x=x, a=a, b=b, h=h, scale=scale, expert_offsets=expert_offsets, sorted_pair_ids=sorted_pair_ids,
-          dx=dx, da=da, db=db, workspace=workspace)
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().grouped_lora_backward(_ptr(dy), _DTYPE_CODE[x.dtype], OROW[out_row], _ptr(x), x.shape[0], AROW[a_row],
-                                     _ptr(a), _ptr(b), _ptr(scale), _ptr(h), _ptr(expert_offsets),
-                                     _ptr(sorted_pair_ids), P, topk, E, N, K, R, _ptr(dx), _ptr(da), _ptr(db),
-                                     _ptr(workspace), wsb, _stream())
+    da = _fit(da, "da", (E, R, K), dt, x)
+    db = _fit(db, "db", (E, N, R), dt, x)
+    workspace, wsb = _lora_ws(workspace, (P, E, N, K, R), True, x)
+    stream = _here("dy x a b h scale expert_offsets sorted_pair_ids dx da db workspace", dy, x, a, b, h, scale,
+                   expert_offsets, sorted_pair_ids, dx, da, db, workspace)
+    st = lib().grouped_lora_backward(dy.data_ptr(), _DTYPE_CODE[dt], OROW[out_row], x.data_ptr(), rows, AROW[a_row],
+                                     a.data_ptr(), b.data_ptr(), _ptr(scale), h.data_ptr(), expert_offsets.data_ptr(),
+                                     _ptr(sorted_pair_ids), P, topk, E, N, K, R, _ptr(dx), da.data_ptr(),
+                                     db.data_ptr(), _ptr(workspace), wsb, stream)
     _check("grouped_lora_backward", st)
     return dx, da, db

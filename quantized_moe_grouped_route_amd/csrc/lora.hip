@@ -11,12 +11,13 @@
 // pass over the wide operand (x, base and out, dy, dx), so each reads it once,
 // in 16-byte pieces straight into MFMA registers.  All use the 16x16x32 MFMA,
 // whose contraction order is free as long as both operands share it; that
-// freedom is used twice:
-//   * shrink: lane slice q takes k = 32 q .. 32 q + 31 of a 128-wide step, so
-//     a wave reads 256 contiguous bytes of each row;
-//   * expand, outer: MFMA j's column c stands for column 8 c + j of a 128-wide
-//     block, so a lane's eight results (or operands) are 8 consecutive columns,
-//     one 16-byte access, 256 contiguous bytes per row and wave.
+// freedom is used in expand and outer: MFMA j's column c stands for column
+// 8 c + j of a 128-wide block, so a lane's eight results (or operands) are 8
+// consecutive columns, one 16-byte access, 256 contiguous bytes per row and
+// wave.  shrink keeps the plain order, 64 contiguous bytes of each of 16 rows
+// in an access: with a lane's 64 bytes in a row (and so 16-byte pieces 64
+// bytes apart in an access) the L1 saw 45 lookups per access and not 16, and
+// dh of 256 experts took 167 us, not 100.
 //
 // The low-rank operand (h, dh) is fp32.  It enters the MFMAs as a sum of
 // 16-bit parts that carries all its 24 bits: three of bf16 (8 bits each), or
@@ -28,6 +29,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "pipeline.h"
 #include "vec8.h"
 
 namespace moeq {
@@ -60,6 +62,16 @@ __device__ __forceinline__ float scale_of(const Dev& g, int e) { return g.scale 
 constexpr int kTableInts = 1025 + 2 * kMaxWaves;
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
 
+// A tile that every lane has alike, in scalar registers.
+__device__ __forceinline__ Tile uniform(const Tile& t) {
+  Tile u;
+  u.e = __builtin_amdgcn_readfirstlane(t.e);
+  u.row0 = __builtin_amdgcn_readfirstlane(t.row0);
+  u.rows = __builtin_amdgcn_readfirstlane(t.rows);
+  u.nt = 0;
+  return u;
+}
+
 template <int KIND>
 __device__ __forceinline__ v4f mfma16(u32x4 a, u32x4 b, v4f c) {
   if (KIND == OUT_BF16)
@@ -83,9 +95,9 @@ __device__ __forceinline__ void split(float v, uint16_t p[kParts<KIND>]) {
   }
 }
 
-// 8 rows of 8 elements to 8 columns of 8, in registers: column j's word t
-// holds rows 2t and 2t + 1.
-__device__ __forceinline__ u32x4 column_of(const u32x4 rows[8], int j) {
+// Column j of 8 rows of elements held in registers: word t has rows 2t, 2t + 1.
+template <class V>
+__device__ __forceinline__ u32x4 column_of(const V (&rows)[8], int j) {
   const u32 sel = j & 1 ? 0x07060302u : 0x05040100u;
   u32x4 v;
 #pragma unroll
@@ -93,12 +105,18 @@ __device__ __forceinline__ u32x4 column_of(const u32x4 rows[8], int j) {
   return v;
 }
 
+typedef u32 u32x2 __attribute__((ext_vector_type(2)));
+template <int KIND>
+__device__ __forceinline__ void store4(uint16_t* p, float a, float b, float c, float d) {
+  *reinterpret_cast<u32x2*>(p) = u32x2{(u32)OutT<KIND>::from(a) | ((u32)OutT<KIND>::from(b) << 16),
+                                       (u32)OutT<KIND>::from(c) | ((u32)OutT<KIND>::from(d) << 16)};
+}
+
 // Two transposing LDS reads: lane i of each 16 gets column i of the 4 x 16
 // block whose row j/4, columns 4 (j % 4) .. +3 its lane j points at.
 __device__ __forceinline__ u32x4 transposed8(const uint16_t* a, const uint16_t* b) {
   typedef short v4s __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) v4s lds4;
-  typedef u32 u32x2 __attribute__((ext_vector_type(2)));
   const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)a));
   const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)b));
   return u32x4{x[0], x[1], y[0], y[1]};
@@ -127,11 +145,12 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
   constexpr int BM = 16 * RT, RW = 16 * NR + 4;
   __shared__ __align__(16) int sm[cmax(kTableInts, kShrinkWaves * BM * RW)];
   __shared__ __align__(16) uint16_t turn[C_MAJOR ? kShrinkWaves : 1][32 * 16 * NR];
-  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, c = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rc = blockIdx.x % rchunks, sp = blockIdx.x / rchunks % splits, w = blockIdx.x / rchunks / splits;
   sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, BM, 1);
   if (w >= sm[g.E]) return;
-  const Tile t = sched_tile<1>(sm, g.offsets, g.E, g.P, BM, 1, w);
+  const Tile t = uniform(sched_tile<1>(sm, g.offsets, g.E, g.P, BM, 1, w));
 
   const uint16_t* xp[RT];
 #pragma unroll
@@ -143,8 +162,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     if (C_MAJOR) {  // piece p of 32 columns: row p / 2NR, 8 ranks
-      const int p = lane + 64 * n, row = p / (2 * NR), o = min(rc * 8 + p % (2 * NR), g.R / 8 - 1);
-      wp[n] = W + ((int64_t)t.e * C + (row / 8) * 32 + row % 8) * g.R + o * 8;
+      wp[n] = W + (int64_t)t.e * C * g.R + min(rc * 8 + (lane + 64 * n) % (2 * NR), g.R / 8 - 1) * 8;
     } else {
       wp[n] = W + ((int64_t)t.e * g.R + min(rc * 64 + n * 16 + c, g.R - 1)) * C;
     }
@@ -159,20 +177,22 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
   const int steps = (C + 127) / 128, slot = sp * kShrinkWaves + wid, slots = splits * kShrinkWaves;
   const int st0 = (int)((int64_t)steps * slot / slots), st1 = (int)((int64_t)steps * (slot + 1) / slots);
   u32x4 xb[RT][4], wb[NR][4];
+  // Columns past C repeat the last 8 of each operand, W's as zeros.
   auto load = [&](int st, u32x4 (&xv)[RT][4], u32x4 (&wv)[NR][4]) {
-    const int k = st * 128 + q * 32;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = st * 128 + 128 <= C || k + i * 8 < C;
+      const int k = st * 128 + i * 32 + q * 8, kc = min(k, C - 8);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) xv[rt][i] = in ? ld16(xp[rt] + k + i * 8) : u32x4{0, 0, 0, 0};
+      for (int rt = 0; rt < RT; ++rt) xv[rt][i] = ld16(xp[rt] + kc);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         if (C_MAJOR) {
-          const int row = (lane + 64 * n) / (2 * NR), col = st * 128 + (row / 8) * 32 + i * 8 + row % 8;
-          wv[n][i] = col < C ? ld16(wp[n] + (int64_t)(st * 128 + i * 8) * g.R) : u32x4{0, 0, 0, 0};
+          const int col = st * 128 + i * 32 + (lane + 64 * n) / (2 * NR);
+          wv[n][i] = ld16(wp[n] + (int64_t)min(col, C - 1) * g.R);
+          if (col >= C) wv[n][i] = u32x4{0, 0, 0, 0};
         } else {
-          wv[n][i] = in ? ld16(wp[n] + k + i * 8) : u32x4{0, 0, 0, 0};
+          wv[n][i] = ld16(wp[n] + kc);
+          if (k >= C) wv[n][i] = u32x4{0, 0, 0, 0};
         }
       }
     }
@@ -238,6 +258,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
 // ------------------------------------------------------------------ expand
 constexpr int kExpandThreads = 256;
 constexpr int kExpandWaves = kExpandThreads / 64;
+constexpr int kExpandRows = 64;
 
 struct ExpandArgs {
   const float* part;     // [splits][P][R], summed here
@@ -248,6 +269,7 @@ struct ExpandArgs {
   const uint16_t* base;  // or null
   uint16_t* out;
   int out_pair;          // row of out: the pair (else s)
+  int bm;                // rows a workgroup takes, a multiple of 16 up to kExpandRows
   int iters;             // 512-column blocks a workgroup walks
   int cblocks;           // workgroups across the columns
   int main_blocks;       // workgroups of the rows with a group; the others copy
@@ -256,16 +278,19 @@ struct ExpandArgs {
 
 __host__ __device__ constexpr int padded_rank(int R) { return (R + 31) / 32 * 32 + 8; }
 
-// out[o(s)][n] = base + sum_r (scale h[s][r]) W[e][n][r] for 16 RT rows of one
-// group.  The rows' low-rank operand is split once into LDS; each wave then
-// walks blocks of 128 columns.  Ranks are taken 32 at a time (zero past R).
-template <int KIND, int RT, bool TR>
-__global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(Dev g, ExpandArgs a) {
-  constexpr int BM = 16 * RT, NP = kParts<KIND>;
-  extern __shared__ int sm[];
-  __shared__ int orow[BM];
-  __shared__ u32 rmax[BM];
-  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, c = lane & 15, q = lane >> 4;
+// out[o(s)][n] = base + sum_r (scale h[s][r]) W[e][n][r] for bm rows of one
+// group.  The rows' low-rank operand is split once into LDS (zero past R).
+// Each wave then takes 128 columns at a time, keeps their weights of OC x 32
+// ranks in registers and walks the rows 16 at a time, the next rows' base in
+// flight; OC = 0 takes any rank, reloading the weights for every 32 rows.
+template <int KIND, int OC, bool TR>
+__global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev g, ExpandArgs a) {
+  constexpr int NP = kParts<KIND>, RTI = OC ? 1 : 2;
+  extern __shared__ __align__(16) int sm[];
+  __shared__ int orow[kExpandRows];
+  __shared__ u32 rmax[kExpandRows];
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);  // what a wave shares stays in scalar registers
   if ((int)blockIdx.x >= a.main_blocks) {
     const int nw = (gridDim.x - a.main_blocks) * kExpandWaves;
     for (int p = (blockIdx.x - a.main_blocks) * kExpandWaves + wid; p < g.P; p += nw) {
@@ -277,16 +302,44 @@ __global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(Dev g, Expand
     return;
   }
   const int w = blockIdx.x / a.cblocks, cb = blockIdx.x - w * a.cblocks;
-  sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, BM, 1);
+  sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, a.bm, 1);
   if (w >= sm[g.E]) return;
-  const Tile t = sched_tile<1>(sm, g.offsets, g.E, g.P, BM, 1, w);
+  const Tile t = uniform(sched_tile<1>(sm, g.offsets, g.E, g.P, a.bm, 1, w));
+
+  const bool has_base = !TR && a.base;  // dx has none
+  const int octs = g.R / 8, RP = padded_rank(g.R), ochunks = (octs + 3) / 4;
+  // Weights of columns n0 + 8c + j, ranks 32 oc + 8q .. +7; columns past C and
+  // ranks past R repeat the last ones (for results not stored, times zeros).
+  const auto load_w = [&](int n0, int oc, u32x4 (&v)[8]) {
+    const int o = min(oc * 4 + q, octs - 1), col = n0 + c * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (TR) v[i] = ld16(a.W + ((int64_t)t.e * g.R + o * 8 + i) * a.C + min(col, a.C - 8));
+      else v[i] = ld16(a.W + ((int64_t)t.e * a.C + min(col + i, a.C - 1)) * g.R + o * 8);
+    }
+  };
+  const auto turn_w = [&](u32x4 (&v)[8]) {
+    if (TR) {
+      u32x4 r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = column_of(r, j);
+    }
+  };
+  const int first = (cb * a.iters * kExpandWaves + wid) * 128;
+  u32x4 wr[OC ? OC : 1][8];
+  if (OC) {
+#pragma unroll
+    for (int oc = 0; oc < OC; ++oc) load_w(first, oc, wr[oc]);
+  }
   __syncthreads();
 
   // The split operand: parts[p][row][r], rows of RP.
-  const int octs = g.R / 8, RP = padded_rank(g.R), ochunks = (octs + 3) / 4;
   uint16_t* parts = reinterpret_cast<uint16_t*>(sm);
+  const int nrt = (t.rows + 15) / 16, rows16 = nrt * 16;
   const float sc = scale_of(g, t.e);
-  if (tid < BM) {
+  if (tid < rows16) {
     const int pair = tid < t.rows ? pair_of(g, t.row0 + tid) : -1;
     orow[tid] = pair < 0 ? -1 : (a.out_pair ? pair : t.row0 + tid);
     rmax[tid] = 0;
@@ -302,15 +355,13 @@ __global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(Dev g, Expand
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
-    if (a.h && cb == 0 && KIND == OUT_BF16) store8<OUT_F32, false>(a.h, (int64_t)(t.row0 + row) * g.R + o * 8, v);
   };
   if (KIND == OUT_F16) {
     // each row's largest finite magnitude, for its scale
-    for (int i = tid; i < BM * octs; i += kExpandThreads) {
+    for (int i = tid; i < rows16 * octs; i += kExpandThreads) {
       const int row = i / octs, o = i - row * octs;
       float v[8], m = 0.f;
       value(row, o, v);
-      if (a.h && cb == 0 && orow[row] >= 0) store8<OUT_F32, false>(a.h, (int64_t)(t.row0 + row) * g.R + o * 8, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float u = __builtin_fabsf(sc * v[j]);
@@ -320,10 +371,12 @@ __global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(Dev g, Expand
     }
     __syncthreads();
   }
-  for (int i = tid; i < BM * ochunks * 4; i += kExpandThreads) {
+  for (int i = tid; i < rows16 * ochunks * 4; i += kExpandThreads) {
     const int row = i / (ochunks * 4), o = i - row * (ochunks * 4);
     float v[8];
     value(row, o, v);
+    if (a.h && cb == 0 && o < octs && orow[row] >= 0)
+      store8<OUT_F32, false>(a.h, (int64_t)(t.row0 + row) * g.R + o * 8, v);
     const int f = KIND == OUT_F16 ? half_exp(__uint_as_float(rmax[row])) : 0;
     u32x4 pk[NP];
 #pragma unroll
@@ -335,81 +388,101 @@ __global__ __launch_bounds__(kExpandThreads, 2) void expand_kernel(Dev g, Expand
       for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)lo[p] | ((u32)hi[p] << 16);
     }
 #pragma unroll
-    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(parts + (p * BM + row) * RP + o * 8) = pk[p];
+    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(parts + (p * a.bm + row) * RP + o * 8) = pk[p];
   }
   __syncthreads();
 
   for (int it = 0; it < a.iters; ++it) {
-    const int n0 = ((cb * a.iters + it) * kExpandWaves + wid) * 128;
+    const int n0 = first + it * kExpandWaves * 128;
     if (n0 >= a.C) break;
-    const int col = n0 + c * 8;
-    const bool in = col < a.C;
-    u32x4 bv[RT][4];
-    if (a.base) {
+    const int col = n0 + c * 8, colc = min(col, a.C - 8);
+    if (OC) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int oc = 0; oc < OC; ++oc) {
+        if (it > 0) load_w(n0, oc, wr[oc]);
+        turn_w(wr[oc]);
+      }
+    }
+    u32x4 bv[RTI][4], bn[RTI][4];
+    const auto load_base = [&](int rt, u32x4 (&v)[RTI][4]) {
+#pragma unroll
+      for (int x = 0; x < RTI; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[x][i] = ld16(a.base + (int64_t)max(orow[min(rt + x, nrt - 1) * 16 + 4 * q + i], 0) * a.C + colc);
+    };
+    if (has_base) load_base(0, bv);
+    for (int rt = 0; rt < nrt; rt += RTI) {
+      if (has_base && rt + RTI < nrt) load_base(rt + RTI, bn);
+      v4f acc[RTI][8];
+#pragma unroll
+      for (int x = 0; x < RTI; ++x)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[x][j] = v4f{0.f, 0.f, 0.f, 0.f};
+      const auto multiply = [&](int oc, const u32x4 (&v)[8]) {
+#pragma unroll
+        for (int x = 0; x < RTI; ++x)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            const u32x4 l = *reinterpret_cast<u32x4*>(
+                parts + (p * a.bm + min(rt + x, nrt - 1) * 16 + c) * RP + (oc * 4 + q) * 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[x][j] = mfma16<KIND>(l, v[j], acc[x][j]);
+          }
+      };
+      if (OC) {
+#pragma unroll
+        for (int oc = 0; oc < OC; ++oc) multiply(oc, wr[oc]);
+      } else {
+        for (int oc = 0; oc < ochunks; ++oc) {
+          load_w(n0, oc, wr[0]);
+          turn_w(wr[0]);
+          multiply(oc, wr[0]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < RTI; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int o = orow[rt * 16 + 4 * q + i];
-          bv[rt][i] = in && o >= 0 ? ld16(a.base + (int64_t)o * a.C + col) : u32x4{0, 0, 0, 0};
-        }
-    }
-    v4f acc[RT][8];
+          const int row = (rt + x) * 16 + 4 * q + i;
+          const int o = rt + x < nrt ? orow[row] : -1;
+          if (col >= a.C || o < 0) continue;
+          const int f = KIND == OUT_F16 ? -half_exp(__uint_as_float(rmax[row])) : 0;
+          float v[8];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[rt][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int oc = 0; oc < ochunks; ++oc) {
-      const int o = min(oc * 4 + q, octs - 1);  // past R: times the operand's zeros
-      u32x4 raw[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (TR) raw[i] = ld16(a.W + ((int64_t)t.e * g.R + o * 8 + i) * a.C + (in ? col : a.C - 8));
-        else raw[i] = ld16(a.W + ((int64_t)t.e * a.C + min(col + i, a.C - 1)) * g.R + o * 8);
-      }
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        u32x4 l[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          l[rt] = *reinterpret_cast<u32x4*>(parts + (p * BM + rt * 16 + c) * RP + (oc * 4 + q) * 8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const u32x4 b = TR ? column_of(raw, j) : raw[j];
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) acc[rt][j] = mfma16<KIND>(l[rt], b, acc[rt][j]);
-        }
-      }
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = rt * 16 + 4 * q + i, o = orow[row];
-        if (!in || o < 0) continue;
-        const int f = KIND == OUT_F16 ? -half_exp(__uint_as_float(rmax[row])) : 0;
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[j] = KIND == OUT_F16 ? ldexp2(acc[rt][j][i], f) : acc[rt][j][i];
-          if (a.base) {
-            const u32 b = bv[rt][i][j >> 1] >> (16 * (j & 1)) & 0xffffu;
-            v[j] += KIND == OUT_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32((uint16_t)b);
+          for (int j = 0; j < 8; ++j) {
+            v[j] = KIND == OUT_F16 ? ldexp2(acc[x][j][i], f) : acc[x][j][i];
+            if (has_base) {
+              const u32 b = bv[x][i][j >> 1] >> (16 * (j & 1)) & 0xffffu;
+              v[j] += KIND == OUT_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32((uint16_t)b);
+            }
           }
+          store8<KIND, false>(a.out, (int64_t)o * a.C + col, v);
         }
-        store8<KIND, false>(a.out, (int64_t)o * a.C + col, v);
-      }
+#pragma unroll
+      for (int x = 0; x < RTI; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bv[x][i] = bn[x][i];
+    }
   }
 }
 
 // ------------------------------------------------------------------- outer
 constexpr int kOuterWaves = 4;
 constexpr int kOuterThreads = 64 * kOuterWaves;
+constexpr int kOuterCols = 64;   // columns of a wave
+constexpr int kOuterDepth = 3;   // tiles of the wide operand in flight
+constexpr int kOuterChunk = 4096;              // most rows of a chunk, but for the half more of one not cut
+constexpr int kOuterTiles = kOuterChunk / 32 * 2;
 
 // What outer's waves read of a tile of 32 rows of one group, made once by
 // split_kernel: the low-rank operands of both weight gradients as MFMA
 // fragments, fr[side][tile][part][16 ranks][lane][8 rows], the exponents of
-// their scales (F16), and the rows of the wide operands (-1: none).
+// their scales (F16), and the rows of the wide operands.  A row that is not
+// there stands as a row of the tile that is: its low-rank operand is zero, and
+// what the row holds enters its group's sums anyway.  A tile without any row
+// has the exponent kNoRows.
+constexpr int kNoRows = 1 << 20;
 struct Tiles {
   uint16_t* fr;
   int* exps;       // [side][tile]
@@ -427,7 +500,7 @@ struct Side {
   uint16_t* out;       // [E][R][C], or col_major: [E][C][R]
   int col_major;
   float* part;         // [slots][R][C] of the cut groups
-  int slabs;           // 128 columns each
+  int blocks;          // kOuterWaves * kOuterCols columns each
 };
 
 // Exponent of a 32-row tile's scale, a multiple of 16 so that neighbours
@@ -436,57 +509,74 @@ __device__ __forceinline__ int tile_exp(float m) {
   return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~15) - 128;
 }
 
+// One workgroup: one side of one tile.
 template <int KIND>
 __global__ __launch_bounds__(256) void split_kernel(Dev g, Side sa, Side sb, Tiles tl) {
   constexpr int NP = kParts<KIND>;
   __shared__ int sm[kTableInts];
-  __shared__ u32 tmax[2];
+  __shared__ u32 tmax;
+  __shared__ int some;
   const int tid = threadIdx.x;
   sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, 32, 1);
-  const int w = blockIdx.x;
+  const int side = blockIdx.x & 1, w = blockIdx.x >> 1;
   if (w >= sm[g.E]) return;
-  const Tile t = sched_tile<1>(sm, g.offsets, g.E, g.P, 32, 1, w);
+  const Tile t = uniform(sched_tile<1>(sm, g.offsets, g.E, g.P, 32, 1, w));
   const float sc = scale_of(g, t.e);
+  const float* L = side ? sb.L : sa.L;
+  const int splits = side ? sb.splits : sa.splits;
+  const int64_t at = side * tl.tiles + w;
   if (tid < 64) {
-    const int side = tid >> 5, i = tid & 31;
+    const int i = tid & 31;
     const int pair = i < t.rows ? pair_of(g, t.row0 + i) : -1;
-    tl.rows[(side * tl.tiles + w) * 32 + i] = pair < 0 ? -1 : map_row(side ? sb.xm : sa.xm, t.row0 + i, pair);
+    const int row = pair < 0 ? -1 : map_row(side ? sb.xm : sa.xm, t.row0 + i, pair);
+    const unsigned long long there = __ballot(row >= 0);
+    const int stand_in = __shfl(row, max(0, __ffsll(there) - 1), 64);
+    if (tid < 32) tl.rows[at * 32 + i] = row >= 0 ? row : max(0, stand_in);
+    if (tid == 0) {
+      tmax = 0;
+      some = there != 0;
+    }
   }
-  if (tid < 2) tmax[tid] = 0;
   __syncthreads();
-  // task: 8 rows (slice q) of one rank of one side
+  // task: 8 rows (slice q) of one rank
   const int per = 64 * tl.rank_tiles;
-  const auto low = [&](int i, float (&v)[8]) {
-    const int side = i >= per, k = i - side * per, rank = (k >> 6) * 16 + (k & 15), q = k >> 4 & 3;
-    const Side& d = side ? sb : sa;
+  const auto low = [&](int k, float (&v)[8]) {
+    const int rank = (k >> 6) * 16 + (k & 15), q = k >> 4 & 3;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v[j] = 0.f;
       const int s = t.row0 + q * 8 + j;
       if (rank < g.R && q * 8 + j < t.rows && pair_of(g, s) >= 0)
-        for (int sp = 0; sp < d.splits; ++sp) v[j] += d.L[((int64_t)sp * g.P + s) * g.R + rank];
+        for (int sp = 0; sp < splits; ++sp) v[j] += L[((int64_t)sp * g.P + s) * g.R + rank];
       v[j] *= sc;
     }
   };
+  float v[8];
+  if (tid < per) low(tid, v);
   if (KIND == OUT_F16) {
-    for (int i = tid; i < 2 * per; i += 256) {
-      float v[8], big = 0.f;
-      low(i, v);
+    float big = 0.f;
+    const auto raise = [&](const float (&u)[8]) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = __builtin_fabsf(v[j]);
-        big = u < __builtin_inff() ? fmaxf(big, u) : big;
+        const float m = __builtin_fabsf(u[j]);
+        big = m < __builtin_inff() ? fmaxf(big, m) : big;
       }
-      atomicMax(&tmax[i >= per], __float_as_uint(big));
+    };
+    if (tid < per) raise(v);
+    for (int k = tid + 256; k < per; k += 256) {
+      float u[8];
+      low(k, u);
+      raise(u);
     }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
+    if ((tid & 63) == 0) atomicMax(&tmax, __float_as_uint(big));
     __syncthreads();
-    if (tid < 2) tl.exps[tid * tl.tiles + w] = tile_exp(__uint_as_float(tmax[tid]));
   }
-  for (int i = tid; i < 2 * per; i += 256) {
-    const int side = i >= per, k = i - side * per;
-    float v[8];
-    low(i, v);
-    const int f = KIND == OUT_F16 ? tile_exp(__uint_as_float(tmax[side])) : 0;
+  const int f = KIND == OUT_F16 ? tile_exp(__uint_as_float(tmax)) : 0;
+  if (tid == 0) tl.exps[at] = some ? f : kNoRows;
+  for (int k = tid; k < per; k += 256) {
+    if (k >= 256) low(k, v);
     u32x4 pk[NP];
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -497,30 +587,41 @@ __global__ __launch_bounds__(256) void split_kernel(Dev g, Side sa, Side sb, Til
       for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)u0[p] | ((u32)u1[p] << 16);
     }
 #pragma unroll
-    for (int p = 0; p < NP; ++p) st16(tl.fr + (((side * tl.tiles + w) * NP + p) * per + k) * 8, pk[p]);
+    for (int p = 0; p < NP; ++p) st16(tl.fr + ((at * NP + p) * per + k) * 8, pk[p]);
   }
 }
 
-// Slot of the partial sums of the chunk that starts at sorted row s: at most
-// one first and one later chunk of the groups longer than a chunk start in
-// the same `chunk` rows.
-__host__ __device__ constexpr int outer_slot(int s, bool first, int chunk) { return 2 * (s / chunk) + (first ? 1 : 0); }
-__host__ __device__ constexpr int64_t outer_slots(int64_t P, int chunk) { return P > chunk ? 2 * ((P - 1) / chunk + 1) : 0; }
+// A group of m rows is cut into chunks_of(m) runs of its tiles, equal to a
+// tile, of 3/4 to 3/2 of `chunk` rows (at least 256); without rows it has one
+// that writes zeros.
+__host__ __device__ constexpr int chunks_of(int m, int chunk) { return m < chunk ? 1 : (m + chunk / 2) / chunk; }
+__device__ __forceinline__ int chunk_tile(int nt, int i, int n) { return (int)((int64_t)nt * i / n); }
 
-// Chunks of a group of m rows; a group without rows has one that writes zeros.
-__device__ __forceinline__ int chunks_of(int m, int chunk) { return max(1, (m + chunk - 1) / chunk); }
+// Slot of the partial sums of the chunk of a cut group that starts at sorted
+// row s: starts of one group are more than chunk / 2 rows apart, so in the same
+// chunk / 2 rows lie at most one group's first and another's later start.
+__host__ __device__ constexpr int outer_slot(int s, bool first, int chunk) { return 2 * (s / (chunk / 2)) + (first ? 1 : 0); }
+__host__ __device__ constexpr int64_t outer_slots(int64_t P, int chunk) {
+  return chunks_of((int)P, chunk) > 1 ? 2 * ((P - 1) / (chunk / 2) + 1) : 0;
+}
 
-// dW[r][n] = sum_s (scale L[s][r]) X[row(s)][n]: each wave by itself takes one
-// chunk of a group's rows, 128 columns and 16 NR ranks, and walks the chunk's
-// tiles of 32 rows (the MFMA's contraction) with the next tile's 8 KB in
-// flight.  Waves of the same columns and other ranks sit side by side, where
-// the second finds the wide operand in the L1.
+// dW[r][n] = sum_s (scale L[s][r]) X[row(s)][n] for one chunk of a group's
+// rows, 256 columns and 16 NR ranks.  Each of the 4 waves owns 64 columns and
+// walks the chunk's tiles of 32 rows (the MFMA's contraction), three tiles of
+// 4 KB in flight to registers.  The low-rank fragments, which all columns
+// share, and the rows come through LDS by direct-to-LDS copies, pairs of tiles
+// ahead: a row or an exponent that came through a register would be the newest
+// load when it is needed, and waiting for it would be waiting for everything
+// in flight.
 template <int KIND, int NR>
-__global__ __launch_bounds__(kOuterThreads, 2) void outer_kernel(Dev g, Side sa, Side sb, Tiles tl, int rchunks,
+__global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa, Side sb, Tiles tl, int rchunks,
                                                                  int chunk) {
-  constexpr int NP = kParts<KIND>;
+  constexpr int NP = kParts<KIND>, kPieces = NR * NP;  // 1 KB fragments of a tile
+  __shared__ __align__(16) uint16_t ring[2][2][kPieces][512];
+  __shared__ __align__(16) int rows[4][64], exps[kOuterTiles];
   __shared__ int tab[1025], tiles[1025], scratch[2 * kOuterWaves];
-  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6, c = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);  // what a wave shares stays in scalar registers
 
   // Tables of the groups' chunks and 32-row tiles: one scan of both counts.
   {
@@ -561,135 +662,148 @@ __global__ __launch_bounds__(kOuterThreads, 2) void outer_kernel(Dev g, Side sa,
     if (tid == kOuterThreads - 1) tab[g.E] = rc;
     __syncthreads();
   }
-  const int slabs = sa.slabs + sb.slabs;
-  const int task = blockIdx.x * kOuterWaves + wid;
-  const int rc = task % rchunks, w = task / rchunks / slabs;
-  int slab = task / rchunks % slabs;
+  const int rc = blockIdx.x % rchunks, w = blockIdx.x / rchunks / (sa.blocks + sb.blocks);
+  int block = blockIdx.x / rchunks % (sa.blocks + sb.blocks);
   if (w >= tab[g.E]) return;
-  const int side = slab >= sa.slabs;
+  const int side = block >= sa.blocks;
+  if (side) block -= sa.blocks;
   const Side& d = side ? sb : sa;
-  if (side) slab -= sa.slabs;
   int bl = 0, bh = g.E - 1;
   while (bl < bh) {
     const int mid = (bl + bh + 1) >> 1;
     if (tab[mid] <= w) bl = mid; else bh = mid - 1;
   }
-  const int e = bl, ch = w - tab[e];
+  const int e = __builtin_amdgcn_readfirstlane(bl), ch = w - __builtin_amdgcn_readfirstlane(tab[e]);
   int lo, hi;
   expert_range(g.offsets, e, g.P, lo, hi);
-  const int s0 = lo + ch * chunk, first = tiles[e] + ch * (chunk / 32);
+  const int cuts = chunks_of(hi - lo, chunk), all = (hi - lo + 31) / 32;
+  const int k0 = chunk_tile(all, ch, cuts), s0 = lo + k0 * 32;
+  const int first = __builtin_amdgcn_readfirstlane(tiles[e]) + k0;
   // (a malformed offsets table may count more tiles than there can be)
-  const int nt = min((min(chunk, hi - s0) + 31) / 32, (int)max<int64_t>(0, tl.tiles - first));
+  const int nt = min(chunk_tile(all, ch + 1, cuts) - k0, (int)max<int64_t>(0, tl.tiles - first));
   const int64_t t0 = side * tl.tiles + first;
 
-  const int col = min(slab * 128 + c * 8, d.C - 8);
+  // Lane: columns col .. col+3 (past C the last ones again, not stored).
+  const int n0 = (block * kOuterWaves + wid) * kOuterCols + c * 4, col = min(n0, d.C - 4);
   const uint16_t* X = d.X + col;
-  const int* rowp = tl.rows + t0 * 32 + q * 8;
-  // ranks past R: results that are not stored
-  const uint16_t* fp[NR];
-#pragma unroll
-  for (int n = 0; n < NR; ++n)
-    fp[n] = tl.fr + t0 * NP * tl.rank_tiles * 512 + min(rc * NR + n, tl.rank_tiles - 1) * 512 + lane * 8;
-
-  v4f acc[NR][8];
+  v4f acc[NR][4];
 #pragma unroll
   for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[n][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  u32x4 raw[8], fr[NR][NP];
-  int row[8];
-  const auto load_rows = [&](int k) {
-    const v4i r0 = *reinterpret_cast<const v4i*>(rowp + k * 32), r1 = *reinterpret_cast<const v4i*>(rowp + k * 32 + 4);
+    for (int j = 0; j < 4; ++j) acc[n][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  u32x2 raw[kOuterDepth][8];
+  const auto load_x = [&](int k, u32x2 (&v)[8]) {
+    if (k >= nt) return;
+    const int* p = &rows[(k >> 1) & 3][(k & 1) * 32 + q * 8];
+    const v4i r0 = *reinterpret_cast<const v4i*>(p), r1 = *reinterpret_cast<const v4i*>(p + 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      row[i] = r0[i];
-      row[4 + i] = r1[i];
+    for (int i = 0; i < 8; ++i)
+      v[i] = *reinterpret_cast<const u32x2*>(X + (int64_t)(i < 4 ? r0[i] : r1[i - 4]) * d.C);
+  };
+  // The rows of tiles k and k + 1.
+  const auto copy_rows = [&](int k) {
+    if (wid == 0 && k < nt)
+      dma4(tl.rows + (t0 + min(k + (lane >> 5), nt - 1)) * 32 + (lane & 31), lds_addr(rows[(k >> 1) & 3]));
+  };
+  // The fragments of tiles k and k + 1, dealt to the waves; ranks past R
+  // repeat the last ones.
+  const auto copy_fr = [&](int k) {
+    for (int i = wid; i < 2 * kPieces; i += kOuterWaves) {
+      const int x = i / kPieces, p = (i - x * kPieces) / NR, n = i % NR;
+      const int64_t piece = ((t0 + min(k + x, nt - 1)) * NP + p) * tl.rank_tiles + min(rc * NR + n, tl.rank_tiles - 1);
+      dma16(tl.fr + piece * 512 + lane * 8, lds_addr(ring[(k >> 1) & 1][x][p * NR + n]));
     }
   };
-  const auto load_x = [&]() {
+  static_assert(kOuterDepth == 3, "rows are copied for tiles up to k + 4 while tile k is at work");
+  int f = 128;  // F16: exponent of the scale of the sums, the largest while they are zero
+  const auto step = [&](int k, u32x2 (&x8)[8]) {
+    if ((k & 1) == 0) {
+      // The pair's fragments, and the rows of pair k + 4, were copied before
+      // the loads of wide tiles k + 1 and k + 2, 16 of them where both tiles
+      // are there; all waves have them, and are done with the other half of
+      // the ring, behind the barrier.
+      if (k == 0 && nt >= kOuterDepth) wait_vmcnt<8 * kOuterDepth>();
+      else if (k > 0 && k - 1 + kOuterDepth < nt) wait_vmcnt<16>();
+      else wait_vmcnt<0>();
+      raw_barrier();
+      if (k + 2 < nt) copy_fr(k + 2);
+      copy_rows(k + 6);
+    }
+    const int te = __builtin_amdgcn_readfirstlane(exps[k]);
+    if (te == kNoRows) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = row[i] >= 0 ? ld16(X + (int64_t)row[i] * d.C) : u32x4{0, 0, 0, 0};
-  };
-  const auto load_fr = [&](int k) {
+      for (int i = 0; i < 8; ++i) x8[i] = u32x2{0, 0};
+    }
+    int down = 0;
+    if (KIND == OUT_F16 && te != kNoRows) {
+      // The sums keep the smallest scale so far; a tile with a larger one is
+      // brought down to it (what that drops is below 2^-22 of the largest).
+      if (te < f) {
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][j][i] = ldexp2(acc[n][j][i], te - f);
+        f = te;
+      }
+      down = f - te;
+    }
+    u32x4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = column_of(x8, j);
+    load_x(k + kOuterDepth, x8);
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
-      for (int p = 0; p < NP; ++p) fr[n][p] = ld16(fp[n] + ((int64_t)k * NP + p) * tl.rank_tiles * 512);
+      for (int p = 0; p < NP; ++p) {
+        u32x4 a = ld16(&ring[(k >> 1) & 1][k & 1][p * NR + n][lane * 8]);
+        if (KIND == OUT_F16 && down)
+          a = __builtin_bit_cast(u32x4, __builtin_bit_cast(v8h, a) * (_Float16)ldexp2(1.f, down));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[n][j] = mfma16<KIND>(a, x[j], acc[n][j]);
+      }
   };
-  int f = 0;
   if (nt > 0) {
-    load_rows(0);
-    load_x();
-    load_fr(0);
-    if (nt > 1) load_rows(1);
-    f = KIND == OUT_F16 ? tl.exps[t0] : 0;
+    copy_rows(0);
+    copy_rows(2);
+    copy_rows(4);
+    for (int i = wid * 64; i < nt; i += kOuterThreads) dma4(tl.exps + t0 + min(i + lane, nt - 1), lds_addr(exps + i));
+    wait_vmcnt<0>();
+    raw_barrier();
+    copy_fr(0);
+#pragma unroll
+    for (int i = 0; i < kOuterDepth; ++i) load_x(i, raw[i]);
   }
-  for (int k = 0; k < nt; ++k) {
-    if (KIND == OUT_F16) {
-      // The sums keep the smallest scale so far; a tile with a larger one is
-      // brought down to it (what that drops is below 2^-22 of the largest).
-      const int ft = tl.exps[t0 + k];
-      if (ft < f) {
+  for (int k = 0; k < nt; k += kOuterDepth) {
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][j][i] = ldexp2(acc[n][j][i], ft - f);
-        f = ft;
-      } else if (ft > f) {
-        const _Float16 down = (_Float16)ldexp2(1.f, f - ft);
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) fr[n][p] = __builtin_bit_cast(u32x4, __builtin_bit_cast(v8h, fr[n][p]) * down);
-      }
-    }
-#pragma unroll
-    for (int jh = 0; jh < 8; jh += 4) {  // half of the columns at a time: fewer live registers
-      u32x4 x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = column_of(raw, jh + j);
-      if (jh == 4 && k + 1 < nt) {
-        load_x();
-        if (k + 2 < nt) load_rows(k + 2);
-      }
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[n][jh + j] = mfma16<KIND>(fr[n][p], x[j], acc[n][jh + j]);
-    }
-    if (k + 1 < nt) load_fr(k + 1);
+    for (int i = 0; i < kOuterDepth; ++i)
+      if (k + i < nt) step(k + i, raw[i]);
   }
 
-  // Lane: ranks 4q .. 4q+3 of each tile, columns col .. col+7.
-  if (slab * 128 + c * 8 >= d.C) return;
-  const bool cut = hi - lo > chunk;
+  // Lane: ranks 4q .. 4q+3 of each 16, columns col .. col+3.
+  if (n0 >= d.C) return;
 #pragma unroll
   for (int n = 0; n < NR; ++n) {
     const int r0 = (rc * NR + n) * 16 + 4 * q;
     if (r0 >= g.R) continue;
-    float v[4][8];
+    v4f v[4];  // [rank][column]
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = KIND == OUT_F16 ? ldexp2(acc[n][j][i], -f) : acc[n][j][i];
-    if (cut) {
+      for (int j = 0; j < 4; ++j) v[i][j] = KIND == OUT_F16 ? ldexp2(acc[n][j][i], -f) : acc[n][j][i];
+    if (cuts > 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        store8<OUT_F32, false>(d.part, ((int64_t)outer_slot(s0, ch == 0, chunk) * g.R + r0 + i) * d.C + col, v[i]);
+        *reinterpret_cast<v4f*>(d.part + ((int64_t)outer_slot(s0, ch == 0, chunk) * g.R + r0 + i) * d.C + col) = v[i];
     } else if (d.col_major) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const u32 o0 = (u32)OutT<KIND>::from(v[0][j]) | ((u32)OutT<KIND>::from(v[1][j]) << 16);
-        const u32 o1 = (u32)OutT<KIND>::from(v[2][j]) | ((u32)OutT<KIND>::from(v[3][j]) << 16);
-        *reinterpret_cast<uint2*>(d.out + ((int64_t)e * d.C + col + j) * g.R + r0) = make_uint2(o0, o1);
-      }
+      for (int j = 0; j < 4; ++j)
+        store4<KIND>(d.out + ((int64_t)e * d.C + col + j) * g.R + r0, v[0][j], v[1][j], v[2][j], v[3][j]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) store8<KIND, false>(d.out, ((int64_t)e * g.R + r0 + i) * d.C + col, v[i]);
+      for (int i = 0; i < 4; ++i)
+        store4<KIND>(d.out + ((int64_t)e * g.R + r0 + i) * d.C + col, v[i][0], v[i][1], v[i][2], v[i][3]);
     }
   }
 }
@@ -705,20 +819,19 @@ __global__ __launch_bounds__(256) void join_kernel(Dev g, Side sa, Side sb, int 
   if (b >= blocks_a) b -= blocks_a;
   int lo, hi;
   expert_range(g.offsets, e, g.P, lo, hi);
-  if (hi - lo <= chunk) return;
+  const int cuts = chunks_of(hi - lo, chunk), all = (hi - lo + 31) / 32;
+  if (cuts == 1) return;
   const int64_t i = (int64_t)b * 256 + threadIdx.x;
   const int r = (int)(i / d.C) * 4, n = (int)(i % d.C);
   if (r >= g.R) return;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = lo; s < hi; s += chunk) {
-    const float* p = d.part + ((int64_t)outer_slot(s, s == lo, chunk) * g.R + r) * d.C + n;
+  for (int c = 0; c < cuts; ++c) {
+    const float* p = d.part + ((int64_t)outer_slot(lo + 32 * chunk_tile(all, c, cuts), c == 0, chunk) * g.R + r) * d.C + n;
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum[j] += p[(int64_t)j * d.C];
   }
   if (d.col_major) {
-    const u32 o0 = (u32)OutT<KIND>::from(sum[0]) | ((u32)OutT<KIND>::from(sum[1]) << 16);
-    const u32 o1 = (u32)OutT<KIND>::from(sum[2]) | ((u32)OutT<KIND>::from(sum[3]) << 16);
-    *reinterpret_cast<uint2*>(d.out + ((int64_t)e * d.C + n) * g.R + r) = make_uint2(o0, o1);
+    store4<KIND>(d.out + ((int64_t)e * d.C + n) * g.R + r, sum[0], sum[1], sum[2], sum[3]);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) d.out[((int64_t)e * g.R + r + j) * d.C + n] = OutT<KIND>::from(sum[j]);
@@ -733,23 +846,24 @@ RowMap o_map(const LoraArgs& g) { return RowMap{!g.out_pair, 1}; }
 // Upper bound of the row tiles of bm rows: every group may end in a part tile.
 int64_t max_tiles(int64_t P, int E, int bm) { return P / bm + std::min<int64_t>(P, E); }
 
-// Row tiles (of 16) a workgroup takes: as many as the average group fills.
-int shrink_rt(int64_t P, int E, int nr) {
-  if (P >= 64 * (int64_t)E && nr == 1) return 4;
-  return P >= 24 * (int64_t)E ? 2 : 1;
-}
+// Row tiles (of 16) a workgroup takes.  Two halve the reads of the weights;
+// four took more registers than that gave back (Zipf over 256 experts, dh: 120
+// us at two, 145 at four).
+int shrink_rt(int64_t P, int E, int nr) { return P >= 24 * (int64_t)E ? 2 : 1; }
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }  // per workgroup; 64 ranks at most
 
-// Row tiles (of 16) of an expand workgroup; the split operand has to fit LDS.
-int expand_rt(int64_t P, int E, int R) {
-  if (P >= 64 * (int64_t)E && R <= 128) return 4;
-  return P >= 24 * (int64_t)E ? 2 : 1;
+// Rows of an expand workgroup: about the average group's; their split operand
+// has to leave LDS for three workgroups on a compute unit.
+int expand_rows(int64_t P, int E, int R, int f16) {
+  int bm = kExpandRows;
+  while (bm > 16 && ((f16 ? 2 : 3) * bm * padded_rank(R) * 2 > 52 * 1024 || P < bm * (int64_t)E)) bm /= 2;
+  return bm;
 }
 
-// 512-column blocks an expand workgroup walks: up to 8 while 2048 workgroups
+// 512-column blocks an expand workgroup walks: up to 2 while 2048 workgroups
 // remain, more where one grid could not hold the workgroups.
 int expand_iters(int64_t tiles, int blocks) {
-  int iters = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles * blocks / 2048));
+  int iters = (int)std::max<int64_t>(1, std::min<int64_t>(2, tiles * blocks / 2048));
   while (iters < blocks && tiles * ((blocks + iters - 1) / iters) > kMaxBlocks) iters *= 2;
   return iters;
 }
@@ -777,7 +891,6 @@ template <int KIND, bool CM>
 hipError_t shrink(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint16_t* W, float* part, int splits,
                   hipStream_t stream) {
   const int nr = rank_tiles(d.R), rt = shrink_rt(d.P, d.E, nr);
-  if (nr == 1 && rt == 4) return shrink_launch<KIND, 4, 1, CM>(d, X, xm, C, W, part, splits, stream);
   if (nr == 1 && rt == 2) return shrink_launch<KIND, 2, 1, CM>(d, X, xm, C, W, part, splits, stream);
   if (nr == 1) return shrink_launch<KIND, 1, 1, CM>(d, X, xm, C, W, part, splits, stream);
   if (nr == 2 && rt == 2) return shrink_launch<KIND, 2, 2, CM>(d, X, xm, C, W, part, splits, stream);
@@ -786,56 +899,65 @@ hipError_t shrink(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint1
   return shrink_launch<KIND, 1, 4, CM>(d, X, xm, C, W, part, splits, stream);
 }
 
-template <int KIND, int RT, bool TR>
+template <int KIND, int OC, bool TR>
 hipError_t expand_launch(const Dev& d, ExpandArgs a, bool copy, hipStream_t stream) {
-  const int64_t tiles = max_tiles(d.P, d.E, 16 * RT);
+  a.bm = expand_rows(d.P, d.E, d.R, KIND == OUT_F16);
+  const int64_t tiles = max_tiles(d.P, d.E, a.bm);
   const int blocks = (a.C + 511) / 512;
   a.iters = expand_iters(tiles, blocks);
   a.cblocks = (blocks + a.iters - 1) / a.iters;
   a.main_blocks = (int)(tiles * a.cblocks);
   const int copies = copy ? std::min((d.P + kExpandWaves - 1) / kExpandWaves, 1024) : 0;
   const size_t lds = std::max(sizeof(int) * (d.E + 1 + 2 * kMaxWaves),
-                              sizeof(uint16_t) * kParts<KIND> * 16 * RT * padded_rank(d.R));
-  hipLaunchKernelGGL((expand_kernel<KIND, RT, TR>), dim3(a.main_blocks + copies), dim3(kExpandThreads), lds, stream, d,
+                              sizeof(uint16_t) * kParts<KIND> * a.bm * padded_rank(d.R));
+  hipLaunchKernelGGL((expand_kernel<KIND, OC, TR>), dim3(a.main_blocks + copies), dim3(kExpandThreads), lds, stream, d,
                      a);
   return hipGetLastError();
 }
 
 template <int KIND, bool TR>
 hipError_t expand(const Dev& d, const ExpandArgs& a, bool copy, hipStream_t stream) {
-  switch (expand_rt(d.P, d.E, d.R)) {
-    case 4: return expand_launch<KIND, 4, TR>(d, a, copy, stream);
-    case 2: return expand_launch<KIND, 2, TR>(d, a, copy, stream);
-    default: return expand_launch<KIND, 1, TR>(d, a, copy, stream);
-  }
+  if (d.R <= 32) return expand_launch<KIND, 1, TR>(d, a, copy, stream);
+  if (d.R <= 64) return expand_launch<KIND, 2, TR>(d, a, copy, stream);
+  return expand_launch<KIND, 0, TR>(d, a, copy, stream);
 }
 
-int outer_nr(int R) { return R <= 16 ? 1 : 2; }
-int64_t outer_tasks(int E, int N, int K, int R) {  // waves per chunk of rows
-  const int nr = outer_nr(R);
-  return (int64_t)((N + 127) / 128 + (K + 127) / 128) * ((R + 16 * nr - 1) / (16 * nr));
+int outer_nr(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
+int outer_blocks(int C) { return (C + kOuterWaves * kOuterCols - 1) / (kOuterWaves * kOuterCols); }
+int outer_rchunks(int R) { return (R + 16 * outer_nr(R) - 1) / (16 * outer_nr(R)); }
+int64_t outer_tasks(int N, int K, int R) {  // workgroups per chunk of rows
+  return (int64_t)(outer_blocks(N) + outer_blocks(K)) * outer_rchunks(R);
 }
 
-// Rows a wave sums before a longer group is cut: short enough for eight waves
-// on each of 256 compute units, where the rows allow it.
+// About the rows a workgroup sums before a longer group is cut: four times the
+// average group's, so that the longest of skewed groups do not outlast the
+// others (256 experts of 128 rows on average under Zipf routing: 355 us at 512
+// rows, 364 at 256, 382 at 2048; cutting equal groups costs the join: 8 of 2048
+// rows, 418 us whole, 438 in halves), and less where the rows then make no two
+// workgroups for each of 256 compute units.
 int outer_chunk(int64_t P, int E, int N, int K, int R) {
-  for (int chunk = 1024; chunk > 128; chunk /= 2)
-    if (std::max<int64_t>(P / chunk, std::min<int64_t>(P, E)) * outer_tasks(E, N, K, R) >= 2048) return chunk;
-  return 128;
+  int chunk = 256;
+  while (chunk < kOuterChunk && chunk < 4 * P / E) chunk *= 2;
+  while (chunk > 256 && std::max<int64_t>(P / chunk, std::min<int64_t>(P, E)) * outer_tasks(N, K, R) < 512) chunk /= 2;
+  return chunk;
 }
+// Upper bound of all groups' chunks.
+int64_t max_chunks(int64_t P, int E, int chunk) { return P / chunk + E; }
 
 template <int KIND>
 hipError_t outer(const Dev& d, const Side& sa, const Side& sb, const Tiles& tl, int N, int K, hipStream_t stream) {
   const int chunk = outer_chunk(d.P, d.E, N, K, d.R), nr = outer_nr(d.R);
-  const int64_t tasks = (d.P / chunk + d.E) * outer_tasks(d.E, N, K, d.R);
-  const dim3 grid((unsigned)((tasks + kOuterWaves - 1) / kOuterWaves));
-  const int rchunks = (d.R + 16 * nr - 1) / (16 * nr);
+  const int64_t tasks = max_chunks(d.P, d.E, chunk) * outer_tasks(N, K, d.R);
+  const dim3 grid((unsigned)tasks);
+  const int rchunks = outer_rchunks(d.R);
   if (nr == 1)
     hipLaunchKernelGGL((outer_kernel<KIND, 1>), grid, dim3(kOuterThreads), 0, stream, d, sa, sb, tl, rchunks, chunk);
-  else
+  else if (nr == 2)
     hipLaunchKernelGGL((outer_kernel<KIND, 2>), grid, dim3(kOuterThreads), 0, stream, d, sa, sb, tl, rchunks, chunk);
+  else
+    hipLaunchKernelGGL((outer_kernel<KIND, 4>), grid, dim3(kOuterThreads), 0, stream, d, sa, sb, tl, rchunks, chunk);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || d.P <= chunk) return e;
+  if (e != hipSuccess || outer_slots(d.P, chunk) == 0) return e;
   const int ba = (int)(((int64_t)K * (d.R / 4) + 255) / 256), bb = (int)(((int64_t)N * (d.R / 4) + 255) / 256);
   hipLaunchKernelGGL(join_kernel<KIND>, dim3((unsigned)(d.E * (ba + bb))), dim3(256), 0, stream, d, sa, sb, ba, bb,
                      chunk);
@@ -850,7 +972,7 @@ hipError_t forward(const LoraArgs& g, const uint16_t* x, const uint16_t* a, cons
   float* part = splits == 1 && h ? h : ws;
   hipError_t e = shrink<KIND, false>(d, x, x_map(g), g.K, a, part, splits, stream);
   if (e != hipSuccess) return e;
-  ExpandArgs ea = {part, splits, part == h ? nullptr : h, b, g.N, base, out, g.out_pair, 0, 0, 0, g.p2s};
+  ExpandArgs ea = {part, splits, part == h ? nullptr : h, b, g.N, base, out, g.out_pair, 0, 0, 0, 0, g.p2s};
   return expand<KIND, false>(d, ea, g.out_pair && base != out, stream);
 }
 
@@ -883,18 +1005,18 @@ hipError_t backward(const LoraArgs& g, const uint16_t* dy, const uint16_t* x, co
   const BwdLayout l = bwd_layout(g.P, g.E, g.N, g.K, g.R);
   float* dh = reinterpret_cast<float*>(ws);
   const int splits = shrink_splits(g.P, g.E, g.N, g.R);
-  const Side sa = {dh, splits, x, x_map(g), g.K, da, 0, reinterpret_cast<float*>(ws + l.pa), (g.K + 127) / 128};
-  const Side sb = {h, 1, dy, o_map(g), g.N, db, 1, reinterpret_cast<float*>(ws + l.pb), (g.N + 127) / 128};
+  const Side sa = {dh, splits, x, x_map(g), g.K, da, 0, reinterpret_cast<float*>(ws + l.pa), outer_blocks(g.K)};
+  const Side sb = {h, 1, dy, o_map(g), g.N, db, 1, reinterpret_cast<float*>(ws + l.pb), outer_blocks(g.N)};
   const Tiles tl = {reinterpret_cast<uint16_t*>(ws + l.fr), reinterpret_cast<int*>(ws + l.exps),
                     reinterpret_cast<int*>(ws + l.rows), l.tiles, (g.R + 15) / 16};
   if (g.P > 0) {
     hipError_t e = shrink<KIND, true>(d, dy, o_map(g), g.N, b, dh, splits, stream);
     if (e != hipSuccess) return e;
     if (dx) {
-      ExpandArgs ea = {dh, splits, nullptr, a, g.K, nullptr, dx, 0, 0, 0, 0, nullptr};
+      ExpandArgs ea = {dh, splits, nullptr, a, g.K, nullptr, dx, 0, 0, 0, 0, 0, nullptr};
       if ((e = expand<KIND, true>(d, ea, false, stream)) != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(split_kernel<KIND>, dim3((unsigned)l.tiles), dim3(256), 0, stream, d, sa, sb, tl);
+    hipLaunchKernelGGL(split_kernel<KIND>, dim3((unsigned)(2 * l.tiles)), dim3(256), 0, stream, d, sa, sb, tl);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return outer<KIND>(d, sa, sb, tl, g.N, g.K, stream);
@@ -909,12 +1031,12 @@ bool lora_fits(int64_t P, int E, int N, int K, int R) {
     if (max_tiles(P, E, 16 * shrink_rt(P, E, rank_tiles(R))) * shrink_splits(P, E, C, R) * rchunks *
             kShrinkThreads > kThreadsMax)
       return false;
-    const int64_t tiles = max_tiles(P, E, 16 * expand_rt(P, E, R));
+    const int64_t tiles = max_tiles(P, E, expand_rows(P, E, R, 0));
     const int blocks = (C + 511) / 512, iters = expand_iters(tiles, blocks);
     if (tiles * ((blocks + iters - 1) / iters) > kMaxBlocks) return false;
   }
-  return max_tiles(P, E, 32) * 256 <= kThreadsMax &&
-         (P / outer_chunk(P, E, N, K, R) + E) * outer_tasks(E, N, K, R) * 64 <= kThreadsMax &&
+  return max_tiles(P, E, 32) * 512 <= kThreadsMax &&
+         max_chunks(P, E, outer_chunk(P, E, N, K, R)) * outer_tasks(N, K, R) * kOuterThreads <= kThreadsMax &&
          E * (((int64_t)N + K) * (R / 4) / 256 + 2) * 256 <= kThreadsMax;
 }
 

@@ -209,15 +209,15 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     name.  Device placement is faked: this needs no GPU."""
     class Fake(torch.Tensor):
         is_cuda = True
-        index = 1
 
-        @property
-        def device(self):
-            return type("D", (), {"index": self.index, "type": "cuda"})
+        def get_device(self):
+            return 1
 
     t = torch.zeros(4).as_subclass(Fake)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="y is on cuda:1"):
-        mq._here(y=t)
+        mq._here("x y", None, t)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    mq._here(y=t, absent=None)
+    mq._here("y absent", t, None)
