@@ -58,18 +58,81 @@ __device__ __forceinline__ int pair_of(const Dev& g, int s) {
 __device__ __forceinline__ int map_row(const RowMap& m, int s, int pair) { return m.sorted ? s : pair / m.div; }
 __device__ __forceinline__ float scale_of(const Dev& g, int e) { return g.scale ? g.scale[e] : 1.f; }
 
-// Schedule table and scan scratch for up to 1024 groups.
-constexpr int kTableInts = 1025 + 2 * kMaxWaves;
-constexpr int cmax(int a, int b) { return a > b ? a : b; }
+// Inclusive sum over the wave.
+__device__ __forceinline__ int wave_sum(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
 
-// A tile that every lane has alike, in scalar registers.
-__device__ __forceinline__ Tile uniform(const Tile& t) {
-  Tile u;
-  u.e = __builtin_amdgcn_readfirstlane(t.e);
-  u.row0 = __builtin_amdgcn_readfirstlane(t.row0);
-  u.rows = __builtin_amdgcn_readfirstlane(t.rows);
-  u.nt = 0;
-  return u;
+struct Item {
+  int e, lo, hi;  // group and its rows
+  int local;      // the item's number within the group
+  int before;     // sum of count2 over the groups before
+};
+
+// Item w of the groups' items in order, count(rows) of each group: every wave
+// finds it by itself from the offsets, with two sums over the lanes and no
+// barrier, which takes about one trip to the L2 where E <= 256 (a table in LDS
+// took three barriers and a search more; a small call is little else).
+// False past the last item.  All results are wave-uniform.
+template <class F, class F2>
+__device__ __forceinline__ bool find_item(const int* __restrict__ offsets, int E, int P, int w, F count, F2 count2,
+                                          Item& it) {
+  const int lane = threadIdx.x & 63, per = (E + 63) >> 6, e0 = lane * per;
+  int n = 0, n2 = 0, lo = 0, hi = 0;
+  for (int i = 0; i < per; i += 4) {
+    int o[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) o[j] = offsets[min(e0 + i + j, E)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < per && e0 + i + j < E) {
+        lo = min(max(o[j], 0), P);
+        hi = min(max(o[j + 1], lo), P);
+        n += count(hi - lo);
+        n2 += count2(hi - lo);
+      }
+  }
+  int sum = wave_sum(n, lane), sum2 = wave_sum(n2, lane);
+  if (w >= __builtin_amdgcn_readlane(sum, 63)) return false;
+  const int owner = __ffsll(__ballot(sum > w)) - 1;
+  it.e = owner;
+  it.local = w - __builtin_amdgcn_readlane(sum - n, owner);
+  it.before = __builtin_amdgcn_readlane(sum2 - n2, owner);
+  int at = owner;
+  if (per > 1) {  // among the owner's groups
+    const int e = owner * per + lane;
+    const bool mine = lane < per && e < E;
+    const int a = offsets[min(e, E)], b = offsets[min(e + 1, E)];
+    lo = min(max(a, 0), P);
+    hi = min(max(b, lo), P);
+    n = mine ? count(hi - lo) : 0;
+    n2 = mine ? count2(hi - lo) : 0;
+    sum = wave_sum(n, lane);
+    sum2 = wave_sum(n2, lane);
+    at = __ffsll(__ballot(sum > it.local)) - 1;
+    it.e = owner * per + at;
+    it.local -= __builtin_amdgcn_readlane(sum - n, at);
+    it.before += __builtin_amdgcn_readlane(sum2 - n2, at);
+  }
+  it.lo = __builtin_amdgcn_readlane(lo, at);
+  it.hi = __builtin_amdgcn_readlane(hi, at);
+  return true;
+}
+
+// Tile w of bm rows of the groups' rows; false past the last.
+__device__ __forceinline__ bool find_tile(const Dev& g, int bm, int w, Tile& t) {
+  Item it;
+  if (!find_item(g.offsets, g.E, g.P, w, [=](int m) { return (m + bm - 1) / bm; }, [](int) { return 0; }, it)) return false;
+  t.e = it.e;
+  t.row0 = it.lo + it.local * bm;
+  t.rows = min(bm, it.hi - t.row0);
+  t.nt = 0;
+  return true;
 }
 
 template <int KIND>
@@ -143,14 +206,13 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
                                                                 int C, const uint16_t* __restrict__ W,
                                                                 float* __restrict__ part, int splits, int rchunks) {
   constexpr int BM = 16 * RT, RW = 16 * NR + 4;
-  __shared__ __align__(16) int sm[cmax(kTableInts, kShrinkWaves * BM * RW)];
+  __shared__ __align__(16) float red[kShrinkWaves * BM * RW];
   __shared__ __align__(16) uint16_t turn[C_MAJOR ? kShrinkWaves : 1][32 * 16 * NR];
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rc = blockIdx.x % rchunks, sp = blockIdx.x / rchunks % splits, w = blockIdx.x / rchunks / splits;
-  sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, BM, 1);
-  if (w >= sm[g.E]) return;
-  const Tile t = uniform(sched_tile<1>(sm, g.offsets, g.E, g.P, BM, 1, w));
+  Tile t;
+  if (!find_tile(g, BM, w, t)) return;
 
   const uint16_t* xp[RT];
 #pragma unroll
@@ -197,18 +259,14 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
       }
     }
   };
-  if (st0 < st1) load(st0, xb, wb);
-#pragma unroll 2
-  for (int st = st0; st < st1; ++st) {
-    u32x4 xn[RT][4], wn[NR][4];
-    if (st + 1 < st1) load(st + 1, xn, wn);
+  const auto multiply = [&](const u32x4 (&xv)[RT][4], const u32x4 (&wv)[NR][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       u32x4 wf[NR];
       if (C_MAJOR) {
         uint16_t* tw = turn[wid];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) *reinterpret_cast<u32x4*>(tw + (lane + 64 * n) * 8) = wb[n][i];
+        for (int n = 0; n < NR; ++n) *reinterpret_cast<u32x4*>(tw + (lane + 64 * n) * 8) = wv[n][i];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
           const uint16_t* p = tw + (q * 8 + c / 4) * (16 * NR) + n * 16 + (c & 3) * 4;
@@ -216,25 +274,34 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) wf[n] = wb[n][i];
+        for (int n = 0; n < NR; ++n) wf[n] = wv[n][i];
       }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) acc[rt][n] = mfma16<KIND>(wf[n], xb[rt][i], acc[rt][n]);
+        for (int n = 0; n < NR; ++n) acc[rt][n] = mfma16<KIND>(wf[n], xv[rt][i], acc[rt][n]);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) xb[rt][i] = xn[rt][i];
-#pragma unroll
-      for (int n = 0; n < NR; ++n) wb[n][i] = wn[n][i];
-    }
+  };
+  // Two register sets; inside the loop no load is conditional, which would
+  // make the compiler wait for all of them.
+  int st = st0;
+  if (st < st1) load(st, xb, wb);
+  u32x4 xn[RT][4], wn[NR][4];
+  for (; st + 2 < st1; st += 2) {
+    load(st + 1, xn, wn);
+    multiply(xb, wb);
+    load(st + 2, xb, wb);
+    multiply(xn, wn);
+  }
+  if (st + 1 < st1) {
+    load(st + 1, xn, wn);
+    multiply(xb, wb);
+    multiply(xn, wn);
+  } else if (st < st1) {
+    multiply(xb, wb);
   }
 
-  // The waves' sums meet in LDS (over the schedule, which is done with).
-  __syncthreads();
-  float* red = reinterpret_cast<float*>(sm);
+  // The waves' sums meet in LDS.
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -255,6 +322,121 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
   }
 }
 
+// ------------------------------------------------------------------- split
+// What outer's waves read of a tile of 32 rows of one group, made once by
+// split_tile: the low-rank operands of both weight gradients as MFMA
+// fragments, fr[side][tile][part][16 ranks][lane][8 rows], the exponents of
+// their scales (F16), and the rows of the wide operands.  A row that is not
+// there stands as a row of the tile that is: its low-rank operand is zero, and
+// what the row holds enters its group's sums anyway.  A tile without any row
+// has the exponent kNoRows.
+constexpr int kNoRows = 1 << 20;
+struct Tiles {
+  uint16_t* fr;
+  int* exps;       // [side][tile]
+  int* rows;       // [side][tile][32]
+  int64_t tiles;   // allocated
+  int rank_tiles;
+};
+
+struct Side {
+  const float* L;      // [splits][P][R], summed here; times the group's scale
+  int splits;
+  const uint16_t* X;   // the wide operand
+  RowMap xm;
+  int C;
+  uint16_t* out;       // [E][R][C], or col_major: [E][C][R]
+  int col_major;
+  float* part;         // [slots][R][C] of the cut groups
+  int blocks;          // kOuterWaves * kOuterCols columns each
+};
+
+// Exponent of a 32-row tile's scale, a multiple of 16 so that neighbours
+// rarely differ: brings m to [2^-2, 2^14).
+__device__ __forceinline__ int tile_exp(float m) {
+  return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~15) - 128;
+}
+
+// One workgroup of 256 threads: one side of one tile.
+template <int KIND>
+__device__ void split_tile(const Dev& g, const Side& sa, const Side& sb, const Tiles& tl, int unit) {
+  constexpr int NP = kParts<KIND>;
+  __shared__ u32 tmax;
+  __shared__ int some;
+  const int tid = threadIdx.x;
+  const int side = unit & 1, w = unit >> 1;
+  Tile t;
+  if (!find_tile(g, 32, w, t)) return;
+  const float sc = scale_of(g, t.e);
+  const float* L = side ? sb.L : sa.L;
+  const int splits = side ? sb.splits : sa.splits;
+  const int64_t at = side * tl.tiles + w;
+  if (tid < 64) {
+    const int i = tid & 31;
+    const int pair = i < t.rows ? pair_of(g, t.row0 + i) : -1;
+    const int row = pair < 0 ? -1 : map_row(side ? sb.xm : sa.xm, t.row0 + i, pair);
+    const unsigned long long there = __ballot(row >= 0);
+    const int stand_in = __shfl(row, max(0, __ffsll(there) - 1), 64);
+    if (tid < 32) tl.rows[at * 32 + i] = row >= 0 ? row : max(0, stand_in);
+    if (tid == 0) {
+      tmax = 0;
+      some = there != 0;
+    }
+  }
+  __syncthreads();
+  // task: 8 rows (slice q) of one rank
+  const int per = 64 * tl.rank_tiles;
+  const auto low = [&](int k, float (&v)[8]) {
+    const int rank = (k >> 6) * 16 + (k & 15), q = k >> 4 & 3;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = 0.f;
+      const int s = t.row0 + q * 8 + j;
+      if (rank < g.R && q * 8 + j < t.rows && pair_of(g, s) >= 0)
+        for (int sp = 0; sp < splits; ++sp) v[j] += L[((int64_t)sp * g.P + s) * g.R + rank];
+      v[j] *= sc;
+    }
+  };
+  float v[8];
+  if (tid < per) low(tid, v);
+  if (KIND == OUT_F16) {
+    float big = 0.f;
+    const auto raise = [&](const float (&u)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float m = __builtin_fabsf(u[j]);
+        big = m < __builtin_inff() ? fmaxf(big, m) : big;
+      }
+    };
+    if (tid < per) raise(v);
+    for (int k = tid + 256; k < per; k += 256) {
+      float u[8];
+      low(k, u);
+      raise(u);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
+    if ((tid & 63) == 0) atomicMax(&tmax, __float_as_uint(big));
+    __syncthreads();
+  }
+  const int f = KIND == OUT_F16 ? tile_exp(__uint_as_float(tmax)) : 0;
+  if (tid == 0) tl.exps[at] = some ? f : kNoRows;
+  for (int k = tid; k < per; k += 256) {
+    if (k >= 256) low(k, v);
+    u32x4 pk[NP];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      uint16_t u0[NP], u1[NP];
+      split<KIND>(KIND == OUT_F16 ? ldexp2(v[j], f) : v[j], u0);
+      split<KIND>(KIND == OUT_F16 ? ldexp2(v[j + 1], f) : v[j + 1], u1);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)u0[p] | ((u32)u1[p] << 16);
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) st16(tl.fr + ((at * NP + p) * per + k) * 8, pk[p]);
+  }
+}
+
 // ------------------------------------------------------------------ expand
 constexpr int kExpandThreads = 256;
 constexpr int kExpandWaves = kExpandThreads / 64;
@@ -272,8 +454,10 @@ struct ExpandArgs {
   int bm;                // rows a workgroup takes, a multiple of 16 up to kExpandRows
   int iters;             // 512-column blocks a workgroup walks
   int cblocks;           // workgroups across the columns
-  int main_blocks;       // workgroups of the rows with a group; the others copy
-  const int* p2s;        // the rows without one
+  int main_blocks;       // workgroups of the rows with a group; the others
+  const int* p2s;        // copy the rows without one (by pair_to_sorted), or, in
+  Side sa, sb;           // the gradient, make the outer kernel's tiles
+  Tiles tl;
 };
 
 __host__ __device__ constexpr int padded_rank(int R) { return (R + 31) / 32 * 32 + 8; }
@@ -292,6 +476,10 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);  // what a wave shares stays in scalar registers
   if ((int)blockIdx.x >= a.main_blocks) {
+    if (TR) {
+      split_tile<KIND>(g, a.sa, a.sb, a.tl, blockIdx.x - a.main_blocks);
+      return;
+    }
     const int nw = (gridDim.x - a.main_blocks) * kExpandWaves;
     for (int p = (blockIdx.x - a.main_blocks) * kExpandWaves + wid; p < g.P; p += nw) {
       const int s = a.p2s[p];
@@ -302,9 +490,8 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
     return;
   }
   const int w = blockIdx.x / a.cblocks, cb = blockIdx.x - w * a.cblocks;
-  sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, a.bm, 1);
-  if (w >= sm[g.E]) return;
-  const Tile t = uniform(sched_tile<1>(sm, g.offsets, g.E, g.P, a.bm, 1, w));
+  Tile t;
+  if (!find_tile(g, a.bm, w, t)) return;
 
   const bool has_base = !TR && a.base;  // dx has none
   const int octs = g.R / 8, RP = padded_rank(g.R), ochunks = (octs + 3) / 4;
@@ -333,7 +520,6 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
 #pragma unroll
     for (int oc = 0; oc < OC; ++oc) load_w(first, oc, wr[oc]);
   }
-  __syncthreads();
 
   // The split operand: parts[p][row][r], rows of RP.
   uint16_t* parts = reinterpret_cast<uint16_t*>(sm);
@@ -475,122 +661,6 @@ constexpr int kOuterDepth = 3;   // tiles of the wide operand in flight
 constexpr int kOuterChunk = 4096;              // most rows of a chunk, but for the half more of one not cut
 constexpr int kOuterTiles = kOuterChunk / 32 * 2;
 
-// What outer's waves read of a tile of 32 rows of one group, made once by
-// split_kernel: the low-rank operands of both weight gradients as MFMA
-// fragments, fr[side][tile][part][16 ranks][lane][8 rows], the exponents of
-// their scales (F16), and the rows of the wide operands.  A row that is not
-// there stands as a row of the tile that is: its low-rank operand is zero, and
-// what the row holds enters its group's sums anyway.  A tile without any row
-// has the exponent kNoRows.
-constexpr int kNoRows = 1 << 20;
-struct Tiles {
-  uint16_t* fr;
-  int* exps;       // [side][tile]
-  int* rows;       // [side][tile][32]
-  int64_t tiles;   // allocated
-  int rank_tiles;
-};
-
-struct Side {
-  const float* L;      // [splits][P][R], summed here; times the group's scale
-  int splits;
-  const uint16_t* X;   // the wide operand
-  RowMap xm;
-  int C;
-  uint16_t* out;       // [E][R][C], or col_major: [E][C][R]
-  int col_major;
-  float* part;         // [slots][R][C] of the cut groups
-  int blocks;          // kOuterWaves * kOuterCols columns each
-};
-
-// Exponent of a 32-row tile's scale, a multiple of 16 so that neighbours
-// rarely differ: brings m to [2^-2, 2^14).
-__device__ __forceinline__ int tile_exp(float m) {
-  return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~15) - 128;
-}
-
-// One workgroup: one side of one tile.
-template <int KIND>
-__global__ __launch_bounds__(256) void split_kernel(Dev g, Side sa, Side sb, Tiles tl) {
-  constexpr int NP = kParts<KIND>;
-  __shared__ int sm[kTableInts];
-  __shared__ u32 tmax;
-  __shared__ int some;
-  const int tid = threadIdx.x;
-  sched_build(sm, sm + g.E + 1, g.offsets, g.E, g.P, 32, 1);
-  const int side = blockIdx.x & 1, w = blockIdx.x >> 1;
-  if (w >= sm[g.E]) return;
-  const Tile t = uniform(sched_tile<1>(sm, g.offsets, g.E, g.P, 32, 1, w));
-  const float sc = scale_of(g, t.e);
-  const float* L = side ? sb.L : sa.L;
-  const int splits = side ? sb.splits : sa.splits;
-  const int64_t at = side * tl.tiles + w;
-  if (tid < 64) {
-    const int i = tid & 31;
-    const int pair = i < t.rows ? pair_of(g, t.row0 + i) : -1;
-    const int row = pair < 0 ? -1 : map_row(side ? sb.xm : sa.xm, t.row0 + i, pair);
-    const unsigned long long there = __ballot(row >= 0);
-    const int stand_in = __shfl(row, max(0, __ffsll(there) - 1), 64);
-    if (tid < 32) tl.rows[at * 32 + i] = row >= 0 ? row : max(0, stand_in);
-    if (tid == 0) {
-      tmax = 0;
-      some = there != 0;
-    }
-  }
-  __syncthreads();
-  // task: 8 rows (slice q) of one rank
-  const int per = 64 * tl.rank_tiles;
-  const auto low = [&](int k, float (&v)[8]) {
-    const int rank = (k >> 6) * 16 + (k & 15), q = k >> 4 & 3;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] = 0.f;
-      const int s = t.row0 + q * 8 + j;
-      if (rank < g.R && q * 8 + j < t.rows && pair_of(g, s) >= 0)
-        for (int sp = 0; sp < splits; ++sp) v[j] += L[((int64_t)sp * g.P + s) * g.R + rank];
-      v[j] *= sc;
-    }
-  };
-  float v[8];
-  if (tid < per) low(tid, v);
-  if (KIND == OUT_F16) {
-    float big = 0.f;
-    const auto raise = [&](const float (&u)[8]) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float m = __builtin_fabsf(u[j]);
-        big = m < __builtin_inff() ? fmaxf(big, m) : big;
-      }
-    };
-    if (tid < per) raise(v);
-    for (int k = tid + 256; k < per; k += 256) {
-      float u[8];
-      low(k, u);
-      raise(u);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, 64));
-    if ((tid & 63) == 0) atomicMax(&tmax, __float_as_uint(big));
-    __syncthreads();
-  }
-  const int f = KIND == OUT_F16 ? tile_exp(__uint_as_float(tmax)) : 0;
-  if (tid == 0) tl.exps[at] = some ? f : kNoRows;
-  for (int k = tid; k < per; k += 256) {
-    if (k >= 256) low(k, v);
-    u32x4 pk[NP];
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint16_t u0[NP], u1[NP];
-      split<KIND>(KIND == OUT_F16 ? ldexp2(v[j], f) : v[j], u0);
-      split<KIND>(KIND == OUT_F16 ? ldexp2(v[j + 1], f) : v[j + 1], u1);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)u0[p] | ((u32)u1[p] << 16);
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p) st16(tl.fr + ((at * NP + p) * per + k) * 8, pk[p]);
-  }
-}
-
 // A group of m rows is cut into chunks_of(m) runs of its tiles, equal to a
 // tile, of 3/4 to 3/2 of `chunk` rows (at least 256); without rows it has one
 // that writes zeros.
@@ -619,66 +689,22 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
   constexpr int NP = kParts<KIND>, kPieces = NR * NP;  // 1 KB fragments of a tile
   __shared__ __align__(16) uint16_t ring[2][2][kPieces][512];
   __shared__ __align__(16) int rows[4][64], exps[kOuterTiles];
-  __shared__ int tab[1025], tiles[1025], scratch[2 * kOuterWaves];
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
   const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);  // what a wave shares stays in scalar registers
 
-  // Tables of the groups' chunks and 32-row tiles: one scan of both counts.
-  {
-    const int per = (g.E + kOuterThreads - 1) / kOuterThreads;
-    const int e0 = min(g.E, tid * per), e1 = min(g.E, e0 + per);
-    int nc = 0, nt = 0, lo, hi;
-    for (int e = e0; e < e1; ++e) {
-      expert_range(g.offsets, e, g.P, lo, hi);
-      nc += chunks_of(hi - lo, chunk);
-      nt += (hi - lo + 31) / 32;
-    }
-    int ic = nc, it = nt;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int vc = __shfl_up(ic, o, 64), vt = __shfl_up(it, o, 64);
-      if (lane >= o) {
-        ic += vc;
-        it += vt;
-      }
-    }
-    if (lane == 63) {
-      scratch[wid] = ic;
-      scratch[kOuterWaves + wid] = it;
-    }
-    __syncthreads();
-    int rc = ic - nc, rt = it - nt;
-    for (int v = 0; v < wid; ++v) {
-      rc += scratch[v];
-      rt += scratch[kOuterWaves + v];
-    }
-    for (int e = e0; e < e1; ++e) {
-      tab[e] = rc;
-      tiles[e] = rt;
-      expert_range(g.offsets, e, g.P, lo, hi);
-      rc += chunks_of(hi - lo, chunk);
-      rt += (hi - lo + 31) / 32;
-    }
-    if (tid == kOuterThreads - 1) tab[g.E] = rc;
-    __syncthreads();
-  }
   const int rc = blockIdx.x % rchunks, w = blockIdx.x / rchunks / (sa.blocks + sb.blocks);
   int block = blockIdx.x / rchunks % (sa.blocks + sb.blocks);
-  if (w >= tab[g.E]) return;
+  Item it;
+  if (!find_item(g.offsets, g.E, g.P, w, [=](int m) { return chunks_of(m, chunk); },
+                 [](int m) { return (m + 31) / 32; }, it))
+    return;
   const int side = block >= sa.blocks;
   if (side) block -= sa.blocks;
   const Side& d = side ? sb : sa;
-  int bl = 0, bh = g.E - 1;
-  while (bl < bh) {
-    const int mid = (bl + bh + 1) >> 1;
-    if (tab[mid] <= w) bl = mid; else bh = mid - 1;
-  }
-  const int e = __builtin_amdgcn_readfirstlane(bl), ch = w - __builtin_amdgcn_readfirstlane(tab[e]);
-  int lo, hi;
-  expert_range(g.offsets, e, g.P, lo, hi);
+  const int e = it.e, ch = it.local, lo = it.lo, hi = it.hi;
   const int cuts = chunks_of(hi - lo, chunk), all = (hi - lo + 31) / 32;
   const int k0 = chunk_tile(all, ch, cuts), s0 = lo + k0 * 32;
-  const int first = __builtin_amdgcn_readfirstlane(tiles[e]) + k0;
+  const int first = it.before + k0;
   // (a malformed offsets table may count more tiles than there can be)
   const int nt = min(chunk_tile(all, ch + 1, cuts) - k0, (int)max<int64_t>(0, tl.tiles - first));
   const int64_t t0 = side * tl.tiles + first;
@@ -900,26 +926,25 @@ hipError_t shrink(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint1
 }
 
 template <int KIND, int OC, bool TR>
-hipError_t expand_launch(const Dev& d, ExpandArgs a, bool copy, hipStream_t stream) {
+hipError_t expand_launch(const Dev& d, ExpandArgs a, int others, hipStream_t stream) {
   a.bm = expand_rows(d.P, d.E, d.R, KIND == OUT_F16);
   const int64_t tiles = max_tiles(d.P, d.E, a.bm);
   const int blocks = (a.C + 511) / 512;
   a.iters = expand_iters(tiles, blocks);
   a.cblocks = (blocks + a.iters - 1) / a.iters;
   a.main_blocks = (int)(tiles * a.cblocks);
-  const int copies = copy ? std::min((d.P + kExpandWaves - 1) / kExpandWaves, 1024) : 0;
-  const size_t lds = std::max(sizeof(int) * (d.E + 1 + 2 * kMaxWaves),
-                              sizeof(uint16_t) * kParts<KIND> * a.bm * padded_rank(d.R));
-  hipLaunchKernelGGL((expand_kernel<KIND, OC, TR>), dim3(a.main_blocks + copies), dim3(kExpandThreads), lds, stream, d,
+  if (!a.out) a.main_blocks = 0;
+  const size_t lds = sizeof(uint16_t) * kParts<KIND> * a.bm * padded_rank(d.R);
+  hipLaunchKernelGGL((expand_kernel<KIND, OC, TR>), dim3(a.main_blocks + others), dim3(kExpandThreads), lds, stream, d,
                      a);
   return hipGetLastError();
 }
 
 template <int KIND, bool TR>
-hipError_t expand(const Dev& d, const ExpandArgs& a, bool copy, hipStream_t stream) {
-  if (d.R <= 32) return expand_launch<KIND, 1, TR>(d, a, copy, stream);
-  if (d.R <= 64) return expand_launch<KIND, 2, TR>(d, a, copy, stream);
-  return expand_launch<KIND, 0, TR>(d, a, copy, stream);
+hipError_t expand(const Dev& d, const ExpandArgs& a, int others, hipStream_t stream) {
+  if (d.R <= 32) return expand_launch<KIND, 1, TR>(d, a, others, stream);
+  if (d.R <= 64) return expand_launch<KIND, 2, TR>(d, a, others, stream);
+  return expand_launch<KIND, 0, TR>(d, a, others, stream);
 }
 
 int outer_nr(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
@@ -972,8 +997,9 @@ hipError_t forward(const LoraArgs& g, const uint16_t* x, const uint16_t* a, cons
   float* part = splits == 1 && h ? h : ws;
   hipError_t e = shrink<KIND, false>(d, x, x_map(g), g.K, a, part, splits, stream);
   if (e != hipSuccess) return e;
+  const int copies = g.out_pair && base != out ? std::min((d.P + kExpandWaves - 1) / kExpandWaves, 1024) : 0;
   ExpandArgs ea = {part, splits, part == h ? nullptr : h, b, g.N, base, out, g.out_pair, 0, 0, 0, 0, g.p2s};
-  return expand<KIND, false>(d, ea, g.out_pair && base != out, stream);
+  return expand<KIND, false>(d, ea, copies, stream);
 }
 
 // Workspace of the gradients: dh's partial sums, the tiles of both low-rank
@@ -1012,12 +1038,8 @@ hipError_t backward(const LoraArgs& g, const uint16_t* dy, const uint16_t* x, co
   if (g.P > 0) {
     hipError_t e = shrink<KIND, true>(d, dy, o_map(g), g.N, b, dh, splits, stream);
     if (e != hipSuccess) return e;
-    if (dx) {
-      ExpandArgs ea = {dh, splits, nullptr, a, g.K, nullptr, dx, 0, 0, 0, 0, 0, nullptr};
-      if ((e = expand<KIND, true>(d, ea, false, stream)) != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(split_kernel<KIND>, dim3((unsigned)(2 * l.tiles)), dim3(256), 0, stream, d, sa, sb, tl);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    ExpandArgs ea = {dh, splits, nullptr, a, g.K, nullptr, dx, 0, 0, 0, 0, 0, nullptr, sa, sb, tl};
+    if ((e = expand<KIND, true>(d, ea, (int)(2 * l.tiles), stream)) != hipSuccess) return e;
   }
   return outer<KIND>(d, sa, sb, tl, g.N, g.K, stream);
 }
@@ -1035,7 +1057,7 @@ bool lora_fits(int64_t P, int E, int N, int K, int R) {
     const int blocks = (C + 511) / 512, iters = expand_iters(tiles, blocks);
     if (tiles * ((blocks + iters - 1) / iters) > kMaxBlocks) return false;
   }
-  return max_tiles(P, E, 32) * 512 <= kThreadsMax &&
+  return max_tiles(P, E, 32) * 512 <= kThreadsMax / 2 &&
          max_chunks(P, E, outer_chunk(P, E, N, K, R)) * outer_tasks(N, K, R) * kOuterThreads <= kThreadsMax &&
          E * (((int64_t)N + K) * (R / 4) / 256 + 2) * 256 <= kThreadsMax;
 }
