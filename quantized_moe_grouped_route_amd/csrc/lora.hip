@@ -467,7 +467,7 @@ __host__ __device__ constexpr int padded_rank(int R) { return (R + 31) / 32 * 32
 // Each wave then takes 128 columns at a time, keeps their weights of OC x 32
 // ranks in registers and walks the rows 16 at a time, the next rows' base in
 // flight; OC = 0 takes any rank, reloading the weights for every 32 rows.
-template <int KIND, int OC, bool TR>
+template <int KIND, int OC, bool TR, bool NT>
 __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev g, ExpandArgs a) {
   constexpr int NP = kParts<KIND>, RTI = OC ? 1 : 2;
   extern __shared__ __align__(16) int sm[];
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
       for (int x = 0; x < RTI; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          v[x][i] = ld16(a.base + (int64_t)max(orow[min(rt + x, nrt - 1) * 16 + 4 * q + i], 0) * a.C + colc);
+          v[x][i] = ld16_nt<NT>(a.base + (int64_t)max(orow[min(rt + x, nrt - 1) * 16 + 4 * q + i], 0) * a.C + colc);
     };
     if (has_base) load_base(0, bv);
     for (int rt = 0; rt < nrt; rt += RTI) {
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
               v[j] += KIND == OUT_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32((uint16_t)b);
             }
           }
-          store8<KIND, false>(a.out, (int64_t)o * a.C + col, v);
+          store8<KIND, NT>(a.out, (int64_t)o * a.C + col, v);
         }
 #pragma unroll
       for (int x = 0; x < RTI; ++x)
@@ -724,7 +724,8 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
     const v4i r0 = *reinterpret_cast<const v4i*>(p), r1 = *reinterpret_cast<const v4i*>(p + 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      v[i] = *reinterpret_cast<const u32x2*>(X + (int64_t)(i < 4 ? r0[i] : r1[i - 4]) * d.C);
+      v[i] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x2*>(X + (int64_t)(i < 4 ? r0[i] : r1[i - 4]) * d.C));
   };
   // The rows of tiles k and k + 1.
   const auto copy_rows = [&](int k) {
@@ -925,7 +926,7 @@ hipError_t shrink(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint1
   return shrink_launch<KIND, 1, 4, CM>(d, X, xm, C, W, part, splits, stream);
 }
 
-template <int KIND, int OC, bool TR>
+template <int KIND, int OC, bool TR, bool NT>
 hipError_t expand_launch(const Dev& d, ExpandArgs a, int others, hipStream_t stream) {
   a.bm = expand_rows(d.P, d.E, d.R, KIND == OUT_F16);
   const int64_t tiles = max_tiles(d.P, d.E, a.bm);
@@ -935,16 +936,27 @@ hipError_t expand_launch(const Dev& d, ExpandArgs a, int others, hipStream_t str
   a.main_blocks = (int)(tiles * a.cblocks);
   if (!a.out) a.main_blocks = 0;
   const size_t lds = sizeof(uint16_t) * kParts<KIND> * a.bm * padded_rank(d.R);
-  hipLaunchKernelGGL((expand_kernel<KIND, OC, TR>), dim3(a.main_blocks + others), dim3(kExpandThreads), lds, stream, d,
+  hipLaunchKernelGGL((expand_kernel<KIND, OC, TR, NT>), dim3(a.main_blocks + others), dim3(kExpandThreads), lds, stream, d,
                      a);
   return hipGetLastError();
 }
 
+template <int KIND, bool TR, bool NT>
+hipError_t expand_nt(const Dev& d, const ExpandArgs& a, int others, hipStream_t stream) {
+  if (d.R <= 32) return expand_launch<KIND, 1, TR, NT>(d, a, others, stream);
+  if (d.R <= 64) return expand_launch<KIND, 2, TR, NT>(d, a, others, stream);
+  return expand_launch<KIND, 0, TR, NT>(d, a, others, stream);
+}
+
+// `bytes`: what the launch streams, with what the launches after it read
+// again.  Where that is more than the Infinity Cache holds, base and out go
+// past it: beside the Mixtral-sized gate+up projection 386 -> 369 us, and the
+// gradients, whose next launch reads dy again, 387 -> 346 us (rank 64,
+// Mixtral-sized) and 345 -> 335 us (Zipf over 256 experts).
 template <int KIND, bool TR>
-hipError_t expand(const Dev& d, const ExpandArgs& a, int others, hipStream_t stream) {
-  if (d.R <= 32) return expand_launch<KIND, 1, TR>(d, a, others, stream);
-  if (d.R <= 64) return expand_launch<KIND, 2, TR>(d, a, others, stream);
-  return expand_launch<KIND, 0, TR>(d, a, others, stream);
+hipError_t expand(const Dev& d, const ExpandArgs& a, int others, int64_t bytes, hipStream_t stream) {
+  return bytes >= (int64_t(256) << 20) ? expand_nt<KIND, TR, true>(d, a, others, stream)
+                                       : expand_nt<KIND, TR, false>(d, a, others, stream);
 }
 
 int outer_nr(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
@@ -999,7 +1011,7 @@ hipError_t forward(const LoraArgs& g, const uint16_t* x, const uint16_t* a, cons
   if (e != hipSuccess) return e;
   const int copies = g.out_pair && base != out ? std::min((d.P + kExpandWaves - 1) / kExpandWaves, 1024) : 0;
   ExpandArgs ea = {part, splits, part == h ? nullptr : h, b, g.N, base, out, g.out_pair, 0, 0, 0, 0, g.p2s};
-  return expand<KIND, false>(d, ea, copies, stream);
+  return expand<KIND, false>(d, ea, copies, g.P * g.N * (base ? 4 : 2), stream);
 }
 
 // Workspace of the gradients: dh's partial sums, the tiles of both low-rank
@@ -1039,7 +1051,8 @@ hipError_t backward(const LoraArgs& g, const uint16_t* dy, const uint16_t* x, co
     hipError_t e = shrink<KIND, true>(d, dy, o_map(g), g.N, b, dh, splits, stream);
     if (e != hipSuccess) return e;
     ExpandArgs ea = {dh, splits, nullptr, a, g.K, nullptr, dx, 0, 0, 0, 0, 0, nullptr, sa, sb, tl};
-    if ((e = expand<KIND, true>(d, ea, (int)(2 * l.tiles), stream)) != hipSuccess) return e;
+    if ((e = expand<KIND, true>(d, ea, (int)(2 * l.tiles), g.P * (g.N + 2 * (int64_t)g.K) * 2, stream)) != hipSuccess)
+      return e;
   }
   return outer<KIND>(d, sa, sb, tl, g.N, g.K, stream);
 }
