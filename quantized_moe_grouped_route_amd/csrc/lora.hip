@@ -194,26 +194,40 @@ __device__ __forceinline__ float ldexp2(float v, int e) { return __builtin_amdgc
 constexpr int kShrinkWaves = 8;
 constexpr int kShrinkThreads = 64 * kShrinkWaves;
 
-// part[split][s][r] = sum over the split's columns of X[row(s)][k] W[e][r][k]
-// (W [E][R][C]; C_MAJOR: W [E][C][R], as B is stored for dh).  One workgroup: 16 RT rows of one group, 16 NR ranks, one split of the
-// columns, dealt to its 8 waves in steps of 128.  Rows past the tile and ranks
-// past R repeat valid ones: they only reach results that are not stored.
-// C_MAJOR weights pass through the wave's own piece of LDS, 32 columns at a
-// time, and come back through the transposing read (lane i of 16 gets column
-// i of a 4 x 16 block), so that B needs no transposed copy in memory.
-template <int KIND, int RT, int NR, bool C_MAJOR>
-__global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm,
-                                                                int C, const uint16_t* __restrict__ W,
-                                                                float* __restrict__ part, int splits, int rchunks) {
-  constexpr int BM = 16 * RT, RW = 16 * NR + 4;
-  __shared__ __align__(16) float red[kShrinkWaves * BM * RW];
-  __shared__ __align__(16) uint16_t turn[C_MAJOR ? kShrinkWaves : 1][32 * 16 * NR];
-  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
-  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rc = blockIdx.x % rchunks, sp = blockIdx.x / rchunks % splits, w = blockIdx.x / rchunks / splits;
-  Tile t;
-  if (!find_tile(g, BM, w, t)) return;
+// red[wave][row][rank] = the wave's share of sum_k X[row(s)][k] W[e][r][k] for
+// 16 RT rows of one group and 16 NR ranks (W [E][R][C]; C_MAJOR: W [E][C][R],
+// as B is stored for dh), complete behind the barrier at the end.  The columns
+// are dealt in steps of 128: this wave takes share `slot` of `slots`.  Rows
+// past the tile and ranks past R repeat valid ones: they only reach results
+// that are not used.  C_MAJOR weights pass through the wave's own piece of LDS,
+// 32 columns at a time, and come back through the transposing read (lane i of
+// 16 gets column i of a 4 x 16 block), so that B needs no transposed copy in
+// memory.
+template <int RT, int NR, bool C_MAJOR>
+struct ShrinkLds {
+  static constexpr int BM = 16 * RT, RW = 16 * NR + 4;
+  float red[kShrinkWaves * BM * RW] __attribute__((aligned(16)));
+  uint16_t turn[C_MAJOR ? kShrinkWaves : 1][32 * 16 * NR] __attribute__((aligned(16)));
+  // Four ranks from r of a row, over the waves.
+  __device__ __forceinline__ v4f sum4(int row, int r) const {
+    v4f sum = *reinterpret_cast<const v4f*>(red + row * RW + r);
+#pragma unroll
+    for (int v = 1; v < kShrinkWaves; ++v) {
+      const v4f o = *reinterpret_cast<const v4f*>(red + (v * BM + row) * RW + r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] += o[j];
+    }
+    return sum;
+  }
+};
 
+template <int KIND, int RT, int NR, bool C_MAJOR>
+__device__ __forceinline__ void shrink_tile(const Dev& g, const uint16_t* __restrict__ X, const RowMap& xm, int C,
+                                            const uint16_t* __restrict__ W, const Tile& t, int rc, int slot, int slots,
+                                            ShrinkLds<RT, NR, C_MAJOR>& lds) {
+  constexpr int BM = 16 * RT, RW = 16 * NR + 4;
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint16_t* xp[RT];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -236,7 +250,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
 #pragma unroll
     for (int n = 0; n < NR; ++n) acc[rt][n] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = (C + 127) / 128, slot = sp * kShrinkWaves + wid, slots = splits * kShrinkWaves;
+  const int steps = (C + 127) / 128;
   const int st0 = (int)((int64_t)steps * slot / slots), st1 = (int)((int64_t)steps * (slot + 1) / slots);
   u32x4 xb[RT][4], wb[NR][4];
   // Columns past C repeat the last 8 of each operand, W's as zeros.
@@ -264,7 +278,7 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
     for (int i = 0; i < 4; ++i) {
       u32x4 wf[NR];
       if (C_MAJOR) {
-        uint16_t* tw = turn[wid];
+        uint16_t* tw = lds.turn[wid];
 #pragma unroll
         for (int n = 0; n < NR; ++n) *reinterpret_cast<u32x4*>(tw + (lane + 64 * n) * 8) = wv[n][i];
 #pragma unroll
@@ -301,24 +315,31 @@ __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uin
     multiply(xb, wb);
   }
 
-  // The waves' sums meet in LDS.
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int n = 0; n < NR; ++n)
-      *reinterpret_cast<v4f*>(red + (wid * BM + rt * 16 + c) * RW + n * 16 + 4 * q) = acc[rt][n];
+      *reinterpret_cast<v4f*>(lds.red + (wid * BM + rt * 16 + c) * RW + n * 16 + 4 * q) = acc[rt][n];
   __syncthreads();
+}
+
+// part[split][s][r]: one workgroup takes 16 RT rows of one group, 64 ranks at
+// most, and one split of the columns.
+template <int KIND, int RT, int NR, bool C_MAJOR>
+__global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm,
+                                                                int C, const uint16_t* __restrict__ W,
+                                                                float* __restrict__ part, int splits, int rchunks) {
+  constexpr int BM = 16 * RT;
+  __shared__ ShrinkLds<RT, NR, C_MAJOR> lds;
+  const int tid = threadIdx.x, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rc = blockIdx.x % rchunks, sp = blockIdx.x / rchunks % splits, w = blockIdx.x / rchunks / splits;
+  Tile t;
+  if (!find_tile(g, BM, w, t)) return;
+  shrink_tile<KIND>(g, X, xm, C, W, t, rc, sp * kShrinkWaves + wid, splits * kShrinkWaves, lds);
   for (int i = tid; i < BM * NR * 4; i += kShrinkThreads) {
     const int row = i / (NR * 4), r = (i - row * (NR * 4)) * 4;
     if (row >= t.rows || rc * 64 + r >= g.R || pair_of(g, t.row0 + row) < 0) continue;
-    v4f sum = *reinterpret_cast<v4f*>(red + row * RW + r);
-#pragma unroll
-    for (int v = 1; v < kShrinkWaves; ++v) {
-      const v4f o = *reinterpret_cast<v4f*>(red + (v * BM + row) * RW + r);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] += o[j];
-    }
-    *reinterpret_cast<v4f*>(part + ((int64_t)sp * g.P + t.row0 + row) * g.R + rc * 64 + r) = sum;
+    *reinterpret_cast<v4f*>(part + ((int64_t)sp * g.P + t.row0 + row) * g.R + rc * 64 + r) = lds.sum4(row, r);
   }
 }
 
@@ -462,6 +483,61 @@ struct ExpandArgs {
 
 __host__ __device__ constexpr int padded_rank(int R) { return (R + 31) / 32 * 32 + 8; }
 
+// Weights of columns n0 + 8c + j, ranks 32 oc + 8q .. +7 (TR: their rows, to be
+// turned by column_of); columns past C and ranks past R repeat the last ones
+// (for results not stored, times zeros).
+template <bool TR>
+__device__ __forceinline__ void load_weights(const ExpandArgs& a, int R, int e, int n0, int oc, u32x4 (&v)[8]) {
+  const int lane = threadIdx.x & 63, o = min(oc * 4 + (lane >> 4), R / 8 - 1), col = n0 + (lane & 15) * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (TR) v[i] = ld16(a.W + ((int64_t)e * R + o * 8 + i) * a.C + min(col, a.C - 8));
+    else v[i] = ld16(a.W + ((int64_t)e * a.C + min(col + i, a.C - 1)) * R + o * 8);
+  }
+}
+
+// The 16-bit parts of 8 ranks of one row, times 2^f (F16), to parts[p * stride].
+template <int KIND>
+__device__ __forceinline__ void put_parts(uint16_t* parts, int stride, const float v[8], int f) {
+  constexpr int NP = kParts<KIND>;
+  u32x4 pk[NP];
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    uint16_t lo[NP], hi[NP];
+    split<KIND>(KIND == OUT_F16 ? ldexp2(v[j], f) : v[j], lo);
+    split<KIND>(KIND == OUT_F16 ? ldexp2(v[j + 1], f) : v[j + 1], hi);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)lo[p] | ((u32)hi[p] << 16);
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(parts + p * stride) = pk[p];
+}
+
+// Row i of the lane's four: 8 columns, times 2^-f (F16), with the base.
+template <int KIND, bool NT>
+__device__ __forceinline__ void store_row(const v4f (&acc)[8], int i, int f, bool has_base, u32x4 base, uint16_t* out) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = KIND == OUT_F16 ? ldexp2(acc[j][i], -f) : acc[j][i];
+    if (has_base) {
+      const u32 b = base[j >> 1] >> (16 * (j & 1)) & 0xffffu;
+      v[j] += KIND == OUT_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32((uint16_t)b);
+    }
+  }
+  store8<KIND, NT>(out, 0, v);
+}
+
+// Pair-ordered rows without a group: base, or zeros.
+__device__ __forceinline__ void copy_rows_without(const Dev& g, const ExpandArgs& a, int wave, int waves) {
+  for (int p = wave; p < g.P; p += waves) {
+    const int s = a.p2s[p];
+    if (s >= 0 && s < g.P) continue;
+    for (int n = (threadIdx.x & 63) * 8; n < a.C; n += 512)
+      st16(a.out + (int64_t)p * a.C + n, a.base ? ld16(a.base + (int64_t)p * a.C + n) : u32x4{0, 0, 0, 0});
+  }
+}
+
 // out[o(s)][n] = base + sum_r (scale h[s][r]) W[e][n][r] for bm rows of one
 // group.  The rows' low-rank operand is split once into LDS (zero past R).
 // Each wave then takes 128 columns at a time, keeps their weights of OC x 32
@@ -480,13 +556,8 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
       split_tile<KIND>(g, a.sa, a.sb, a.tl, blockIdx.x - a.main_blocks);
       return;
     }
-    const int nw = (gridDim.x - a.main_blocks) * kExpandWaves;
-    for (int p = (blockIdx.x - a.main_blocks) * kExpandWaves + wid; p < g.P; p += nw) {
-      const int s = a.p2s[p];
-      if (s >= 0 && s < g.P) continue;
-      for (int n = lane * 8; n < a.C; n += 512)
-        st16(a.out + (int64_t)p * a.C + n, a.base ? ld16(a.base + (int64_t)p * a.C + n) : u32x4{0, 0, 0, 0});
-    }
+    copy_rows_without(g, a, (blockIdx.x - a.main_blocks) * kExpandWaves + wid,
+                      (gridDim.x - a.main_blocks) * kExpandWaves);
     return;
   }
   const int w = blockIdx.x / a.cblocks, cb = blockIdx.x - w * a.cblocks;
@@ -495,16 +566,7 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
 
   const bool has_base = !TR && a.base;  // dx has none
   const int octs = g.R / 8, RP = padded_rank(g.R), ochunks = (octs + 3) / 4;
-  // Weights of columns n0 + 8c + j, ranks 32 oc + 8q .. +7; columns past C and
-  // ranks past R repeat the last ones (for results not stored, times zeros).
-  const auto load_w = [&](int n0, int oc, u32x4 (&v)[8]) {
-    const int o = min(oc * 4 + q, octs - 1), col = n0 + c * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (TR) v[i] = ld16(a.W + ((int64_t)t.e * g.R + o * 8 + i) * a.C + min(col, a.C - 8));
-      else v[i] = ld16(a.W + ((int64_t)t.e * a.C + min(col + i, a.C - 1)) * g.R + o * 8);
-    }
-  };
+  const auto load_w = [&](int n0, int oc, u32x4 (&v)[8]) { load_weights<TR>(a, g.R, t.e, n0, oc, v); };
   const auto turn_w = [&](u32x4 (&v)[8]) {
     if (TR) {
       u32x4 r[8];
@@ -563,18 +625,9 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
     value(row, o, v);
     if (a.h && cb == 0 && o < octs && orow[row] >= 0)
       store8<OUT_F32, false>(a.h, (int64_t)(t.row0 + row) * g.R + o * 8, v);
-    const int f = KIND == OUT_F16 ? half_exp(__uint_as_float(rmax[row])) : 0;
-    u32x4 pk[NP];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint16_t lo[NP], hi[NP];
-      split<KIND>(KIND == OUT_F16 ? ldexp2(sc * v[j], f) : sc * v[j], lo);
-      split<KIND>(KIND == OUT_F16 ? ldexp2(sc * v[j + 1], f) : sc * v[j + 1], hi);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) pk[p][j / 2] = (u32)lo[p] | ((u32)hi[p] << 16);
-    }
-#pragma unroll
-    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4*>(parts + (p * a.bm + row) * RP + o * 8) = pk[p];
+    for (int j = 0; j < 8; ++j) v[j] *= sc;
+    put_parts<KIND>(parts + row * RP + o * 8, a.bm * RP, v, KIND == OUT_F16 ? half_exp(__uint_as_float(rmax[row])) : 0);
   }
   __syncthreads();
 
@@ -633,23 +686,102 @@ __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev 
           const int row = (rt + x) * 16 + 4 * q + i;
           const int o = rt + x < nrt ? orow[row] : -1;
           if (col >= a.C || o < 0) continue;
-          const int f = KIND == OUT_F16 ? -half_exp(__uint_as_float(rmax[row])) : 0;
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            v[j] = KIND == OUT_F16 ? ldexp2(acc[x][j][i], f) : acc[x][j][i];
-            if (has_base) {
-              const u32 b = bv[x][i][j >> 1] >> (16 * (j & 1)) & 0xffffu;
-              v[j] += KIND == OUT_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32((uint16_t)b);
-            }
-          }
-          store8<KIND, NT>(a.out, (int64_t)o * a.C + col, v);
+          store_row<KIND, NT>(acc[x], i, KIND == OUT_F16 ? half_exp(__uint_as_float(rmax[row])) : 0, has_base, bv[x][i],
+                              a.out + (int64_t)o * a.C + col);
         }
 #pragma unroll
       for (int x = 0; x < RTI; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) bv[x][i] = bn[x][i];
     }
+  }
+}
+
+// ------------------------------------------------------------------- small
+constexpr int kSmallCols = 128 * kShrinkWaves;
+
+// Shrink and expand in one launch, for few rows: one workgroup takes 16 rows of
+// one group and 1024 columns of the output, and computes the rows' low-rank
+// values for itself.  The column blocks of a tile repeat that, which costs
+// less than a second launch and its trip through memory while A is short.
+template <int KIND, int NR>
+__global__ __launch_bounds__(kShrinkThreads) void small_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm, int K,
+                                                               const uint16_t* __restrict__ A, ExpandArgs a) {
+  constexpr int NP = kParts<KIND>, OC = (NR + 1) / 2, LANES = 4 * OC, RP = 32 * OC + 8;
+  __shared__ ShrinkLds<1, NR, false> lds;
+  __shared__ __align__(16) uint16_t parts[NP * 16 * RP];
+  __shared__ int orow[16], rexp[16];
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
+  if ((int)blockIdx.x >= a.main_blocks) {
+    copy_rows_without(g, a, (blockIdx.x - a.main_blocks) * kShrinkWaves + wid,
+                      (gridDim.x - a.main_blocks) * kShrinkWaves);
+    return;
+  }
+  const int w = blockIdx.x / a.cblocks, cb = blockIdx.x - w * a.cblocks;
+  Tile t;
+  if (!find_tile(g, 16, w, t)) return;
+  const int n0 = (cb * kShrinkWaves + wid) * 128, col = n0 + c * 8;
+  u32x4 wr[OC][8];
+#pragma unroll
+  for (int oc = 0; oc < OC; ++oc) load_weights<false>(a, g.R, t.e, n0, oc, wr[oc]);
+  if (tid < 16) {
+    const int pair = tid < t.rows ? pair_of(g, t.row0 + tid) : -1;
+    orow[tid] = pair < 0 ? -1 : (a.out_pair ? pair : t.row0 + tid);
+  }
+  shrink_tile<KIND>(g, X, xm, K, A, t, 0, wid, kShrinkWaves, lds);
+  if (tid < 16 * LANES) {  // 8 ranks of one row; a row's lanes are neighbours
+    const int row = tid / LANES, o = tid % LANES;
+    float v[8], m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    if (o * 8 < g.R && orow[row] >= 0) {
+      const v4f x = lds.sum4(row, o * 8), y = lds.sum4(row, o * 8 + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = x[j];
+        v[4 + j] = y[j];
+      }
+      if (a.h && cb == 0) store8<OUT_F32, false>(a.h, (int64_t)(t.row0 + row) * g.R + o * 8, v);
+    }
+    const float sc = scale_of(g, t.e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] *= sc;
+      const float u = __builtin_fabsf(v[j]);
+      m = u < __builtin_inff() ? fmaxf(m, u) : m;
+    }
+#pragma unroll
+    for (int x = 1; x < LANES; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
+    const int f = KIND == OUT_F16 ? half_exp(m) : 0;
+    if (o == 0) rexp[row] = f;
+    put_parts<KIND>(parts + row * RP + o * 8, 16 * RP, v, f);
+  }
+  __syncthreads();
+  if (n0 >= a.C) return;
+  u32x4 bv[4];
+  if (a.base) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bv[i] = ld16(a.base + (int64_t)max(orow[4 * q + i], 0) * a.C + min(col, a.C - 8));
+  }
+  v4f acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int oc = 0; oc < OC; ++oc)
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const u32x4 l = *reinterpret_cast<u32x4*>(parts + (p * 16 + c) * RP + (oc * 4 + q) * 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = mfma16<KIND>(l, wr[oc][j], acc[j]);
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int o = orow[4 * q + i];
+    if (col < a.C && o >= 0)
+      store_row<KIND, false>(acc, i, KIND == OUT_F16 ? rexp[4 * q + i] : 0, a.base != nullptr, bv[i],
+                             a.out + (int64_t)o * a.C + col);
   }
 }
 
@@ -1001,15 +1133,44 @@ hipError_t outer(const Dev& d, const Side& sa, const Side& sb, const Tiles& tl, 
   return hipGetLastError();
 }
 
+// Whether a call takes one launch (small_kernel).  Against the two kernels, in
+// graphs, one row to 200: A of 16 KB a group 6.1 - 7.7 us for 8.8 - 10.9, of
+// 64 KB 8.2 - 8.4 for 10.5 - 10.9, of 128 KB 9.8 - 11.2 for 9.9 - 11.0 (and a
+// launch less for the host), of 224 KB 13.0 - 19.1 for 10.8 - 13.7; with more
+// workgroups than CUs 16.8 for 14.4.
+bool one_launch(int64_t P, int E, int N, int K, int R) {
+  return R <= 64 && max_tiles(P, E, 16) * ((N + kSmallCols - 1) / kSmallCols) <= 256 &&
+         (int64_t)rank_tiles(R) * 16 * K <= 65536;
+}
+
+template <int KIND>
+hipError_t small(const Dev& d, const uint16_t* x, RowMap xm, int K, const uint16_t* A, ExpandArgs a, bool copy,
+                 hipStream_t stream) {
+  a.cblocks = (a.C + kSmallCols - 1) / kSmallCols;
+  a.main_blocks = (int)(max_tiles(d.P, d.E, 16) * a.cblocks);
+  const dim3 grid(a.main_blocks + (copy ? (d.P + kShrinkWaves - 1) / kShrinkWaves : 0)), block(kShrinkThreads);
+  switch (rank_tiles(d.R)) {
+    case 1: hipLaunchKernelGGL((small_kernel<KIND, 1>), grid, block, 0, stream, d, x, xm, K, A, a); break;
+    case 2: hipLaunchKernelGGL((small_kernel<KIND, 2>), grid, block, 0, stream, d, x, xm, K, A, a); break;
+    default: hipLaunchKernelGGL((small_kernel<KIND, 4>), grid, block, 0, stream, d, x, xm, K, A, a); break;
+  }
+  return hipGetLastError();
+}
+
 template <int KIND>
 hipError_t forward(const LoraArgs& g, const uint16_t* x, const uint16_t* a, const uint16_t* b, const uint16_t* base,
                    uint16_t* out, float* h, float* ws, hipStream_t stream) {
   const Dev d = dev_args(g);
+  const bool copy = g.out_pair && base != out;
+  if (one_launch(g.P, g.E, g.N, g.K, g.R)) {
+    const ExpandArgs ea = {nullptr, 0, h, b, g.N, base, out, g.out_pair, 0, 0, 0, 0, g.p2s};
+    return small<KIND>(d, x, x_map(g), g.K, a, ea, copy, stream);
+  }
   const int splits = shrink_splits(g.P, g.E, g.K, g.R);
   float* part = splits == 1 && h ? h : ws;
   hipError_t e = shrink<KIND, false>(d, x, x_map(g), g.K, a, part, splits, stream);
   if (e != hipSuccess) return e;
-  const int copies = g.out_pair && base != out ? std::min((d.P + kExpandWaves - 1) / kExpandWaves, 1024) : 0;
+  const int copies = copy ? std::min((d.P + kExpandWaves - 1) / kExpandWaves, 1024) : 0;
   ExpandArgs ea = {part, splits, part == h ? nullptr : h, b, g.N, base, out, g.out_pair, 0, 0, 0, 0, g.p2s};
   return expand<KIND, false>(d, ea, copies, g.P * g.N * (base ? 4 : 2), stream);
 }
