@@ -17,14 +17,15 @@
 // wave.  shrink keeps the plain order, 64 contiguous bytes of each of 16 rows
 // in an access: with a lane's 64 bytes in a row (and so 16-byte pieces 64
 // bytes apart in an access) the L1 saw 45 lookups per access and not 16, and
-// dh of 256 experts took 167 us, not 100.
+// dh of 256 experts under Zipf routing took 167 us, not 145.
 //
 // The low-rank operand (h, dh) is fp32.  It enters the MFMAs as a sum of
 // 16-bit parts that carries all its 24 bits: three of bf16 (8 bits each), or
 // two of binary16 (11 each and the sign between) after scaling by a power of
-// two to the middle of binary16's range (per row in expand; per wave, raised
-// when a step outgrows it, in outer).  A single 16-bit rounding would have put
-// its 2^-9 (2^-12) error into every product; the extra MFMAs are free here.
+// two to the middle of binary16's range (per row in expand; per tile of 32 rows
+// in outer, whose sums move to the smaller scale where the tiles' differ).  A
+// single 16-bit rounding would have put its 2^-9 (2^-12) error into every
+// product; the extra MFMAs are free here.
 #include <algorithm>
 
 #include "common.h"
@@ -372,10 +373,13 @@ struct Side {
   int blocks;          // kOuterWaves * kOuterCols columns each
 };
 
-// Exponent of a 32-row tile's scale, a multiple of 16 so that neighbours
-// rarely differ: brings m to [2^-2, 2^14).
+// Exponent of a 32-row tile's scale, a multiple of 4 so that neighbours often
+// agree: brings m (finite, >= 0) to [2^10, 2^14), so that the parts resolve
+// 2^-35 of the tile's largest value.  (Multiples of 16 left 2^-23 where m came
+// out lowest: ranks 2^-20 below the others came out wrong.)
+constexpr int kMaxTileExp = 136;
 __device__ __forceinline__ int tile_exp(float m) {
-  return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~15) - 128;
+  return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~3) - 128;
 }
 
 // One workgroup of 256 threads: one side of one tile.
@@ -874,7 +878,7 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
     }
   };
   static_assert(kOuterDepth == 3, "rows are copied for tiles up to k + 4 while tile k is at work");
-  int f = 128;  // F16: exponent of the scale of the sums, the largest while they are zero
+  int f = kMaxTileExp;  // F16: exponent of the scale of the sums
   const auto step = [&](int k, u32x2 (&x8)[8]) {
     if ((k & 1) == 0) {
       // The pair's fragments, and the rows of pair k + 4, were copied before
@@ -896,7 +900,7 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
     int down = 0;
     if (KIND == OUT_F16 && te != kNoRows) {
       // The sums keep the smallest scale so far; a tile with a larger one is
-      // brought down to it (what that drops is below 2^-22 of the largest).
+      // brought down to it, to the same 2^-35 of the largest value.
       if (te < f) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
@@ -908,6 +912,8 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
       }
       down = f - te;
     }
+    // 2^down as a product of nonzero factors, so that infinities stay.
+    const _Float16 down1 = (_Float16)ldexp2(1.f, max(down, -14)), down2 = (_Float16)ldexp2(1.f, max(down + 14, -24));
     u32x4 x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = column_of(x8, j);
@@ -917,8 +923,11 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         u32x4 a = ld16(&ring[(k >> 1) & 1][k & 1][p * NR + n][lane * 8]);
-        if (KIND == OUT_F16 && down)
-          a = __builtin_bit_cast(u32x4, __builtin_bit_cast(v8h, a) * (_Float16)ldexp2(1.f, down));
+        if (KIND == OUT_F16 && down) {
+          v8h v = __builtin_bit_cast(v8h, a) * down1;
+          if (down < -14) v = v * down2;
+          a = __builtin_bit_cast(u32x4, v);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][j] = mfma16<KIND>(a, x[j], acc[n][j]);
       }

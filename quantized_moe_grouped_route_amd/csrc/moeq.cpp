@@ -472,13 +472,15 @@ moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_a
   if ((base != out && overlap(out, ob, base, ob)) || overlap(out, ob, x, rows_x * K * 2) ||
       overlap(out, ob, a, E * K * R * 2) || overlap(out, ob, b, E * N * R * 2))
     return fail(MOEQ_EINVAL, "%s: out overlaps an input (base may be out itself)", fn);
-  if (overlap(h, hb, out, ob) || overlap(h, hb, base, ob) || overlap(h, hb, x, rows_x * K * 2))
+  if (overlap(h, hb, out, ob) || overlap(h, hb, base, ob) || overlap(h, hb, x, rows_x * K * 2) ||
+      overlap(h, hb, a, E * K * R * 2) || overlap(h, hb, b, E * N * R * 2))
     return fail(MOEQ_EINVAL, "%s: h overlaps another argument", fn);
   const size_t need = moeq::lora_workspace_bytes(P, E, (int)N, (int)K, R);
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
   if (overlap(workspace, (int64_t)need, out, ob) || overlap(workspace, (int64_t)need, base, ob) ||
-      overlap(workspace, (int64_t)need, x, rows_x * K * 2) || overlap(workspace, (int64_t)need, h, hb))
+      overlap(workspace, (int64_t)need, x, rows_x * K * 2) || overlap(workspace, (int64_t)need, h, hb) ||
+      overlap(workspace, (int64_t)need, a, E * K * R * 2) || overlap(workspace, (int64_t)need, b, E * N * R * 2))
     return fail(MOEQ_EINVAL, "%s: workspace overlaps another argument", fn);
   const moeq::LoraArgs g = lora_args(dtype, a_row, scale, expert_offsets, sorted_pair_ids, pair_to_sorted, P, topk, E,
                                      N, K, R, out_row);

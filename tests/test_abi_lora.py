@@ -108,6 +108,8 @@ LORA_SHARED = [
     (dict(h=at(9) + 4), mq.EALIGN), (dict(orow=1), mq.EINVAL), (dict(orow=1, base=None), mq.EINVAL),
     (dict(out=at(0)), mq.EINVAL), (dict(out=at(6) + 16), mq.EINVAL), (dict(out=at(1)), mq.EINVAL),
     (dict(h=at(7)), mq.EINVAL), (dict(ws=at(7)), mq.EINVAL), (dict(h=at(8)), mq.EINVAL),
+    (dict(h=at(1)), mq.EINVAL), (dict(h=at(2) + 16), mq.EINVAL), (dict(ws=at(1)), mq.EINVAL),
+    (dict(ws=at(2)), mq.EINVAL),
 ])
 def test_lora_rejects(L, kw, status):
     assert _lora(L, **kw) == status
@@ -135,6 +137,20 @@ BWD_AT = dict(x=at(1) + 8, a=at(2) + 2, b=at(3) + 4, sc=at(4) + 2)
 ])
 def test_lora_backward_rejects(L, kw, status):
     assert _lora_bwd(L, **kw) == status
+
+
+# More workgroups than one launch holds: rows, columns and ranks near their
+# limits together; fewer rows of the same are taken.
+@pytest.mark.parametrize("P,E,N,K,R", [(2 ** 31 - 1, 1, 2 ** 20, 8, 256), (2 ** 30, 1, 64, 2 ** 20, 256)])
+def test_lora_refuses_what_one_launch_cannot_hold(L, P, E, N, K, R):
+    kw = dict(P=P, E=E, N=N, K=K, R=R, rows=P, arow=1, topk=1, wsb=1 << 62)
+    assert _lora(L, **kw) == mq.EINVAL
+    assert b"too large for one launch" in L.moeq_last_error()
+    assert _lora_bwd(L, **kw) == mq.EINVAL
+    assert b"too large for one launch" in L.moeq_last_error()
+    for f in (L.grouped_lora_workspace_bytes, L.grouped_lora_backward_workspace_bytes):
+        assert f(P, E, N, K, R) == 0
+        assert f(P >> 12, E, N, K, R) > 0
 
 
 def test_lora_workspace_sizes_of_refused_arguments_are_zero(L):
