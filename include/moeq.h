@@ -461,8 +461,9 @@ moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype
  * N, K <= 2^20, 1 <= E <= 1024, P < 2^31, 1 <= topk <= 64, rows_x * topk >= P
  * (TOKEN) or rows_x >= P (SORTED), 16-byte aligned pointers (4-byte for the
  * int32 tables and scale), and out, h and workspace disjoint from each other
- * and the inputs (else MOEQ_EINVAL).  The workspace size of arguments
- * outside these ranges is 0.
+ * and the inputs (else MOEQ_EINVAL).  Sizes near these limits together, which
+ * one launch cannot hold, are MOEQ_EINVAL too.  The workspace size of
+ * arguments outside these ranges is 0.
  * ---------------------------------------------------------------------- */
 size_t grouped_lora_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R); /* host */
 
@@ -479,6 +480,7 @@ moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_a
  *   da[e]    = sum_{s of e} dh[s]^T x[row]       [R][K]
  *   db[e]    = scale[e] * sum_{s of e} dy[o]^T h[s]   [N][R]
  * sums in fp32, one rounding, in a fixed order: equal inputs give equal bits.
+ * In F16, dh and h enter da and db with 2^-35 of their group's largest value.
  *
  *   dy   [P][N] in out_row's order; x, a, b, scale and the tables as in the
  *        forward call; h f32 [P][R] as it wrote it

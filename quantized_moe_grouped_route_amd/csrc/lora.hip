@@ -326,6 +326,10 @@ __device__ __forceinline__ void shrink_tile(const Dev& g, const uint16_t* __rest
 
 // part[split][s][r]: one workgroup takes 16 RT rows of one group, 64 ranks at
 // most, and one split of the columns.
+// Bound by its one read of X with what it has in flight.  dh of 32768 bf16
+// rows of 7168, 256 experts under Zipf routing, rank 16: 124 us, 0.53 GB, 4.3
+// TB/s; h of 16384 f16 rows of 4096 from 8192 tokens, 8 experts: 40 - 44 us.
+// 4 waves or 8, 1, 2 or 4 row tiles, 1 split or 2 are within 2 % there.
 template <int KIND, int RT, int NR, bool C_MAJOR>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm,
                                                                 int C, const uint16_t* __restrict__ W,
@@ -547,6 +551,9 @@ __device__ __forceinline__ void copy_rows_without(const Dev& g, const ExpandArgs
 // Each wave then takes 128 columns at a time, keeps their weights of OC x 32
 // ranks in registers and walks the rows 16 at a time, the next rows' base in
 // flight; OC = 0 takes any rank, reloading the weights for every 32 rows.
+// Bound by base and out: 16384 f16 rows of 28672 at rank 16, 1.88 GB, 341 us,
+// 5.5 TB/s.  dx with the outer kernel's tiles: 16384 f16 rows of 14336 at rank
+// 64 97 - 113 us (0.47 GB written), 32768 bf16 rows of 2048 47 us.
 template <int KIND, int OC, bool TR, bool NT>
 __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev g, ExpandArgs a) {
   constexpr int NP = kParts<KIND>, RTI = OC ? 1 : 2;
@@ -708,6 +715,9 @@ constexpr int kSmallCols = 128 * kShrinkWaves;
 // one group and 1024 columns of the output, and computes the rows' low-rank
 // values for itself.  The column blocks of a tile repeat that, which costs
 // less than a second launch and its trip through memory while A is short.
+// Bound by its chain of trips to memory (offsets, pairs, x and A, B) and one
+// compute unit's loads of A: one row, K = N = 4096, rank 16, 10.0 us (two
+// launches 4.6 + 6.8 us); K = N = 1024, rank 8, 6.1 us in a graph for 8.8.
 template <int KIND, int NR>
 __global__ __launch_bounds__(kShrinkThreads) void small_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm, int K,
                                                                const uint16_t* __restrict__ A, ExpandArgs a) {
@@ -819,6 +829,10 @@ __host__ __device__ constexpr int64_t outer_slots(int64_t P, int chunk) {
 // ahead: a row or an exponent that came through a register would be the newest
 // load when it is needed, and waiting for it would be waiting for everything
 // in flight.
+// Bound by its one read of both wide operands, 0.60 GB each: bf16 rows of 7168
+// and 2048, 256 experts under Zipf routing, rank 16, 137 us, 4.4 TB/s; f16 rows
+// of 4096 and 14336, 8 experts, rank 64, 136 - 147 us.  Two tiles in flight,
+// double buffers for the MFMA operands, or 128 columns a wave were no faster.
 template <int KIND, int NR>
 __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa, Side sb, Tiles tl, int rchunks,
                                                                  int chunk) {
@@ -978,6 +992,7 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
 
 // Joins the chunks of the groups longer than one: a thread takes 4 ranks of
 // one column, so that both output orders store 4 values at once or in runs.
+// 13 us (256 experts, most of them whole) and 5 us (8 experts) after the above.
 template <int KIND>
 __global__ __launch_bounds__(256) void join_kernel(Dev g, Side sa, Side sb, int blocks_a, int blocks_b,
                                                   int chunk) {
@@ -1020,8 +1035,9 @@ int64_t max_tiles(int64_t P, int E, int bm) { return P / bm + std::min<int64_t>(
 int shrink_rt(int64_t P, int E, int nr) { return P >= 24 * (int64_t)E ? 2 : 1; }
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }  // per workgroup; 64 ranks at most
 
-// Rows of an expand workgroup: about the average group's; their split operand
-// has to leave LDS for three workgroups on a compute unit.
+// Rows of an expand workgroup: about the average group's, up to 64 (beside the
+// Mixtral-sized gate+up projection 128 rows took 405 us for 387); their split
+// operand has to leave LDS for three workgroups on a compute unit.
 int expand_rows(int64_t P, int E, int R, int f16) {
   int bm = kExpandRows;
   while (bm > 16 && ((f16 ? 2 : 3) * bm * padded_rank(R) * 2 > 52 * 1024 || P < bm * (int64_t)E)) bm /= 2;
@@ -1029,7 +1045,8 @@ int expand_rows(int64_t P, int E, int R, int f16) {
 }
 
 // 512-column blocks an expand workgroup walks: up to 2 while 2048 workgroups
-// remain, more where one grid could not hold the workgroups.
+// remain (there 4 blocks took 414 us for 387), more where one grid could not
+// hold the workgroups.
 int expand_iters(int64_t tiles, int blocks) {
   int iters = (int)std::max<int64_t>(1, std::min<int64_t>(2, tiles * blocks / 2048));
   while (iters < blocks && tiles * ((blocks + iters - 1) / iters) > kMaxBlocks) iters *= 2;

@@ -60,8 +60,12 @@ CASES = [  # T, k, E, N, kind, skip
     (37, 3, 5, 1000, "repeat", 0.3),
     (64, 2, 4, 256, "none", 0.0),
     (130, 4, 7, 2056, "one", 0.0),
-    (1023, 2, 8, 4096, "distinct", 0.0),       # one pair tile short of the all-slots form
-    (1025, 3, 37, 512, "repeat", 0.2),         # all slots of a token in one workgroup
+    (255, 8, 16, 1032, "repeat", 0.1),         # around one workgroup of tokens per compute unit,
+    (257, 8, 16, 1032, "repeat", 0.1),         # where all slots of a token move to one
+    (511, 5, 16, 2048, "distinct", 0.1),       # and around two
+    (513, 5, 16, 2048, "distinct", 0.1),
+    (1023, 2, 8, 4096, "distinct", 0.0),
+    (1025, 3, 37, 512, "repeat", 0.2),
     (9, 2, 4, 20000, "distinct", 0.1),
 ]
 
