@@ -452,8 +452,8 @@ moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype
  *   pair_to_sorted  int32 [P] (else NULL, not read)
  *   h      NULL, or f32 [P][R] that receives h (rows past expert_offsets[E]
  *          not written): what grouped_lora_backward reads
- *   workspace  grouped_lora_workspace_bytes(P, E, N, K, R) bytes, contents
- *          on entry ignored.  Calls that may overlap in time need their own.
+ *   workspace  grouped_lora_workspace_bytes(P, E, N, K, R) bytes (0 for few
+ *          rows and a short A: NULL will do), contents on entry ignored.  Calls that may overlap in time need their own.
  * A group's rank may be below R: pad its A and B with zeros.  An infinity or
  * NaN in an operand makes the outputs it enters infinite or NaN, without
  * promise which of the two.

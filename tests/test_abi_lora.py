@@ -79,8 +79,9 @@ def test_combine_backward_rejects(L, kw, status):
 
 
 def _lora(L, **kw):
+    # (K long enough to need a workspace)
     a = dict(x=at(0), dt=mq.BF16, rows=8, arow=0, a=at(1), b=at(2), sc=at(3), off=at(4), srt=at(5), p2s=None, P=16,
-             topk=2, E=4, N=64, K=128, R=16, base=at(6), orow=0, out=at(7), h=None, ws=at(8), wsb=1 << 30)
+             topk=2, E=4, N=64, K=8192, R=16, base=at(6), orow=0, out=at(7), h=None, ws=at(8), wsb=1 << 30)
     a.update(kw)
     return L.grouped_lora(a["x"], a["dt"], a["rows"], a["arow"], a["a"], a["b"], a["sc"], a["off"], a["srt"],
                           a["p2s"], a["P"], a["topk"], a["E"], a["N"], a["K"], a["R"], a["base"], a["orow"],
@@ -153,9 +154,16 @@ def test_lora_refuses_what_one_launch_cannot_hold(L, P, E, N, K, R):
         assert f(P >> 12, E, N, K, R) > 0
 
 
+def test_lora_of_few_rows_needs_no_workspace(L):
+    assert L.grouped_lora_workspace_bytes(16, 4, 64, 128, 16) == 0
+    assert _lora(L, K=128, ws=None, wsb=0, out=None) == mq.EINVAL      # refused for out, not for the workspace
+    assert b"null pointer" in L.moeq_last_error()
+    assert L.grouped_lora_backward_workspace_bytes(16, 4, 64, 128, 16) > 0
+
+
 def test_lora_workspace_sizes_of_refused_arguments_are_zero(L):
     for f in (L.grouped_lora_workspace_bytes, L.grouped_lora_backward_workspace_bytes):
-        assert f(16, 4, 64, 128, 16) > 0
+        assert f(16, 4, 64, 8192, 16) > 0
         for bad in ((-1, 4, 64, 128, 16), (2 ** 31, 4, 64, 128, 16), (16, 0, 64, 128, 16), (16, 1025, 64, 128, 16),
                     (16, 4, 60, 128, 16), (16, 4, 64, 100, 16), (16, 4, 64, 128, 12), (16, 4, 64, 128, 264),
                     (16, 4, 2 ** 20 + 8, 128, 16)):
