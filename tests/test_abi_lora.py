@@ -240,8 +240,8 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     t = torch.zeros(4).as_subclass(Fake)
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0, raising=False)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     with pytest.raises(ValueError, match="y is on cuda:1"):
         mq._here("x y", None, t)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     mq._here("y absent", t, None)
