@@ -470,7 +470,9 @@ def nvfp4_repack(w, sf_swizzled, *, swap_halves: bool, sf_layout="rows", w_layou
     return w_out, sf_out
 
 
-_FLOATS = (torch.float16, torch.bfloat16, torch.float32)
+_HALVES = (torch.float16, torch.bfloat16)
+_FLOATS = (*_HALVES, torch.float32)
+_ROWS = (*_FLOATS, torch.uint8)
 
 
 def _pairs(pair_to_sorted, topk):
@@ -497,7 +499,7 @@ def moe_permute(x, pair_to_sorted, topk: int, *, out=None):
     """Token rows x [T][N] (f16, bf16, f32, or uint8 codes) copied to rows
     sorted by expert: out[pair_to_sorted[t*topk+j]] = x[t].  Returns out
     [T*topk][N]; rows past expert_offsets[E] are not written."""
-    _need(x, "x", (torch.float16, torch.bfloat16, torch.float32, torch.uint8), 2)
+    _need(x, "x", _ROWS, 2)
     T = _pairs(pair_to_sorted, topk)
     rows, N = x.shape
     if rows != T:
@@ -561,7 +563,7 @@ def lora_workspace_bytes(P: int, E: int, N: int, K: int, R: int, *, backward=Fal
 
 
 def _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids):
-    _need(x, "x", (torch.float16, torch.bfloat16), 2)
+    _need(x, "x", _HALVES, 2)
     dt = x.dtype
     _need(a, "a", dt, 3)
     _need(b, "b", dt, 3)
