@@ -559,3 +559,38 @@ def test_offsets_that_reach_past_the_rows_are_clamped():
     ref = p.oracle()
     out = p.forward(pair_to_sorted=None)
     close(host(out), ref["out"], ref["mag"], F16, p.len, "out")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_very_long_groups_of_short_rows(dtype):
+    """Hundreds of chunks a group, joined in order; a group between them and
+    the last one without rows."""
+    rng = np.random.default_rng(56)
+    P, N, K, R = 700_000, 16, 8, 8
+    off = np.array([0, 250_001, 250_001, 699_990, 699_990], np.int32)
+    x, dy = values(rng, (P, K), dtype), values(rng, (P, N), dtype, 0.1)
+    a, b = values(rng, (4, R, K), dtype, 0.3), values(rng, (4, N, R), dtype, 0.3)
+    h = torch.zeros(P, R, device="cuda")
+    out = torch.full((P, N), 7.0, dtype=dtype, device="cuda")
+    mq.grouped_lora(x, a, b, dev(off), None, 1, a_row="sorted", out=out, h=h)
+    ref = oracle.grouped_lora(host(x), host(a), host(b), off, None, 1, a_row="sorted", P=P)
+    n = int(off[-1])
+    close(host(out)[:n], ref["out"][:n], ref["mag"][:n], dtype, (K, N, R), "out")
+    assert np.all(host(out)[n:] == 7)
+    dx, da, db = mq.grouped_lora_backward(dy, x, a, b, h, dev(off), None, 1, a_row="sorted",
+                                          dx=torch.full((P, K), 7.0, dtype=dtype, device="cuda"))
+    g = oracle.grouped_lora_backward(host(dy), host(x), host(a), host(b), host(h), off, None, 1, a_row="sorted")
+    close(host(dx)[:n], g["dx"][:n], g["mdx"][:n], dtype, (K, N, R), "dx")
+    assert np.all(host(dx)[n:] == 7)
+    close(host(da), g["da"], g["mda"], dtype, (K, N, R, P), "da")
+    close(host(db), g["db"], g["mdb"], dtype, (K, N, R, P), "db")
+
+
+def test_two_launch_forward_captured_and_replayed():
+    from tests.test_gpu_graphs import _capture_and_replay
+    p = Problem(57, 300, 2, 8, 1032, 5000, 40, BF16, out_row="pair", kind="repeat", skip=0.2)
+    out, h = torch.zeros(p.P, p.N, dtype=BF16, device="cuda"), torch.zeros(p.P, p.R, device="cuda")
+    need = mq.lora_workspace_bytes(p.P, p.E, p.N, p.K, p.R)
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    _capture_and_replay(lambda: p.forward(out=out, h=h, workspace=ws), [out, h])

@@ -189,3 +189,31 @@ def test_offsets_past_32_bits():
     assert torch.equal(dy[-1], (x[t].float() * w.view(-1)[last]).to(BF16))
     ref = x[t].double().square().sum()
     assert abs(float(dw.view(-1)[last] - ref)) <= (N / 256 + 16) * 2.0 ** -24 * float(ref)
+
+
+def test_more_tokens_than_one_grid_holds():
+    """Past 2^23 workgroups every call goes out in runs of tokens; rows are
+    powers of two, so every result is exact."""
+    T, k, N = 2 ** 23 + 77, 2, 8
+    P = T * k
+    g = torch.Generator(device="cuda").manual_seed(55)
+    p2s = torch.randperm(P, generator=g, device="cuda").int()
+    p2s[torch.arange(0, P, 5, device="cuda")] = -1
+    pairs = (p2s >= 0).nonzero().view(-1)
+    s, t = p2s[pairs].long(), torch.div(pairs, k, rounding_mode="floor")
+    two = lambda *shape: torch.randint(-3, 4, shape, generator=g, device="cuda").float().exp2()
+    x, w, y = two(T, N).to(F16), two(T, k), two(P, N).to(F16)
+    xs = torch.full((P, N), 7.0, dtype=F16, device="cuda")
+    want = xs.clone()
+    want[s] = x[t]
+    assert torch.equal(mq.moe_permute(x, p2s, k, out=xs), want)
+    both = torch.where((p2s >= 0)[:, None], y[p2s.clamp(min=0).long()], 0).view(T, k, N)
+    assert torch.equal(mq.moe_permute_backward(y, p2s, k), both[:, 0] + both[:, 1])
+    wide = both.float() * w[:, :, None]
+    assert torch.equal(mq.moe_scatter_combine(y, p2s, w, out_dtype=F32),
+                       wide[:, 0] + wide[:, 1])
+    dy, dw = mq.moe_scatter_combine_backward(x, y, p2s, w, dy=torch.full_like(y, 7.0))
+    want.fill_(7.0)
+    want[s] = (x[t].float() * w.view(-1)[pairs, None]).to(F16)
+    assert torch.equal(dy, want)
+    assert torch.equal(dw, (both.float() * x[:, None].float()).sum(2))
