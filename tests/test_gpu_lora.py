@@ -593,4 +593,5 @@ def test_two_launch_forward_captured_and_replayed():
     need = mq.lora_workspace_bytes(p.P, p.E, p.N, p.K, p.R)
     assert need > 0
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
-    _capture_and_replay(lambda: p.forward(out=out, h=h, workspace=ws), [out, h])
+    # (rows of h without a group are not written)
+    _capture_and_replay(lambda: p.forward(out=out, h=h, workspace=ws), [out, h[:p.n]])
