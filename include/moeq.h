@@ -439,7 +439,8 @@ moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype
  * group e, with p = sorted_pair_ids[s]:
  *   h[s][:]   = x[row][:] . A[e]^T            row = p / topk (TOKEN), s (SORTED)
  *   out[o][:] = base[o][:] + scale[e] * h[s][:] . B[e]^T      o = s or p
- * h is kept in fp32; sums in fp32; one rounding to the element type.
+ * h is kept in fp32; sums in fp32; one rounding to the element type.  In F16,
+ * scale * h enters out with 2^-33 of its row's largest value.
  *
  *   dtype  F16 | BF16: the type of x, a, b, base and out
  *   x      [rows_x][K];  a [E][R][K];  b [E][N][R];  scale f32 [E] or NULL (1)
