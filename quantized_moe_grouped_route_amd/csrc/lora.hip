@@ -23,9 +23,9 @@
 // 16-bit parts that carries all its 24 bits: three of bf16 (8 bits each), or
 // two of binary16 (11 each and the sign between) after scaling by a power of
 // two to the middle of binary16's range (per row in expand; per tile of 32 rows
-// in outer, whose sums move to the smaller scale where the tiles' differ).  A
-// single 16-bit rounding would have put its 2^-9 (2^-12) error into every
-// product; the extra MFMAs are free here.
+// in outer, whose sums move to the scale of the tile at work).  A single 16-bit
+// rounding would have put its 2^-9 (2^-12) error into every product; the extra
+// MFMAs are free here.
 #include <algorithm>
 
 #include "common.h"
@@ -382,6 +382,7 @@ struct Side {
 // 2^-35 of the tile's largest value.  (Multiples of 16 left 2^-23 where m came
 // out lowest: ranks 2^-20 below the others came out wrong.)
 constexpr int kMaxTileExp = 136;
+constexpr int kMaxSpread = 80;  // of the exponents among which outer's sums move
 __device__ __forceinline__ int tile_exp(float m) {
   return ((13 + 127 - max(1, __float_as_int(m) >> 23) + 128) & ~3) - 128;
 }
@@ -892,7 +893,7 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
     }
   };
   static_assert(kOuterDepth == 3, "rows are copied for tiles up to k + 4 while tile k is at work");
-  int f = kMaxTileExp;  // F16: exponent of the scale of the sums
+  int f = kMaxTileExp, low = f;  // F16: exponent of the scale of the sums, the smallest so far
   const auto step = [&](int k, u32x2 (&x8)[8]) {
     if ((k & 1) == 0) {
       // The pair's fragments, and the rows of pair k + 4, were copied before
@@ -911,11 +912,18 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
 #pragma unroll
       for (int i = 0; i < 8; ++i) x8[i] = u32x2{0, 0};
     }
-    int down = 0;
+    bool lost = false;
     if (KIND == OUT_F16 && te != kNoRows) {
-      // The sums keep the smallest scale so far; a tile with a larger one is
-      // brought down to it, to the same 2^-35 of the largest value.
-      if (te < f) {
+      // The sums move to the tile's scale, in fp32 and so without loss.  At the
+      // smallest scale so far they are below 2^43 (2^14, times x's 2^16, times
+      // 6144 rows), so 2^kMaxSpread above it they cannot overflow.  A tile past
+      // that, all below 2^-80 of the largest value so far, is dropped but for
+      // its infinities and NaN.  (Fragments brought down to the smaller scale
+      // in binary16 stopped at its lowest step, 2^-34 of the largest value,
+      // however small they were.)
+      low = min(low, te);
+      lost = te - low > kMaxSpread;
+      if (!lost && te != f) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -924,10 +932,7 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
             for (int i = 0; i < 4; ++i) acc[n][j][i] = ldexp2(acc[n][j][i], te - f);
         f = te;
       }
-      down = f - te;
     }
-    // 2^down as a product of nonzero factors, so that infinities stay.
-    const _Float16 down1 = (_Float16)ldexp2(1.f, max(down, -14)), down2 = (_Float16)ldexp2(1.f, max(down + 14, -24));
     u32x4 x[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) x[j] = column_of(x8, j);
@@ -937,10 +942,9 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         u32x4 a = ld16(&ring[(k >> 1) & 1][k & 1][p * NR + n][lane * 8]);
-        if (KIND == OUT_F16 && down) {
-          v8h v = __builtin_bit_cast(v8h, a) * down1;
-          if (down < -14) v = v * down2;
-          a = __builtin_bit_cast(u32x4, v);
+        if (KIND == OUT_F16 && lost) {  // times 2^-42: zero, but infinities stay
+          const _Float16 tiny = (_Float16)0x1p-14f;
+          a = __builtin_bit_cast(u32x4, __builtin_bit_cast(v8h, a) * tiny * tiny * tiny);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][j] = mfma16<KIND>(a, x[j], acc[n][j]);
