@@ -490,7 +490,9 @@ moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_a
  *        NULL: not computed
  *   da   [E][R][K], db [E][N][R]: written whole, zero for groups without rows
  *   workspace  grouped_lora_backward_workspace_bytes(P, E, N, K, R) bytes
- * Requires as grouped_lora; P == 0 writes zero da and db.
+ * Requires as grouped_lora; P == 0 writes zero da and db.  Its launches need
+ * more workgroups than the forward call's: some sizes near the limits together
+ * are taken there and MOEQ_EINVAL here.
  * ---------------------------------------------------------------------- */
 size_t grouped_lora_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R); /* host */
 

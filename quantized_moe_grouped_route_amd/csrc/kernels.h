@@ -91,8 +91,9 @@ struct LoraArgs {
   int f16;                  // element type: binary16 (else bf16)
   const float* scale;       // [E] or null (1)
 };
-// Whether every launch of these sizes fits one grid.
+// Whether every launch of these sizes fits one grid, forward and gradients.
 bool lora_fits(int64_t P, int E, int N, int K, int R);
+bool lora_bwd_fits(int64_t P, int E, int N, int K, int R);
 size_t lora_workspace_bytes(int64_t P, int E, int N, int K, int R);
 size_t lora_bwd_workspace_bytes(int64_t P, int E, int N, int K, int R);
 // h: null, or [P][R] that receives the shrunk rows.

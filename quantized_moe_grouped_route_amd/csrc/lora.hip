@@ -1250,18 +1250,24 @@ hipError_t backward(const LoraArgs& g, const uint16_t* dy, const uint16_t* x, co
 
 }  // namespace
 
-bool lora_fits(int64_t P, int E, int N, int K, int R) {
-  constexpr int64_t kThreadsMax = int64_t(1) << 31;  // per launch, half the packet's limit
-  const int64_t rchunks = (R + 63) / 64;
-  for (const int C : {N, K}) {
-    if (max_tiles(P, E, 16 * shrink_rt(P, E, rank_tiles(R))) * shrink_splits(P, E, C, R) * rchunks *
-            kShrinkThreads > kThreadsMax)
-      return false;
-    const int64_t tiles = max_tiles(P, E, expand_rows(P, E, R, 0));
-    const int blocks = (C + 511) / 512, iters = expand_iters(tiles, blocks);
-    if (tiles * ((blocks + iters - 1) / iters) > kMaxBlocks) return false;
-  }
-  return max_tiles(P, E, 32) * 512 <= kThreadsMax / 2 &&
+namespace {
+constexpr int64_t kThreadsMax = int64_t(1) << 31;  // per launch, half the packet's limit
+
+// Whether a shrink of C columns and an expand to C2 fit one grid each.
+bool products_fit(int64_t P, int E, int C, int C2, int R) {
+  if (max_tiles(P, E, 16 * shrink_rt(P, E, rank_tiles(R))) * shrink_splits(P, E, C, R) * ((R + 63) / 64) *
+          kShrinkThreads > kThreadsMax)
+    return false;
+  const int64_t tiles = max_tiles(P, E, expand_rows(P, E, R, 0));
+  const int blocks = (C2 + 511) / 512, iters = expand_iters(tiles, blocks);
+  return tiles * ((blocks + iters - 1) / iters) <= kMaxBlocks;
+}
+}  // namespace
+
+bool lora_fits(int64_t P, int E, int N, int K, int R) { return products_fit(P, E, K, N, R); }
+
+bool lora_bwd_fits(int64_t P, int E, int N, int K, int R) {
+  return products_fit(P, E, N, K, R) && max_tiles(P, E, 32) * 512 <= kThreadsMax / 2 &&
          max_chunks(P, E, outer_chunk(P, E, N, K, R)) * outer_tasks(N, K, R) * kOuterThreads <= kThreadsMax &&
          E * (((int64_t)N + K) * (R / 4) / 256 + 2) * 256 <= kThreadsMax;
 }

@@ -127,16 +127,18 @@ moeq_status check_tokens(const char* fn, int64_t T, int32_t topk, int64_t N, int
   return MOEQ_OK;
 }
 
-bool lora_sizes_ok(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
+using LoraFits = bool (*)(int64_t P, int E, int N, int K, int R);
+
+bool lora_sizes_ok(LoraFits fits, int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
   return P >= 0 && P < (int64_t(1) << 31) && E >= 1 && E <= kMaxE && N >= 8 && N <= (1 << 20) && N % 8 == 0 &&
          K >= 8 && K <= (1 << 20) && K % 8 == 0 && R >= 8 && R <= kMaxRank && R % 8 == 0 &&
-         moeq::lora_fits(P, E, (int)N, (int)K, R);
+         fits(P, E, (int)N, (int)K, R);
 }
 
 // Checks shared by grouped_lora and its gradient.
-moeq_status check_lora(const char* fn, moeq_dtype dtype, const void* x, int64_t rows_x, int a_row, const void* a,
-                       const void* b, const float* scale, const int32_t* offsets, const int32_t* sorted, int64_t P,
-                       int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, int out_row) {
+moeq_status check_lora(const char* fn, LoraFits fits, moeq_dtype dtype, const void* x, int64_t rows_x, int a_row,
+                       const void* a, const void* b, const float* scale, const int32_t* offsets, const int32_t* sorted,
+                       int64_t P, int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, int out_row) {
   if (dtype != MOEQ_F16 && dtype != MOEQ_BF16) return fail(MOEQ_EUNSUPPORTED, "%s: dtype %d", fn, dtype);
   if (E < 1 || E > kMaxE) return fail(MOEQ_EINVAL, "%s: E=%d outside [1, %d]", fn, E, kMaxE);
   if (topk < 1 || topk > kMaxTopk) return fail(MOEQ_EINVAL, "%s: topk=%d outside [1, %d]", fn, topk, kMaxTopk);
@@ -146,7 +148,7 @@ moeq_status check_lora(const char* fn, moeq_dtype dtype, const void* x, int64_t 
   if (R < 1 || R > kMaxRank) return fail(MOEQ_EINVAL, "%s: R=%d outside [1, %d]", fn, R, kMaxRank);
   if (N % 8 != 0 || K % 8 != 0 || R % 8 != 0)
     return fail(MOEQ_EALIGN, "%s: N=%lld, K=%lld and R=%d must be multiples of 8", fn, (long long)N, (long long)K, R);
-  if (!moeq::lora_fits(P, E, (int)N, (int)K, R))
+  if (!fits(P, E, (int)N, (int)K, R))
     return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld, R=%d are too large for one launch", fn, (long long)P, E,
                 (long long)N, (long long)K, R);
   if (a_row != MOEQ_AROW_TOKEN && a_row != MOEQ_AROW_SORTED) return fail(MOEQ_EINVAL, "%s: bad a_row %d", fn, a_row);
@@ -446,11 +448,13 @@ moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype
 }
 
 size_t grouped_lora_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
-  return lora_sizes_ok(P, E, N, K, R) ? moeq::lora_workspace_bytes(P, E, (int)N, (int)K, R) : 0;
+  return lora_sizes_ok(moeq::lora_fits, P, E, N, K, R) ? moeq::lora_workspace_bytes(P, E, (int)N, (int)K, R) : 0;
 }
 
 size_t grouped_lora_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K, int32_t R) {
-  return lora_sizes_ok(P, E, N, K, R) ? moeq::lora_bwd_workspace_bytes(P, E, (int)N, (int)K, R) : 0;
+  return lora_sizes_ok(moeq::lora_bwd_fits, P, E, N, K, R)
+             ? moeq::lora_bwd_workspace_bytes(P, E, (int)N, (int)K, R)
+             : 0;
 }
 
 moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_arow a_row, const void* a,
@@ -459,8 +463,8 @@ moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_a
                          int32_t E, int64_t N, int64_t K, int32_t R, const void* base, moeq_orow out_row, void* out,
                          float* h, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "grouped_lora";
-  moeq_status st = check_lora(fn, dtype, x, rows_x, a_row, a, b, scale, expert_offsets, sorted_pair_ids, P, topk, E,
-                              N, K, R, out_row);
+  moeq_status st = check_lora(fn, moeq::lora_fits, dtype, x, rows_x, a_row, a, b, scale, expert_offsets,
+                              sorted_pair_ids, P, topk, E, N, K, R, out_row);
   if (st != MOEQ_OK) return st;
   if (P > 0 && !out) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(out, 16) || !aligned(base, 16) || !aligned(h, 16) || !aligned(workspace, 16) ||
@@ -496,8 +500,8 @@ moeq_status grouped_lora_backward(const void* dy, moeq_dtype dtype, moeq_orow ou
                                   int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, void* dx, void* da,
                                   void* db, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "grouped_lora_backward";
-  moeq_status st = check_lora(fn, dtype, x, rows_x, a_row, a, b, scale, expert_offsets, sorted_pair_ids, P, topk, E,
-                              N, K, R, out_row);
+  moeq_status st = check_lora(fn, moeq::lora_bwd_fits, dtype, x, rows_x, a_row, a, b, scale, expert_offsets,
+                              sorted_pair_ids, P, topk, E, N, K, R, out_row);
   if (st != MOEQ_OK) return st;
   if (!da || !db || (P > 0 && (!dy || !h))) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(dx, 16) || !aligned(da, 16) || !aligned(db, 16) ||
