@@ -113,6 +113,23 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// One of the outputs shares a byte with another of them or with an input.
+template <size_t NO, size_t NI>
+bool outputs_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
+  for (size_t i = 0; i < NO; ++i) {
+    for (size_t j = 0; j < NI; ++j)
+      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return true;
+    for (size_t j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return true;
+  }
+  return false;
+}
+
 bool float_dtype(moeq_dtype d) { return d == MOEQ_F16 || d == MOEQ_BF16 || d == MOEQ_F32; }
 int64_t float_bytes(moeq_dtype d) { return d == MOEQ_F32 ? 4 : 2; }
 
@@ -472,20 +489,15 @@ moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_a
     return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
   if (P > 0 && out_row == MOEQ_OROW_PAIR && base != out && !pair_to_sorted)
     return fail(MOEQ_EINVAL, "%s: pair-ordered rows out of place need pair_to_sorted", fn);
-  const int64_t ob = P * N * 2, hb = P * R * 4;
-  if ((base != out && overlap(out, ob, base, ob)) || overlap(out, ob, x, rows_x * K * 2) ||
-      overlap(out, ob, a, E * K * R * 2) || overlap(out, ob, b, E * N * R * 2))
-    return fail(MOEQ_EINVAL, "%s: out overlaps an input (base may be out itself)", fn);
-  if (overlap(h, hb, out, ob) || overlap(h, hb, base, ob) || overlap(h, hb, x, rows_x * K * 2) ||
-      overlap(h, hb, a, E * K * R * 2) || overlap(h, hb, b, E * N * R * 2))
-    return fail(MOEQ_EINVAL, "%s: h overlaps another argument", fn);
+  const int64_t ob = P * N * 2;
   const size_t need = moeq::lora_workspace_bytes(P, E, (int)N, (int)K, R);
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
-  if (overlap(workspace, (int64_t)need, out, ob) || overlap(workspace, (int64_t)need, base, ob) ||
-      overlap(workspace, (int64_t)need, x, rows_x * K * 2) || overlap(workspace, (int64_t)need, h, hb) ||
-      overlap(workspace, (int64_t)need, a, E * K * R * 2) || overlap(workspace, (int64_t)need, b, E * N * R * 2))
-    return fail(MOEQ_EINVAL, "%s: workspace overlaps another argument", fn);
+  const Span outs[] = {{out, ob}, {h, P * R * 4}, {workspace, (int64_t)need}},
+             ins[] = {{base == out ? nullptr : base, ob}, {x, rows_x * K * 2}, {a, E * K * R * 2}, {b, E * N * R * 2},
+                      {scale, E * 4}, {expert_offsets, (E + 1) * 4}, {sorted_pair_ids, P * 4}, {pair_to_sorted, P * 4}};
+  if (outputs_overlap(outs, ins))
+    return fail(MOEQ_EINVAL, "%s: out, h or the workspace overlaps another argument (base may be out itself)", fn);
   const moeq::LoraArgs g = lora_args(dtype, a_row, scale, expert_offsets, sorted_pair_ids, pair_to_sorted, P, topk, E,
                                      N, K, R, out_row);
   return hip_status(moeq::launch_lora(g, static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(a),
@@ -510,17 +522,11 @@ moeq_status grouped_lora_backward(const void* dy, moeq_dtype dtype, moeq_orow ou
   const size_t need = moeq::lora_bwd_workspace_bytes(P, E, (int)N, (int)K, R);
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
-  const struct { const void* p; int64_t n; } outs[4] = {{dx, P * K * 2}, {da, E * K * R * 2}, {db, E * N * R * 2},
-                                                        {workspace, (int64_t)need}},
-      ins[5] = {{dy, P * N * 2}, {x, rows_x * K * 2}, {a, E * K * R * 2}, {b, E * N * R * 2}, {h, P * R * 4}};
-  for (int i = 0; i < 4; ++i) {
-    for (int j = 0; j < 5; ++j)
-      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
-        return fail(MOEQ_EINVAL, "%s: an output or the workspace overlaps an input", fn);
-    for (int j = 0; j < i; ++j)
-      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
-        return fail(MOEQ_EINVAL, "%s: two outputs, or an output and the workspace, overlap", fn);
-  }
+  const Span outs[] = {{dx, P * K * 2}, {da, E * K * R * 2}, {db, E * N * R * 2}, {workspace, (int64_t)need}},
+             ins[] = {{dy, P * N * 2}, {x, rows_x * K * 2}, {a, E * K * R * 2}, {b, E * N * R * 2}, {h, P * R * 4},
+                      {scale, E * 4}, {expert_offsets, (E + 1) * 4}, {sorted_pair_ids, P * 4}};
+  if (outputs_overlap(outs, ins))
+    return fail(MOEQ_EINVAL, "%s: an output or the workspace overlaps an input or another output", fn);
   const moeq::LoraArgs g = lora_args(dtype, a_row, scale, expert_offsets, sorted_pair_ids, nullptr, P, topk, E, N, K,
                                      R, out_row);
   return hip_status(moeq::launch_lora_bwd(g, static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),

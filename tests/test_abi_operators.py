@@ -3,7 +3,7 @@ their limits (no GPU needed; the C calls see addresses only)."""
 import pytest
 
 import quantized_moe_grouped_route_amd as mq
-from tests.test_abi_lora import L, _lora, _lora_bwd  # noqa: F401  (L: the library, a fixture)
+from tests.test_abi_lora import L, _lora, _lora_bwd, at  # noqa: F401  (L: the library, a fixture)
 
 
 # Many wide groups of a high rank: the gradients' weight sums need more
@@ -24,3 +24,28 @@ def test_the_forward_call_takes_more_rows_than_its_gradients(L):
     assert L.grouped_lora_workspace_bytes(P, 1, 8, 8, 8) == P * 8 * 4
     assert L.grouped_lora_backward_workspace_bytes(P, 1, 8, 8, 8) == 0
     assert L.grouped_lora_workspace_bytes(2 * P, 1, 8, 8, 8) == 0
+
+
+# The tables and the scales are inputs too: an output over one of them would
+# change them while the call reads them.
+@pytest.mark.parametrize("out", ["out", "h", "ws"])
+@pytest.mark.parametrize("table,nbytes", [("sc", 4 * 4), ("off", 5 * 4), ("srt", 16 * 4), ("p2s", 16 * 4)])
+def test_lora_refuses_outputs_over_the_tables(L, out, table, nbytes):
+    kw = dict(p2s=at(12), orow=1, h=at(9))
+    where = dict(sc=at(3), off=at(4), srt=at(5), p2s=at(12))[table]
+    need = L.grouped_lora_workspace_bytes(16, 4, 64, 8192, 16)
+    size = dict(out=16 * 64 * 2, h=16 * 16 * 4, ws=need)[out]
+    for p in (where, where + (nbytes - 1) // 16 * 16, where - (size - 1) // 16 * 16):
+        assert _lora(L, **{**kw, out: p}) == mq.EINVAL
+        assert b"overlaps" in L.moeq_last_error()
+
+
+@pytest.mark.parametrize("out", ["dx", "da", "db", "ws"])
+@pytest.mark.parametrize("table,nbytes", [("sc", 4 * 4), ("off", 5 * 4), ("srt", 16 * 4)])
+def test_lora_backward_refuses_outputs_over_the_tables(L, out, table, nbytes):
+    where = dict(sc=at(4), off=at(6), srt=at(7))[table]
+    size = dict(dx=16 * 128 * 2, da=4 * 16 * 128 * 2, db=4 * 64 * 16 * 2,
+                ws=L.grouped_lora_backward_workspace_bytes(16, 4, 64, 128, 16))[out]
+    for p in (where, where + (nbytes - 1) // 16 * 16, where - (size - 1) // 16 * 16):
+        assert _lora_bwd(L, **{out: p}) == mq.EINVAL
+        assert b"overlaps" in L.moeq_last_error()
