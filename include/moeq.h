@@ -389,7 +389,7 @@ moeq_status moe_sum_pairs(const void* y_pairs, moeq_dtype y_dtype, const int32_t
  *       every pair that has an expert; the other rows (those past
  *       expert_offsets[E]) are not written
  * Requires N % 8 == 0 (U8: N % 16 == 0; else MOEQ_EALIGN), 16-byte aligned
- * x and xs, xs disjoint from x (else MOEQ_EINVAL), 1 <= topk <= 64,
+ * x and xs, xs disjoint from the inputs (else MOEQ_EINVAL), 1 <= topk <= 64,
  * T*topk < 2^31.
  * ---------------------------------------------------------------------- */
 moeq_status moe_permute(const void* x, moeq_dtype dtype, const int32_t* pair_to_sorted, int64_t T, int32_t topk,
@@ -405,7 +405,7 @@ moeq_status moe_permute(const void* x, moeq_dtype dtype, const int32_t* pair_to_
  *
  *   dxs  [T*topk][N] dxs_dtype (F16 | BF16 | F32), rows in sorted order
  *   dx   [T][N] dx_dtype (F16 | BF16 | F32)
- * Requires as moe_permute, dx disjoint from dxs.
+ * Requires as moe_permute, dx disjoint from the inputs.
  * ---------------------------------------------------------------------- */
 moeq_status moe_permute_backward(const void* dxs, moeq_dtype dxs_dtype, const int32_t* pair_to_sorted, int64_t T,
                                  int32_t topk, int64_t N, moeq_dtype dx_dtype, void* dx, void* stream);

@@ -418,7 +418,8 @@ moeq_status moe_permute(const void* x, moeq_dtype dtype, const int32_t* pair_to_
   if (T > 0 && (!x || !pair_to_sorted || !xs)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(pair_to_sorted, 4))
     return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
-  if (overlap(xs, T * topk * N * elem, x, T * N * elem)) return fail(MOEQ_EINVAL, "%s: xs overlaps x", fn);
+  const Span outs[] = {{xs, T * topk * N * elem}}, ins[] = {{x, T * N * elem}, {pair_to_sorted, T * topk * 4}};
+  if (outputs_overlap(outs, ins)) return fail(MOEQ_EINVAL, "%s: xs overlaps an input", fn);
   return hip_status(moeq::launch_permute(x, pair_to_sorted, (int)T, topk, N * elem, xs, device_cus(),
                                          (hipStream_t)stream),
                     fn);
@@ -434,8 +435,9 @@ moeq_status moe_permute_backward(const void* dxs, moeq_dtype dxs_dtype, const in
   if (T > 0 && (!dxs || !pair_to_sorted || !dx)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(dxs, 16) || !aligned(dx, 16) || !aligned(pair_to_sorted, 4))
     return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
-  if (overlap(dx, T * N * float_bytes(dx_dtype), dxs, T * topk * N * float_bytes(dxs_dtype)))
-    return fail(MOEQ_EINVAL, "%s: dx overlaps dxs", fn);
+  const Span outs[] = {{dx, T * N * float_bytes(dx_dtype)}},
+             ins[] = {{dxs, T * topk * N * float_bytes(dxs_dtype)}, {pair_to_sorted, T * topk * 4}};
+  if (outputs_overlap(outs, ins)) return fail(MOEQ_EINVAL, "%s: dx overlaps an input", fn);
   return hip_status(moeq::launch_permute_bwd(dxs, (int)dxs_dtype, pair_to_sorted, (int)T, topk, (int)N,
                                              (int)dx_dtype, dx, (hipStream_t)stream),
                     fn);
@@ -454,10 +456,10 @@ moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype
   if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(pair_to_sorted, 4) ||
       !aligned(topk_weights, 4) || !aligned(dw, 4))
     return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
-  const int64_t db = T * N * float_bytes(dout_dtype), yb = T * topk * N * float_bytes(y_dtype), wb = T * topk * 4;
-  if (overlap(dy, yb, dout, db) || overlap(dy, yb, y, yb) || overlap(dy, yb, topk_weights, wb) ||
-      overlap(dw, wb, topk_weights, wb) || overlap(dw, wb, dy, yb) || overlap(dw, wb, y, yb) ||
-      overlap(dw, wb, dout, db))
+  const int64_t yb = T * topk * N * float_bytes(y_dtype), pb = T * topk * 4;
+  const Span outs[] = {{dy, yb}, {dw, pb}},
+             ins[] = {{dout, T * N * float_bytes(dout_dtype)}, {y, yb}, {pair_to_sorted, pb}, {topk_weights, pb}};
+  if (outputs_overlap(outs, ins))
     return fail(MOEQ_EINVAL, "%s: an output overlaps an input or the other output", fn);
   return hip_status(moeq::launch_combine_bwd(dout, (int)dout_dtype, y, (int)y_dtype, pair_to_sorted, topk_weights,
                                              (int)T, topk, (int)N, dy, dw, device_cus(), (hipStream_t)stream),

@@ -3,7 +3,7 @@ their limits (no GPU needed; the C calls see addresses only)."""
 import pytest
 
 import quantized_moe_grouped_route_amd as mq
-from tests.test_abi_lora import L, _lora, _lora_bwd, at  # noqa: F401  (L: the library, a fixture)
+from tests.test_abi_lora import L, _combine_bwd, _lora, _lora_bwd, _permute, _permute_bwd, at  # noqa: F401  (L: the library, a fixture)
 
 
 # Many wide groups of a high rank: the gradients' weight sums need more
@@ -48,4 +48,14 @@ def test_lora_backward_refuses_outputs_over_the_tables(L, out, table, nbytes):
                 ws=L.grouped_lora_backward_workspace_bytes(16, 4, 64, 128, 16))[out]
     for p in (where, where + (nbytes - 1) // 16 * 16, where - (size - 1) // 16 * 16):
         assert _lora_bwd(L, **{out: p}) == mq.EINVAL
+        assert b"overlaps" in L.moeq_last_error()
+
+
+@pytest.mark.parametrize("call,out,size,table", [
+    (_permute, "xs", 8 * 64 * 2, at(1)), (_permute_bwd, "dx", 4 * 64 * 4, at(1)),
+    (_combine_bwd, "dy", 8 * 64 * 2, at(2)), (_combine_bwd, "dw", 8 * 4, at(2)),
+])
+def test_permutation_and_gradients_refuse_outputs_over_the_pair_table(L, call, out, size, table):
+    for p in (table, table + 8 * 4 - 16, table - size + 16):
+        assert call(L, **{out: p}) == mq.EINVAL
         assert b"overlaps" in L.moeq_last_error()
