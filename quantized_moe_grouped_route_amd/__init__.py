@@ -535,8 +535,9 @@ def moe_permute_backward(dxs, pair_to_sorted, topk: int, *, out_dtype=None, out=
 def moe_scatter_combine_backward(dout, y, pair_to_sorted, topk_weights, *, dy=None, dw=None):
     """Gradients of moe_scatter_combine: dy[s] = topk_weights[t, j] * dout[t]
     (y's type) and dw[t, j] = <dout[t], y[s]> (f32; 0 for slots without an
-    expert), s = pair_to_sorted[t*topk+j].  Returns (dy, dw); rows of dy past
-    expert_offsets[E] are not written."""
+    expert), s = pair_to_sorted[t*topk+j].  y may have rows past T*topk, as in
+    the forward call; dy then has to be given, with y's rows or T*topk.  Returns
+    (dy, dw); rows of dy past expert_offsets[E] are not written."""
     _need(dout, "dout", _FLOATS, 2)
     _need(y, "y", _FLOATS, 2)
     _need(pair_to_sorted, "pair_to_sorted", torch.int32, 1)
@@ -545,9 +546,12 @@ def moe_scatter_combine_backward(dout, y, pair_to_sorted, topk_weights, *, dy=No
     rows, N = y.shape
     if dout.shape != (T, N):
         raise ValueError(f"dout must be [{T}][{N}], got {tuple(dout.shape)}")
-    if pair_to_sorted.numel() != T * k or rows != T * k:
-        raise ValueError("pair_to_sorted needs T*topk entries and y T*topk rows")
-    dy = _fit(dy, "dy", (T * k, N), y.dtype, y)
+    if pair_to_sorted.numel() != T * k or rows < T * k:
+        raise ValueError("pair_to_sorted needs T*topk entries and y at least T*topk rows")
+    if rows != T * k and dy is None:
+        raise ValueError(f"y has {rows} rows for {T * k} pairs: give dy, with as many rows or {T * k}")
+    spare = isinstance(dy, torch.Tensor) and dy.shape[:1] == (rows,)
+    dy = _fit(dy, "dy", (rows if spare else T * k, N), y.dtype, y)
     dw = _fit(dw, "dw", (T, k), torch.float32, y)
     stream = _here("dout y pair_to_sorted topk_weights dy dw", dout, y, pair_to_sorted, topk_weights, dy, dw)
     st = lib().moe_scatter_combine_backward(dout.data_ptr(), _DTYPE_CODE[dout.dtype], y.data_ptr(),

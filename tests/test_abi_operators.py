@@ -1,6 +1,7 @@
 """What the permutation, combine-gradient and adapter calls take and refuse at
 their limits (no GPU needed; the C calls see addresses only)."""
 import pytest
+import torch
 
 import quantized_moe_grouped_route_amd as mq
 from tests.test_abi_lora import L, _combine_bwd, _lora, _lora_bwd, _permute, _permute_bwd, at  # noqa: F401  (L: the library, a fixture)
@@ -59,3 +60,21 @@ def test_permutation_and_gradients_refuse_outputs_over_the_pair_table(L, call, o
     for p in (table, table + 8 * 4 - 16, table - size + 16):
         assert call(L, **{out: p}) == mq.EINVAL
         assert b"overlaps" in L.moeq_last_error()
+
+
+def test_combine_gradient_takes_y_with_spare_rows_where_dy_is_given():
+    # (a workspace of a larger batch, as the forward call takes; refused here
+    # for being on the CPU, not for its shape)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    p2s, w = torch.zeros(8, dtype=torch.int32), torch.zeros(4, 2)
+    for rows in (9, 8):
+        with pytest.raises(ValueError, match="GPU"):
+            mq.moe_scatter_combine_backward(bf(4, 64), bf(9, 64), p2s, w, dy=bf(rows, 64))
+    with pytest.raises(ValueError, match="give dy"):
+        mq.moe_scatter_combine_backward(bf(4, 64), bf(9, 64), p2s, w)
+    with pytest.raises(ValueError, match="dy must be"):
+        mq.moe_scatter_combine_backward(bf(4, 64), bf(9, 64), p2s, w, dy=bf(10, 64))
+    with pytest.raises(ValueError, match="dy must be"):
+        mq.moe_scatter_combine_backward(bf(4, 64), bf(8, 64), p2s, w, dy=bf(9, 64))
+    with pytest.raises(ValueError, match="at least"):
+        mq.moe_scatter_combine_backward(bf(4, 64), bf(7, 64), p2s, w, dy=bf(7, 64))

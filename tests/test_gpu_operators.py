@@ -5,7 +5,7 @@ import torch
 
 from tests.gpu_util import dev, host
 from tests.test_gpu_lora import close, values
-from tests.test_gpu_permute import BF16, F16
+from tests.test_gpu_permute import BF16, F16, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +57,19 @@ def test_forward_of_more_rows_than_the_gradients_take():
         h, m = xh[i] @ host(a[e]).T, np.abs(xh[i]) @ np.abs(host(a[e])).T
         close(got[i], h @ host(b[e]).T, m @ np.abs(host(b[e])).T, F16, (K, N, R), e)
     assert np.all(got[s >= off[2]] == 7)
+
+
+def test_combine_gradient_of_y_with_spare_rows():
+    """Buffers of a larger batch: the rows past T*topk are neither read nor
+    written, and the results are those of the exact sizes."""
+    T, k, E, N = 37, 3, 5, 264
+    rng, _, (off, _, p2s, _) = tables(73, T, k, E, "repeat", 0.2)
+    dout, y, w = values(rng, (T, N), BF16), values(rng, (T * k + 9, N), BF16), dev(rng.random((T, k)).astype(np.float32))
+    y[int(off[-1]):] = float("nan")
+    dy0, dw0 = mq.moe_scatter_combine_backward(dout, y[:T * k], dev(p2s), w)
+    n = int(off[-1])
+    for rows in (T * k + 9, T * k):
+        dy = torch.full((rows, N), 7.0, dtype=BF16, device="cuda")
+        got, dw = mq.moe_scatter_combine_backward(dout, y, dev(p2s), w, dy=dy)
+        assert got is dy and torch.equal(dw, dw0)
+        assert torch.equal(dy[:n], dy0[:n]) and torch.all(dy[n:] == 7)
