@@ -439,8 +439,9 @@ moeq_status moe_scatter_combine_backward(const void* dout, moeq_dtype dout_dtype
  * group e, with p = sorted_pair_ids[s]:
  *   h[s][:]   = x[row][:] . A[e]^T            row = p / topk (TOKEN), s (SORTED)
  *   out[o][:] = base[o][:] + scale[e] * h[s][:] . B[e]^T      o = s or p
- * h is kept in fp32; sums in fp32; one rounding to the element type.  In F16,
- * scale * h enters out with 2^-33 of its row's largest value.
+ * h is kept in fp32; sums in fp32; one rounding to the element type.  In BF16
+ * scale * h enters out with all its bits (past 3.39e38, bf16's range, as an
+ * infinity), in F16 to 2^-23 of itself plus 2^-33 of its row's largest value.
  *
  *   dtype  F16 | BF16: the type of x, a, b, base and out
  *   x      [rows_x][K];  a [E][R][K];  b [E][N][R];  scale f32 [E] or NULL (1)
@@ -481,7 +482,10 @@ moeq_status grouped_lora(const void* x, moeq_dtype dtype, int64_t rows_x, moeq_a
  *   da[e]    = sum_{s of e} dh[s]^T x[row]       [R][K]
  *   db[e]    = scale[e] * sum_{s of e} dy[o]^T h[s]   [N][R]
  * sums in fp32, one rounding, in a fixed order: equal inputs give equal bits.
- * In F16, dh and h enter da and db with 2^-35 of their group's largest value.
+ * In BF16 dh and h enter with all their bits, in F16 to 2^-23 of themselves plus,
+ * for dx, 2^-33 of their row's largest value and, for da and db, 2^-35 of their
+ * group's.  da and db have the element type: in F16, gradients below 2^-24 are
+ * lost, so scale the loss where they may be.
  *
  *   dy   [P][N] in out_row's order; x, a, b, scale and the tables as in the
  *        forward call; h f32 [P][R] as it wrote it

@@ -8,6 +8,10 @@ kernels.  PyTorch supplies device memory and streams only.
 
 If libmoeq.so is missing or cannot be loaded, every call raises: there is
 no fallback implementation.
+
+No call records a graph for autograd: a result never requires gradients,
+whatever its arguments do.  Where a gradient exists it is a call of its own
+(moe_permute_backward, moe_scatter_combine_backward, grouped_lora_backward).
 """
 from __future__ import annotations
 
@@ -498,7 +502,8 @@ def _fit(t, name, shape, dtype, like):
 def moe_permute(x, pair_to_sorted, topk: int, *, out=None):
     """Token rows x [T][N] (f16, bf16, f32, or uint8 codes) copied to rows
     sorted by expert: out[pair_to_sorted[t*topk+j]] = x[t].  Returns out
-    [T*topk][N]; rows past expert_offsets[E] are not written."""
+    [T*topk][N]; rows past expert_offsets[E] are not written.  Not recorded by
+    autograd: the gradient is moe_permute_backward."""
     _need(x, "x", _ROWS, 2)
     T = _pairs(pair_to_sorted, topk)
     rows, N = x.shape
@@ -611,7 +616,8 @@ def grouped_lora(x, a, b, expert_offsets, sorted_pair_ids, topk: int, *, base=No
     'pair' rows without a group become base and need pair_to_sorted; 'sorted'
     rows past expert_offsets[E] are not written.  h (f32 [P][R]) receives
     x[row] a[e]^T for grouped_lora_backward.  workspace: uint8,
-    lora_workspace_bytes(P, E, N, K, R).  Returns out [P][N]."""
+    lora_workspace_bytes(P, E, N, K, R).  Returns out [P][N].  Not recorded by
+    autograd: the gradients are grouped_lora_backward."""
     E, R, K, N, P, rows = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids)
     dt = x.dtype
     if base is not None:
@@ -640,7 +646,8 @@ def grouped_lora_backward(dy, x, a, b, h, expert_offsets, sorted_pair_ids, topk:
     (dx [P][K] in sorted order, or None without need_dx; da [E][R][K];
     db [E][N][R]), all of x's type: da and db are written whole, rows of dx
     past expert_offsets[E] are not.  With a_row 'token', moe_permute_backward
-    sums dx over each token's slots.  workspace: uint8,
+    sums dx over each token's slots.  f16 gradients below 2^-24 are lost: scale
+    the loss where they may be.  workspace: uint8,
     lora_workspace_bytes(P, E, N, K, R, backward=True)."""
     E, R, K, N, P, rows = _lora_common(x, a, b, scale, expert_offsets, sorted_pair_ids)
     dt = x.dtype

@@ -20,12 +20,13 @@
 // dh of 256 experts under Zipf routing took 167 us, not 145.
 //
 // The low-rank operand (h, dh) is fp32.  It enters the MFMAs as a sum of
-// 16-bit parts that carries all its 24 bits: three of bf16 (8 bits each), or
-// two of binary16 (11 each and the sign between) after scaling by a power of
-// two to the middle of binary16's range (per row in expand; per tile of 32 rows
-// in outer, whose sums move to the scale of the tile at work).  A single 16-bit
-// rounding would have put its 2^-9 (2^-12) error into every product; the extra
-// MFMAs are free here.
+// 16-bit parts: three of bf16 (8 bits each), exactly, or two of binary16 (11
+// bits each and the sign between), to 2^-23 of itself, after scaling by a power
+// of two to the middle of binary16's range: per row in expand, where values far
+// below the row's largest keep 2^-33 of that; per tile of 32 rows in outer,
+// 2^-35 of the tile's largest, with sums that move to the scale of the tile at
+// work.  A single 16-bit rounding would have put its 2^-9 (2^-12) error into
+// every product; the extra MFMAs are free here.
 #include <algorithm>
 
 #include "common.h"
@@ -326,10 +327,16 @@ __device__ __forceinline__ void shrink_tile(const Dev& g, const uint16_t* __rest
 
 // part[split][s][r]: one workgroup takes 16 RT rows of one group, 64 ranks at
 // most, and one split of the columns.
-// Bound by its one read of X with what it has in flight.  dh of 32768 bf16
-// rows of 7168, 256 experts under Zipf routing, rank 16: 124 us, 0.53 GB, 4.3
-// TB/s; h of 16384 f16 rows of 4096 from 8192 tokens, 8 experts: 40 - 44 us.
-// 4 waves or 8, 1, 2 or 4 row tiles, 1 split or 2 are within 2 % there.
+// Up to rank 32 bound by its one read of X with what it has in flight, below
+// what reads alone reach (7.0 TB/s).  dh of 32768 bf16 rows of 7168, 256 experts
+// under Zipf routing, rank 16: 124 - 129 us, 0.53 GB, 4.3 TB/s; h of 16384 f16
+// rows of 4096 from 8192 tokens, 8 experts: 36 - 46 us.  4 waves or 8, 1, 2 or 4
+// row tiles, 1 split or 2 are within 2 % there.
+// At rank 64 W bounds it: every workgroup reads the group's whole W through the
+// L2, 512 KB for 256 KB of X in 32 rows (1 MB in 16), and the two-row-tile form
+// spills 8 to 12 registers in its loop, with 74 - 102 KB of LDS one workgroup on
+// a compute unit.  dh of 16384 f16 rows of 4096, 8 experts: 68 - 80 us, 0.15 GB.
+// Above rank 64, X is read again for every 64 ranks.
 template <int KIND, int RT, int NR, bool C_MAJOR>
 __global__ __launch_bounds__(kShrinkThreads) void shrink_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm,
                                                                 int C, const uint16_t* __restrict__ W,
@@ -554,7 +561,8 @@ __device__ __forceinline__ void copy_rows_without(const Dev& g, const ExpandArgs
 // flight; OC = 0 takes any rank, reloading the weights for every 32 rows.
 // Bound by base and out: 16384 f16 rows of 28672 at rank 16, 1.88 GB, 341 us,
 // 5.5 TB/s.  dx with the outer kernel's tiles: 16384 f16 rows of 14336 at rank
-// 64 97 - 113 us (0.47 GB written), 32768 bf16 rows of 2048 47 us.
+// 64 96 - 116 us (0.47 GB written), 32768 bf16 rows of 2048 47 - 51 us.  Above
+// rank 64 (OC = 0) bound by the weights, read again for every 32 rows.
 template <int KIND, int OC, bool TR, bool NT>
 __global__ __launch_bounds__(kExpandThreads, OC ? 3 : 2) void expand_kernel(Dev g, ExpandArgs a) {
   constexpr int NP = kParts<KIND>, RTI = OC ? 1 : 2;
@@ -716,9 +724,12 @@ constexpr int kSmallCols = 128 * kShrinkWaves;
 // one group and 1024 columns of the output, and computes the rows' low-rank
 // values for itself.  The column blocks of a tile repeat that, which costs
 // less than a second launch and its trip through memory while A is short.
-// Bound by its chain of trips to memory (offsets, pairs, x and A, B) and one
-// compute unit's loads of A: one row, K = N = 4096, rank 16, 10.0 us (two
-// launches 4.6 + 6.8 us); K = N = 1024, rank 8, 6.1 us in a graph for 8.8.
+// Bound by its chain of trips to memory and one compute unit's loads of A.  In
+// series: the offsets; the row's pair, whose wait holds for B's loads too; the
+// pair again for x's row; x and A, two steps of 128 columns a wave at a time; the
+// scale, after the reduction; base, after the barrier behind it.  One row, K = N
+// = 4096, rank 16, 10.0 us (two launches 4.6 + 6.8 us); K = N = 1024, rank 8, 6.1
+// us in a graph for 8.8.
 template <int KIND, int NR>
 __global__ __launch_bounds__(kShrinkThreads) void small_kernel(Dev g, const uint16_t* __restrict__ X, RowMap xm, int K,
                                                                const uint16_t* __restrict__ A, ExpandArgs a) {
@@ -830,10 +841,13 @@ __host__ __device__ constexpr int64_t outer_slots(int64_t P, int chunk) {
 // ahead: a row or an exponent that came through a register would be the newest
 // load when it is needed, and waiting for it would be waiting for everything
 // in flight.
-// Bound by its one read of both wide operands, 0.60 GB each: bf16 rows of 7168
-// and 2048, 256 experts under Zipf routing, rank 16, 137 us, 4.4 TB/s; f16 rows
-// of 4096 and 14336, 8 experts, rank 64, 136 - 147 us.  Two tiles in flight,
-// double buffers for the MFMA operands, or 128 columns a wave were no faster.
+// One read of both wide operands, 0.60 GB together: bf16 rows of 7168 and 2048,
+// 256 experts under Zipf routing, rank 16, 136 - 148 us, 4.4 TB/s; f16 rows of
+// 4096 and 14336, 8 experts, rank 64, 132 - 152 us.  What holds it below the 7.0
+// TB/s of reads alone is not shown; it is not HBM, as the second takes dy from
+// the Infinity Cache and is no faster.  Two tiles in flight, double buffers for
+// the MFMA operands, or 128 columns a wave were no faster.  Above rank 64, both
+// operands are read again for every 64 ranks.
 template <int KIND, int NR>
 __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa, Side sb, Tiles tl, int rchunks,
                                                                  int chunk) {
@@ -996,7 +1010,8 @@ __global__ __launch_bounds__(kOuterThreads, 3) void outer_kernel(Dev g, Side sa,
 
 // Joins the chunks of the groups longer than one: a thread takes 4 ranks of
 // one column, so that both output orders store 4 values at once or in runs.
-// 13 us (256 experts, most of them whole) and 5 us (8 experts) after the above.
+// 14 - 16 us (256 experts, most of them whole) and 4 - 6 us (8 experts, none cut:
+// the launch covers every group whose rows could fill one that is) after the above.
 template <int KIND>
 __global__ __launch_bounds__(256) void join_kernel(Dev g, Side sa, Side sb, int blocks_a, int blocks_b,
                                                   int chunk) {
@@ -1035,8 +1050,9 @@ int64_t max_tiles(int64_t P, int E, int bm) { return P / bm + std::min<int64_t>(
 
 // Row tiles (of 16) a workgroup takes.  Two halve the reads of the weights;
 // four took more registers than that gave back (Zipf over 256 experts, dh: 120
-// us at two, 145 at four).
-int shrink_rt(int64_t P, int E, int nr) { return P >= 24 * (int64_t)E ? 2 : 1; }
+// us at two, 145 at four).  At rank 64 two spill, and one, which reads the
+// weights twice as often, was no faster.
+int shrink_rt(int64_t P, int E) { return P >= 24 * (int64_t)E ? 2 : 1; }
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }  // per workgroup; 64 ranks at most
 
 // Rows of an expand workgroup: about the average group's, up to 64 (beside the
@@ -1060,8 +1076,8 @@ int expand_iters(int64_t tiles, int blocks) {
 // Column splits of a shrink: enough workgroups for two on each of 256 compute
 // units, at least one 128-column step per wave.
 int shrink_splits(int64_t P, int E, int C, int R) {
-  const int nr = rank_tiles(R), steps = (C + 127) / 128;
-  const int64_t wgs = max_tiles(P, E, 16 * shrink_rt(P, E, nr)) * ((R + 63) / 64);
+  const int steps = (C + 127) / 128;
+  const int64_t wgs = max_tiles(P, E, 16 * shrink_rt(P, E)) * ((R + 63) / 64);
   const int64_t want = (512 + wgs - 1) / std::max<int64_t>(1, wgs);
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, (steps + kShrinkWaves - 1) / kShrinkWaves, 8}));
 }
@@ -1079,7 +1095,7 @@ hipError_t shrink_launch(const Dev& d, const uint16_t* X, RowMap xm, int C, cons
 template <int KIND, bool CM>
 hipError_t shrink(const Dev& d, const uint16_t* X, RowMap xm, int C, const uint16_t* W, float* part, int splits,
                   hipStream_t stream) {
-  const int nr = rank_tiles(d.R), rt = shrink_rt(d.P, d.E, nr);
+  const int nr = rank_tiles(d.R), rt = shrink_rt(d.P, d.E);
   if (nr == 1 && rt == 2) return shrink_launch<KIND, 2, 1, CM>(d, X, xm, C, W, part, splits, stream);
   if (nr == 1) return shrink_launch<KIND, 1, 1, CM>(d, X, xm, C, W, part, splits, stream);
   if (nr == 2 && rt == 2) return shrink_launch<KIND, 2, 2, CM>(d, X, xm, C, W, part, splits, stream);
@@ -1167,7 +1183,8 @@ hipError_t outer(const Dev& d, const Side& sa, const Side& sb, const Tiles& tl, 
 // graphs, one row to 200: A of 16 KB a group 6.1 - 7.7 us for 8.8 - 10.9, of
 // 64 KB 8.2 - 8.4 for 10.5 - 10.9, of 128 KB 9.8 - 11.2 for 9.9 - 11.0 (and a
 // launch less for the host), of 224 KB 13.0 - 19.1 for 10.8 - 13.7; with more
-// workgroups than CUs 16.8 for 14.4.
+// workgroups than CUs 16.8 for 14.4.  (256 is an MI355X's number, written out: the
+// workspace's size may not depend on the device that is current when it is asked.)
 bool one_launch(int64_t P, int E, int N, int K, int R) {
   return R <= 64 && max_tiles(P, E, 16) * ((N + kSmallCols - 1) / kSmallCols) <= 256 &&
          (int64_t)rank_tiles(R) * 16 * K <= 65536;
@@ -1255,7 +1272,7 @@ constexpr int64_t kThreadsMax = int64_t(1) << 31;  // per launch, half the packe
 
 // Whether a shrink of C columns and an expand to C2 fit one grid each.
 bool products_fit(int64_t P, int E, int C, int C2, int R) {
-  if (max_tiles(P, E, 16 * shrink_rt(P, E, rank_tiles(R))) * shrink_splits(P, E, C, R) * ((R + 63) / 64) *
+  if (max_tiles(P, E, 16 * shrink_rt(P, E)) * shrink_splits(P, E, C, R) * ((R + 63) / 64) *
           kShrinkThreads > kThreadsMax)
     return false;
   const int64_t tiles = max_tiles(P, E, expand_rows(P, E, R, 0));
