@@ -20,6 +20,12 @@
  *   moe_scatter_combine_backward       gradients of the combine
  *   grouped_lora, grouped_lora_backward  low-rank adapters of the experts,
  *                           or of the requests of a batch, and gradients
+ * and, for experts kept in 8-bit integers, served or trained around:
+ *   moe_quantize_int8       per-row INT8 activation quantization
+ *   grouped_gemm_qint8      W8A8 INT8 GEMM, per-token x per-channel scales
+ *   grouped_gemm_qint8_backward  its gradient towards the activations
+ *   moe_silu_mul, moe_silu_mul_backward  the gated activation by itself, with
+ *                           an 8-bit checkpoint of its input, and gradient
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer (memory the caller allocated
@@ -505,6 +511,132 @@ moeq_status grouped_lora_backward(const void* dy, moeq_dtype dtype, moeq_orow ou
                                   const int32_t* expert_offsets, const int32_t* sorted_pair_ids, int64_t P,
                                   int32_t topk, int32_t E, int64_t N, int64_t K, int32_t R, void* dx, void* da,
                                   void* db, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_quantize_int8 - per-row symmetric INT8 quantization of activations,
+ * the operand rows of grouped_gemm_qint8:
+ *   amax = max_k |x[r][k]|,  scale[r] = amax / 127,
+ *   code = clamp(rne(x[r][k] * (127 / amax)), -127, 127)
+ * with each division and the product one fp32 operation; a row with
+ * amax < 2^-120 (an all-zero row included) gives zeros and scale 1.  A row
+ * that holds an infinity or NaN gets scale NaN (and unspecified codes): what
+ * is made of it is NaN.
+ *
+ *   x      [rows][K] x_dtype (F16 | BF16 | F32), rows contiguous
+ *   q      int8 [rows][K];  scale f32 [rows]
+ * Requires K % 16 == 0 (else MOEQ_EALIGN), K <= 2^24, rows < 2^31, x and q
+ * 16-byte aligned, scale 4-byte aligned, and outputs disjoint from x and from
+ * each other (else MOEQ_EINVAL).
+ * ---------------------------------------------------------------------- */
+moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, int64_t K, int8_t* q, float* scale,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * grouped_gemm_qint8 - W8A8 INT8 grouped GEMM: activations quantized per
+ * token, weights per output channel, int32 accumulation, the scales (and the
+ * gated activation) in the epilogue.
+ *
+ *   a          int8 [rows_a][K];  a_scale f32 [rows_a]
+ *   w          int8 [E][N][K];    w_scale f32 [E][N]
+ *   expert_offsets, sorted_pair_ids  from moe_route_prep (see top)
+ *   P          rows of `out` (>= expert_offsets[E]); topk as routed
+ *   out        [P][N] (act NONE) or [P][N/2] (SILU_MUL) of out_dtype:
+ *                F16 | BF16 | F32: a_scale[r] * w_scale[e][n] * acc
+ *                I32: the raw accumulator acc (act NONE only), bit-exact
+ * Computed exactly in integers, every code from -128 to 127, then scaled in
+ * fp32 and rounded to nearest even.
+ * Requires as grouped_gemm_qint4: K % 128 == 0 and N % 32 == 0 (else
+ * MOEQ_EALIGN), K < 131072 so that the int32 accumulator cannot wrap (else
+ * MOEQ_EINVAL), a, w and out 16-byte and the scales and tables 4-byte
+ * aligned, 1 <= E <= 1024, 1 <= topk <= 64; and out disjoint from the inputs
+ * and sizes that one launch can count, (P/8 + E) * N/16 < 2^30 (else
+ * MOEQ_EINVAL).
+ * Two schedules give identical outputs: MFMA tiles of 64, 128 or 256 rows
+ * (PREFILL, by the average rows of an expert), and waves streaming 16 weight
+ * rows x at most 8 routed rows (DECODE).  AUTO streams when P < 16 * E.
+ * ---------------------------------------------------------------------- */
+moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t rows_a, moeq_arow a_row, const int8_t* w,
+                               const float* w_scale, const int32_t* expert_offsets, const int32_t* sorted_pair_ids,
+                               int64_t P, int32_t topk, int32_t E, int64_t N, int64_t K, moeq_act act,
+                               moeq_dtype out_dtype, void* out, moeq_sched sched, void* stream);
+
+/* ------------------------------------------------------------------------
+ * grouped_gemm_qint8_backward - gradient of grouped_gemm_qint8 (act NONE)
+ * towards its activations, straight through their quantization; the weights
+ * are frozen:
+ *   dx[s][:] = base[s][:] + sum_n dy[s][n] * w_scale[e][n] * w[e][n][:]
+ * for every sorted row s < expert_offsets[E] of expert e.  d = dy * w_scale
+ * enters as 16-bit fixed point of its row, to half a step of max_n |d| / 32512
+ * (rows whose largest |d| is below 2^-100 count as zero); the sums over n are
+ * exact integers, joined in fp32 and rounded once.  A row whose d holds an
+ * infinity or NaN gives a row of NaN.  Equal inputs give equal bits.
+ *
+ *   dtype  F16 | BF16: the type of dy, base and dx
+ *   dy     [P][N] in SORTED order;  w, w_scale, expert_offsets as above
+ *   base   [P][K], NULL (zero), or dx itself (in place): another part of the
+ *          same gradient, such as grouped_lora_backward's dx
+ *   dx     [P][K] in SORTED order, whatever a_row was (moe_permute_backward
+ *          sums TOKEN rows; rows past expert_offsets[E] are not written)
+ *   workspace  grouped_gemm_qint8_backward_workspace_bytes(P, E, N, K) bytes,
+ *          contents on entry ignored.  Calls that may overlap in time need
+ *          their own.
+ * Requires K % 128 == 0 and N % 32 == 0 (else MOEQ_EALIGN), N < 131072 and
+ * K <= 131072, 1 <= E <= 1024, P < 2^31, 16-byte aligned pointers (4-byte for
+ * the table and w_scale), outputs disjoint from the inputs and each other, and
+ * sizes that one launch can count (else MOEQ_EINVAL).  The workspace size of
+ * arguments outside these ranges is 0.
+ * ---------------------------------------------------------------------- */
+size_t grouped_gemm_qint8_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K); /* host */
+
+moeq_status grouped_gemm_qint8_backward(const void* dy, moeq_dtype dtype, const int8_t* w, const float* w_scale,
+                                        const int32_t* expert_offsets, int64_t P, int32_t E, int64_t N, int64_t K,
+                                        const void* base, void* dx, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+/* Columns that share one scale of moe_silu_mul's checkpoint. */
+#define MOEQ_CHECKPOINT_BLOCK 128
+
+/* ------------------------------------------------------------------------
+ * moe_silu_mul - the gated activation of rows [gate | up] by itself, for
+ * projections whose columns change before it (grouped_lora beside gate+up):
+ *   h[s][i] = silu(gu[s][i]) * gu[s][I + i]
+ * in fp32, rounded once, with an optional 8-bit checkpoint of gu, which
+ * moe_silu_mul_backward reads in its place.
+ *
+ *   gu     [P][2I] dtype (F16 | BF16 | F32);  h [P][I] dtype
+ *   expert_offsets  int32 [E+1]: rows s < expert_offsets[E] are computed, the
+ *          others not written; NULL: all P rows (E is then not read)
+ *   ck     NULL, or int8 [P][2I]: codes of gu, with
+ *   cs     (NULL exactly where ck is) f32 [P][2B], B = ceil(I / 128): the
+ *          scale of each 128 columns of a row's gate (the first B) and up (the
+ *          others; the last block of either may be shorter), by
+ *          moe_quantize_int8's rule within the block
+ * Requires I % 8 == 0 (else MOEQ_EALIGN), I <= 2^20, P < 2^31, 1 <= E <= 1024
+ * with offsets, 16-byte aligned pointers (4-byte for the table and cs), and
+ * outputs disjoint from the inputs and each other (else MOEQ_EINVAL).
+ * ---------------------------------------------------------------------- */
+moeq_status moe_silu_mul(const void* gu, moeq_dtype dtype, const int32_t* expert_offsets, int32_t E, int64_t P,
+                         int64_t I, void* h, int8_t* ck, float* cs, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_silu_mul_backward - gradient of moe_silu_mul.  With g and u from gu, or
+ * from its checkpoint (code * scale), and sig = 1 / (1 + exp(-g)):
+ *   dgu[s][i]     = dh[s][i] * u * sig * (1 + g * (1 - sig))
+ *   dgu[s][I + i] = dh[s][i] * g * sig
+ * in fp32, rounded once.
+ *
+ *   dh     [P][I] dtype (F16 | BF16 | F32), dgu [P][2I] dtype
+ *   gu     [P][2I] dtype, with ck and cs NULL; or NULL, with ck and cs as
+ *          moe_silu_mul wrote them.  dgu may be gu itself (in place)
+ *   h      NULL, or [P][I] dtype that receives g * sig * u again.  With dh
+ *          and dgu NULL the call makes h alone: what the gradients of adapters
+ *          beside the next projection read, before dh exists
+ * Rows past expert_offsets[E] are not written.  Requires as moe_silu_mul, and
+ * gu or the checkpoint but not both (else MOEQ_EINVAL).
+ * ---------------------------------------------------------------------- */
+moeq_status moe_silu_mul_backward(const void* dh, moeq_dtype dtype, const void* gu, const int8_t* ck, const float* cs,
+                                  const int32_t* expert_offsets, int32_t E, int64_t P, int64_t I, void* dgu, void* h,
+                                  void* stream);
 
 /* ------------------------------------------------------------------------
  * moe_nvfp4_repack - convert NVFP4 expert weights from the layout [MMRM]

@@ -39,6 +39,8 @@ from .layer import int4_layer, int4_ffn_layer, nvfp4_layer, fp8_dense, token_row
 from .quant import quantize_int4_rows
 from .permute import permute, permute_backward, scatter_combine_backward
 from .lora import grouped_lora, grouped_lora_backward
+from .int8 import (quantize_int8, grouped_gemm_qint8, grouped_gemm_qint8_backward, checkpoint, checkpoint_values,
+                   silu_gate, silu_gate_backward)
 from .layouts import (scale_swizzle_offset, unswizzle_scales, swizzle_scales, repack_nvfp4,
                       quads_from_rows, rows_from_quads, tiles_from_rows, rows_from_tiles)
 

@@ -11,7 +11,8 @@ no fallback implementation.
 
 No call records a graph for autograd: a result never requires gradients,
 whatever its arguments do.  Where a gradient exists it is a call of its own
-(moe_permute_backward, moe_scatter_combine_backward, grouped_lora_backward).
+(moe_permute_backward, moe_scatter_combine_backward, grouped_lora_backward,
+grouped_gemm_qint8_backward, moe_silu_mul_backward).
 """
 from __future__ import annotations
 
@@ -43,12 +44,16 @@ EXPORTS = ("moeq_last_error", "moeq_abi_version", "moe_route_prep_workspace_byte
            "moe_nvfp4_repack", "moe_sum_pairs", "moe_cast_bf16_to_f16", "moe_route_prep_noalloc",
            "moe_permute", "moe_permute_backward", "moe_scatter_combine_backward",
            "grouped_lora_workspace_bytes", "grouped_lora", "grouped_lora_backward_workspace_bytes",
-           "grouped_lora_backward")
+           "grouped_lora_backward", "moe_quantize_int8", "grouped_gemm_qint8",
+           "grouped_gemm_qint8_backward_workspace_bytes", "grouped_gemm_qint8_backward", "moe_silu_mul",
+           "moe_silu_mul_backward")
 
 # Fixed device scratch of moe_route_prep_noalloc per GPU (include/moeq.h).
 ROUTE_NOALLOC_SCRATCH_BYTES = 1 << 20
 # int32 counters of grouped_gemm_qnvfp4's optional work queue (include/moeq.h).
 WORK_QUEUE_INTS = 16
+# Columns that share a scale of moe_silu_mul's checkpoint (include/moeq.h).
+CHECKPOINT_BLOCK = 128
 
 
 def work_queue(device="cuda"):
@@ -101,6 +106,13 @@ def lib():
         "grouped_lora_backward_workspace_bytes": (sz, [i64, i32, i64, i64, i32]),
         "grouped_lora_backward": (i32, [vp, i32, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, i64, i32, i32, i64,
                                         i64, i32, vp, vp, vp, vp, sz, vp]),
+        "moe_quantize_int8": (i32, [vp, i32, i64, i64, vp, vp, vp]),
+        "grouped_gemm_qint8": (i32, [vp, vp, i64, i32, vp, vp, vp, vp, i64, i32, i32, i64, i64, i32, i32, vp, i32,
+                                     vp]),
+        "grouped_gemm_qint8_backward_workspace_bytes": (sz, [i64, i32, i64, i64]),
+        "grouped_gemm_qint8_backward": (i32, [vp, i32, vp, vp, vp, i64, i32, i64, i64, vp, vp, vp, sz, vp]),
+        "moe_silu_mul": (i32, [vp, i32, vp, i32, i64, i64, vp, vp, vp, vp]),
+        "moe_silu_mul_backward": (i32, [vp, i32, vp, vp, vp, vp, i32, i64, i64, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -670,3 +682,182 @@ def grouped_lora_backward(dy, x, a, b, h, expert_offsets, sorted_pair_ids, topk:
                                      db.data_ptr(), _ptr(workspace), wsb, stream)
     _check("grouped_lora_backward", st)
     return dx, da, db
+
+
+def quantize_int8_rows(x, *, q=None, scale=None):
+    """Per-row symmetric int8 codes of x [rows][K] (f16/bf16/f32): returns
+    (q int8 [rows][K], scale f32 [rows]), scale = amax/127, codes
+    rne(x * 127/amax).  A row that holds an infinity or NaN gets scale NaN."""
+    _need(x, "x", _FLOATS, 2)
+    rows, K = x.shape
+    q = _fit(q, "q", (rows, K), torch.int8, x)
+    scale = _fit(scale, "scale", (rows,), torch.float32, x)
+    stream = _here("x q scale", x, q, scale)
+    st = lib().moe_quantize_int8(x.data_ptr(), _DTYPE_CODE[x.dtype], rows, K, q.data_ptr(), scale.data_ptr(), stream)
+    _check("moe_quantize_int8", st)
+    return q, scale
+
+
+def _int8_weights(w, w_scale, expert_offsets):
+    _need(w, "w", torch.int8, 3)
+    _need(w_scale, "w_scale", torch.float32, 2)
+    _need(expert_offsets, "expert_offsets", torch.int32, 1)
+    E, N, K = w.shape
+    if w_scale.shape != (E, N) or expert_offsets.numel() != E + 1:
+        raise ValueError("inconsistent INT8 weight shapes: w [E][N][K], w_scale [E][N], expert_offsets [E+1]")
+    return E, N, K
+
+
+def grouped_gemm_qint8(a, a_scale, w, w_scale, expert_offsets, sorted_pair_ids, topk: int, *, a_row="token",
+                       act="none", out_dtype=torch.float16, out=None, P=None, sched="auto"):
+    """W8A8 INT8 grouped GEMM: a int8 [rows_a][K], a_scale f32 [rows_a], w int8
+    [E][N][K], w_scale f32 [E][N].  Returns out [P][N] (act 'none') or [P][N/2]
+    ('silu_mul'); out_dtype torch.int32 gives the raw accumulators.  Rows past
+    expert_offsets[E] are not written.  Not recorded by autograd: the gradient
+    towards the activations is grouped_gemm_qint8_backward."""
+    _need(a, "a", torch.int8, 2)
+    _need(a_scale, "a_scale", torch.float32, 1)
+    E, N, K = _int8_weights(w, w_scale, expert_offsets)
+    rows = a.shape[0]
+    if sorted_pair_ids is not None:
+        _need(sorted_pair_ids, "sorted_pair_ids", torch.int32, 1)
+    if P is None:
+        P = rows if sorted_pair_ids is None else sorted_pair_ids.numel()
+    elif sorted_pair_ids is not None and sorted_pair_ids.numel() < P:
+        raise ValueError(f"sorted_pair_ids needs {P} entries")
+    if a.shape[1] != K or a_scale.numel() != rows:
+        raise ValueError("inconsistent INT8 operand shapes: a [rows][K], a_scale [rows], w [E][N][K]")
+    if out_dtype not in _DTYPE_CODE:
+        raise TypeError(f"out_dtype {out_dtype} is not a type of the library")
+    out = _out(out, P, N // 2 if act == "silu_mul" else N, out_dtype, a.device)
+    stream = _here("a a_scale w w_scale expert_offsets sorted_pair_ids out", a, a_scale, w, w_scale, expert_offsets,
+                   sorted_pair_ids, out)
+    st = lib().grouped_gemm_qint8(a.data_ptr(), a_scale.data_ptr(), rows, AROW[a_row], w.data_ptr(),
+                                  w_scale.data_ptr(), expert_offsets.data_ptr(), _ptr(sorted_pair_ids), P, topk, E, N,
+                                  K, ACT[act], _DTYPE_CODE[out_dtype], out.data_ptr(), SCHED[sched], stream)
+    _check("grouped_gemm_qint8", st)
+    return out
+
+
+def qint8_backward_workspace_bytes(P: int, E: int, N: int, K: int) -> int:
+    return int(lib().grouped_gemm_qint8_backward_workspace_bytes(P, E, N, K))
+
+
+def grouped_gemm_qint8_backward(dy, w, w_scale, expert_offsets, *, base=None, dx=None, workspace=None):
+    """Gradient of grouped_gemm_qint8 (act 'none') towards its activations,
+    straight through their quantization: dx[s] = base[s] + sum_n dy[s][n] *
+    w_scale[e][n] * w[e][n] for every sorted row s of expert e.
+
+    dy f16 or bf16 [P][N] in sorted order; w, w_scale and expert_offsets as in
+    the forward call; base [P][K] (None: zero; the same tensor as dx: in place)
+    another part of the same gradient, such as grouped_lora_backward's dx.
+    Returns dx [P][K] in sorted order, rows past expert_offsets[E] not written;
+    moe_permute_backward sums it over each token's slots.  The products see
+    16 bits of dy * w_scale relative to its row's largest.  workspace: uint8,
+    qint8_backward_workspace_bytes(P, E, N, K)."""
+    _need(dy, "dy", _HALVES, 2)
+    E, N, K = _int8_weights(w, w_scale, expert_offsets)
+    P, dt = dy.shape[0], dy.dtype
+    if dy.shape[1] != N:
+        raise ValueError(f"dy must be [P][{N}], got {list(dy.shape)}")
+    if base is not None:
+        base = _fit(base, "base", (P, K), dt, dy)
+    dx = _fit(dx, "dx", (P, K), dt, dy)
+    if workspace is None:
+        wsb = qint8_backward_workspace_bytes(P, E, N, K)
+        workspace = torch.empty(wsb, dtype=torch.uint8, device=dy.device)
+    else:
+        _need(workspace, "workspace")
+        wsb = workspace.numel() * workspace.element_size()
+    stream = _here("dy w w_scale expert_offsets base dx workspace", dy, w, w_scale, expert_offsets, base, dx,
+                   workspace)
+    st = lib().grouped_gemm_qint8_backward(dy.data_ptr(), _DTYPE_CODE[dt], w.data_ptr(), w_scale.data_ptr(),
+                                           expert_offsets.data_ptr(), P, E, N, K, _ptr(base), dx.data_ptr(),
+                                           workspace.data_ptr(), wsb, stream)
+    _check("grouped_gemm_qint8_backward", st)
+    return dx
+
+
+def _silu_common(rows, cols, expert_offsets, what):
+    if cols % 2:
+        raise ValueError(f"{what} must have an even number of columns [gate | up]")
+    I = cols // 2
+    if expert_offsets is None:
+        return I, -(-I // CHECKPOINT_BLOCK), 0
+    _need(expert_offsets, "expert_offsets", torch.int32, 1)
+    return I, -(-I // CHECKPOINT_BLOCK), expert_offsets.numel() - 1
+
+
+def moe_silu_mul(gu, expert_offsets=None, *, checkpoint=False, h=None, ck=None, cs=None):
+    """The gated activation by itself: h = silu(gate) * up of rows gu [P][2I] =
+    [gate | up] (f16, bf16 or f32), the rows below expert_offsets[E] (None: all
+    of them; the others are not written).
+
+    checkpoint: also keep gu in 8 bits, ck int8 [P][2I] and cs f32 [P][2B] with
+    B = ceil(I / 128): a scale for every 128 columns of gate, then of up.
+    Returns (h [P][I], ck, cs), the last two None without checkpoint.  Not
+    recorded by autograd: the gradient is moe_silu_mul_backward."""
+    _need(gu, "gu", _FLOATS, 2)
+    P, cols = gu.shape
+    I, B, E = _silu_common(P, cols, expert_offsets, "gu")
+    h = _fit(h, "h", (P, I), gu.dtype, gu)
+    if checkpoint:
+        ck = _fit(ck, "ck", (P, cols), torch.int8, gu)
+        cs = _fit(cs, "cs", (P, 2 * B), torch.float32, gu)
+    elif ck is not None or cs is not None:
+        raise ValueError("ck or cs is given, but checkpoint is false")
+    stream = _here("gu expert_offsets h ck cs", gu, expert_offsets, h, ck, cs)
+    st = lib().moe_silu_mul(gu.data_ptr(), _DTYPE_CODE[gu.dtype], _ptr(expert_offsets), E, P, I, h.data_ptr(),
+                            _ptr(ck), _ptr(cs), stream)
+    _check("moe_silu_mul", st)
+    return h, ck, cs
+
+
+def moe_silu_mul_backward(dh, expert_offsets=None, *, gu=None, ck=None, cs=None, need_h=False, dgu=None, h=None):
+    """Gradient of moe_silu_mul: dh [P][I] -> dgu [P][2I], from gu as the
+    forward call read it or from the checkpoint (ck, cs) that it wrote.  dgu
+    may be gu (in place).  need_h: also h again, from the same values.  Returns
+    (dgu, h), h None without need_h; rows past expert_offsets[E] are not
+    written."""
+    _need(dh, "dh", _FLOATS, 2)
+    P, I = dh.shape
+    dt = dh.dtype
+    _, B, E = _silu_common(P, 2 * I, expert_offsets, "dgu")
+    if (gu is None) == (ck is None) or (ck is None) != (cs is None):
+        raise ValueError("give gu, or ck and cs")
+    if gu is not None:
+        _fit(gu, "gu", (P, 2 * I), dt, dh)
+    else:
+        _fit(ck, "ck", (P, 2 * I), torch.int8, dh)
+        _fit(cs, "cs", (P, 2 * B), torch.float32, dh)
+    dgu = _fit(dgu, "dgu", (P, 2 * I), dt, dh)
+    if need_h:
+        h = _fit(h, "h", (P, I), dt, dh)
+    elif h is not None:
+        raise ValueError("h is given, but need_h is false")
+    stream = _here("dh expert_offsets gu ck cs dgu h", dh, expert_offsets, gu, ck, cs, dgu, h)
+    st = lib().moe_silu_mul_backward(dh.data_ptr(), _DTYPE_CODE[dt], _ptr(gu), _ptr(ck), _ptr(cs),
+                                     _ptr(expert_offsets), E, P, I, dgu.data_ptr(), _ptr(h), stream)
+    _check("moe_silu_mul_backward", st)
+    return dgu, h
+
+
+def moe_silu_mul_again(ck, cs, expert_offsets=None, *, dtype=torch.bfloat16, h=None):
+    """h = silu(gate) * up again from a checkpoint that moe_silu_mul wrote (ck
+    int8 [P][2I], cs f32 [P][2B]): what the gradients of adapters beside the
+    next projection read, before dh exists.  Returns h [P][I] of dtype (f16,
+    bf16 or f32); rows past expert_offsets[E] are not written."""
+    _need(ck, "ck", torch.int8, 2)
+    P, cols = ck.shape
+    I, B, E = _silu_common(P, cols, expert_offsets, "ck")
+    _need(cs, "cs", torch.float32, 2)
+    if cs.shape != (P, 2 * B):
+        raise ValueError(f"cs must be [{P}][{2 * B}], got {list(cs.shape)}")
+    if dtype not in _FLOATS:
+        raise TypeError(f"dtype {dtype} is not a floating type of the library")
+    h = _fit(h, "h", (P, I), dtype, ck)
+    stream = _here("ck cs expert_offsets h", ck, cs, expert_offsets, h)
+    st = lib().moe_silu_mul_backward(None, _DTYPE_CODE[dtype], None, ck.data_ptr(), cs.data_ptr(),
+                                     _ptr(expert_offsets), E, P, I, None, h.data_ptr(), stream)
+    _check("moe_silu_mul_backward", st)
+    return h

@@ -1,0 +1,792 @@
+// W8A8 INT8 grouped GEMM with per-token x per-channel scales, and its
+// gradient towards the activations.
+//
+// Forward:  acc[s][n] = sum_k a[row(s)][k] w[e][n][k]   (int32, exact)
+//           y = a_scale * w_scale * acc, optionally silu(gate) * up.
+// Gradient: dx[s][k] = sum_n dy[s][n] w_scale[e][n] w[e][n][k]  (+ base)
+// The int8 MFMA takes w as it is stored in both.  For the gradient a first
+// kernel writes d = dy * w_scale as 16-bit fixed point of its row's largest
+// value, d = step (256 hi + lo) with |256 hi + lo| <= 32512, in two int8
+// planes; both planes' products with w are exact int32 sums, joined in fp32.
+// Two int8 MFMAs take as long as one bf16 MFMA, need no conversion of w in
+// the loop, and keep 16 bits of d where a bf16 product would keep 8 after
+// the w_scale product.
+#include <algorithm>
+
+#include "int8.h"
+#include "kernels.h"
+#include "pipeline.h"
+#include "tile.h"
+#include "vec8.h"
+
+namespace moeq {
+namespace {
+
+enum Mode { NONE = 0, SILU = 1, GRAD = 2 };
+
+constexpr int kRowBytes = 64;  // K (GRAD: N) values of a row per stage
+constexpr int kBN = 256;       // output columns per tile (weight rows; GRAD: weight columns)
+constexpr int kGroupM = 4;     // m-tiles per n-tile sweep
+
+// WM x WN waves; a wave owns XO 32-row operands of the A tile and WO 32-wide
+// operands of the weight tile.  GRAD: the wave's first XO / 2 A operands are
+// the hi planes of its rows, the others the lo planes of the same rows.
+template <int WM_, int WN_, int XO_, int WO_, int STAGES_>
+struct Cfg {
+  static constexpr int WM = WM_, WN = WN_, XO = XO_, WO = WO_, kStages = STAGES_;
+  static constexpr int kWaves = WM * WN;
+  static constexpr int kThreads = 64 * kWaves;
+  static constexpr int kBM = 32 * XO * WM;                          // A tile rows
+  static constexpr int kATile = kBM * kRowBytes;
+  static constexpr int kStageBytes = kATile + kBN * kRowBytes;
+  static constexpr int kCopiesA = kBM / 16 > kWaves ? kBM / 16 / kWaves : 1;  // 1 KB copies per wave
+  static constexpr int kCopiesB = 16 / kWaves;
+  static constexpr int kCopies = kCopiesA + kCopiesB;
+  static constexpr int kAWaves = kBM / 16 / kCopiesA;               // waves with A rows of their own
+  static constexpr int kRW = 16 * kCopiesA;                         // A rows per wave
+  static constexpr int kCW = kBN / kWaves;                          // weight-scale columns per wave
+  static constexpr int kScaleBytes = kWaves * 512;                  // [waves][64] row | [waves][64] column scales
+  // Tile t's scales are read at its epilogue, at the latest one stage after
+  // its last one; by then at most kStages later tiles have been issued.
+  static constexpr int kScaleBufs = kStages + 1;
+  static constexpr int kWaveCols = 32 * WO;
+  static_assert(WN * kWaveCols == kBN, "waves cover the tile");
+  static_assert(kAWaves <= kWaves && kBM % (16 * kCopiesA) == 0, "copies cover the tile");
+};
+
+typedef __attribute__((address_space(4))) const int cint_t;
+typedef int i32x16_a4 __attribute__((ext_vector_type(16), aligned(4)));
+typedef __attribute__((address_space(4))) const i32x16_a4 ci32x16_t;
+// Wave-uniform reads through the constant address space (scalar loads).
+__device__ __forceinline__ int ld_uniform(const int* p, int64_t i) { return ((cint_t*)(p))[i]; }
+__device__ __forceinline__ i32x16_a4 ld_uniform16(const int* p) { return *(ci32x16_t*)(p); }
+
+// LDS rows of 64 bytes: chunk c of row r at position c ^ ((r >> 2) & 3), so
+// that 16 consecutive rows reading one chunk land on 16 bank groups.
+__device__ __forceinline__ int frag_off(int lane, int c) { return ((c ^ ((lane >> 2) & 3)) << 4); }
+// A 1 KB copy moves 16 rows: lane l lands at row l/4, position l%4.
+__device__ __forceinline__ int copy_chunk(int lane) { return ((lane & 3) ^ ((lane >> 4) & 3)) << 4; }
+
+struct TileAt {
+  int e, row0, rows, nt;
+};
+
+// Work item -> tile, wave-uniform: expert-major, and inside an expert
+// kGroupM m-tiles are visited for each n-tile before the next n-tile.
+__device__ __forceinline__ TileAt tile_at(const int* tile_start, const int* __restrict__ offsets, int E, int P,
+                                          int bm, int n_tiles, int item) {
+  int bl = 0, bh = E - 1;
+  while (bl < bh) {
+    const int mid = (bl + bh + 1) >> 1;
+    if (__builtin_amdgcn_readfirstlane(tile_start[mid]) <= item) bl = mid; else bh = mid - 1;
+  }
+  const int e = __builtin_amdgcn_readfirstlane(bl);
+  const int local = item - __builtin_amdgcn_readfirstlane(tile_start[e]);
+  const int lo = min(max(ld_uniform(offsets, e), 0), P);
+  const int hi = min(max(ld_uniform(offsets, e + 1), lo), P);
+  const int m = hi - lo;
+  const int mtiles = (m + bm - 1) / bm;
+  const int group = local / (kGroupM * n_tiles);
+  const int in_group = local - group * kGroupM * n_tiles;
+  const int gm = min(kGroupM, mtiles - group * kGroupM);
+  const int mt = group * kGroupM + in_group % gm;
+  return TileAt{e, lo + mt * bm, min(bm, m - mt * bm), in_group / gm};
+}
+
+// Expert-local weight row of tile row rb.  SILU: a wave's first half are gate
+// rows, its second half the up rows of the same columns.  Rows past N are
+// clamped (their outputs are not stored).
+template <class C, int MODE>
+__device__ __forceinline__ int weight_row(int nt, int rb, int N) {
+  if (MODE == SILU) {
+    constexpr int W = C::kWaveCols, H = W / 2;
+    const int I = N / 2;
+    int col = nt * (kBN / 2) + H * (rb / W) + rb % H;
+    if (col >= I) col = nt * (kBN / 2);
+    return (rb / H % 2) * I + col;
+  }
+  const int r = nt * kBN + rb;
+  return r < N ? r : nt * kBN;
+}
+
+typedef __attribute__((address_space(3))) v2i_t lds_v2i;
+
+template <class C>
+struct Frag {
+  v4i w[C::WO], x[C::XO];
+};
+
+// Fragments of the 32-value substep j (two per stage): lane half h holds the
+// 16 values of chunk 2j + h of its row.  GRAD: the weight tile is [64 n][256
+// k], chunk c of row n at c ^ 2(n % 8), and a transposing read gives lane i
+// of each 16 column i of the 8 x 16 block whose row i/2, half i%2 it points at.
+template <class C, int MODE>
+__device__ __forceinline__ Frag<C> read_frag(const uint8_t* As, int wm, int wn, int lane, int j) {
+  const uint8_t* Bs = As + C::kATile;
+  const int l32 = lane & 31, off = frag_off(lane, 2 * j + (lane >> 5));
+  Frag<C> f;
+  if constexpr (MODE == GRAD) {
+    const int i = lane & 15;
+    const uint8_t* row = Bs + (32 * j + 16 * (lane >> 5) + (i >> 1)) * kBN + 8 * (i & 1);
+#pragma unroll
+    for (int o = 0; o < C::WO; ++o) {
+      const int c = ((2 * (C::WO * wn + o) + ((lane >> 4) & 1)) ^ (2 * (i >> 1))) << 4;
+      const v2i_t a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + c));
+      const v2i_t b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + 8 * kBN + c));
+      f.w[o] = v4i{a[0], a[1], b[0], b[1]};
+    }
+  } else {
+#pragma unroll
+    for (int o = 0; o < C::WO; ++o)
+      f.w[o] = __builtin_bit_cast(v4i, ld16(Bs + (C::kWaveCols * wn + 32 * o + l32) * kRowBytes + off));
+  }
+#pragma unroll
+  for (int o = 0; o < C::XO; ++o)
+    f.x[o] = __builtin_bit_cast(v4i, ld16(As + (32 * C::XO * wm + 32 * o + l32) * kRowBytes + off));
+  return f;
+}
+
+template <class C>
+__device__ __forceinline__ void mma(const Frag<C>& f, v16i (&acc)[C::WO][C::XO]) {
+#pragma unroll
+  for (int wo = 0; wo < C::WO; ++wo)
+#pragma unroll
+    for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = mfma_i8_32x32x32(f.w[wo], f.x[xo], acc[wo][xo]);
+}
+
+template <int OUT>
+__device__ __forceinline__ void put4(void* out, int64_t idx, const float (&o)[4]) {
+  typedef typename OutT<OUT>::T T;
+  T* dst = static_cast<T*>(out) + idx;
+  if constexpr (sizeof(T) == 2) {
+    const u32 lo = (u32)OutT<OUT>::from(o[0]) | ((u32)OutT<OUT>::from(o[1]) << 16);
+    const u32 hi = (u32)OutT<OUT>::from(o[2]) | ((u32)OutT<OUT>::from(o[3]) << 16);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+  } else {
+    *reinterpret_cast<v4f*>(dst) = v4f{o[0], o[1], o[2], o[3]};
+  }
+}
+
+struct Int8Args {
+  const uint8_t* a;        // activations, or the hi | lo planes of d
+  const float* a_scale;    // per activation row, or step per sorted row
+  const uint8_t* w;
+  const float* w_scale;    // not read by GRAD
+  const int* offsets;
+  const int* sorted_ids;   // or null
+  const void* base;        // GRAD: added to dx, or null
+  void* out;
+  int64_t rows_a;
+  int a_sorted, topk, E, P, N, K;
+};
+
+// Epilogue of one tile: value i of accumulator [wo][xo] in lane l is weight
+// row kWaveCols wn + 32wo + 8(i/4) + 4(l/32) + i%4 of the tile and A row
+// 32(XO wm + xo) + l%32.
+template <class C, int OUT, int MODE>
+__device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int wm, int wn, int lane, const Int8Args& g,
+                                         const v16i (&acc)[C::WO][C::XO]) {
+  constexpr int kX = MODE == GRAD ? C::XO / 2 : C::XO;
+  const int h = lane >> 5, l32 = lane & 31;
+  const float* sc = sb + C::kWaves * 64;
+#pragma unroll
+  for (int xo = 0; xo < kX; ++xo) {
+    const int r = 32 * (kX * wm + xo) + l32;      // row of the tile's routed rows
+    if (r >= t.rows) continue;
+    const int ar = 32 * (C::XO * wm + xo) + l32;  // row of the A tile
+    const int64_t orow = t.row0 + r;
+    const float sa = sb[(ar / C::kRW) * 64 + ar % C::kRW];
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int m0 = 8 * qq + 4 * h;  // operand row of values 4qq .. 4qq+3
+      if constexpr (MODE == SILU) {
+        const int I = g.N / 2;
+#pragma unroll
+        for (int wo = 0; wo < C::WO / 2; ++wo) {
+          const int wl = 32 * wo + m0, col0 = t.nt * (kBN / 2) + C::kWaveCols / 2 * wn + wl;
+          if (col0 >= I) continue;
+          const int rg = C::kWaveCols * wn + wl, ru = rg + C::kWaveCols / 2;
+          const v4f sg = *reinterpret_cast<const v4f*>(sc + (rg / C::kCW) * 64 + rg % C::kCW);
+          const v4f su = *reinterpret_cast<const v4f*>(sc + (ru / C::kCW) * 64 + ru % C::kCW);
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = silu(sa * sg[i] * (float)acc[wo][xo][4 * qq + i]) *
+                   (sa * su[i] * (float)acc[wo + C::WO / 2][xo][4 * qq + i]);
+          put4<OUT>(g.out, orow * I + col0, o);
+        }
+      } else {
+#pragma unroll
+        for (int wo = 0; wo < C::WO; ++wo) {
+          const int wl = C::kWaveCols * wn + 32 * wo + m0, col0 = t.nt * kBN + wl;
+          if (col0 >= (MODE == GRAD ? g.K : g.N)) continue;
+          if constexpr (MODE == GRAD) {
+            float b[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
+            const int64_t idx = orow * g.K + col0;
+            if (g.base) {
+              const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.base) + idx);
+              const u32 v[2] = {q.x, q.y};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const u32 bits = i & 1 ? v[i >> 1] >> 16 : v[i >> 1] & 0xffffu;
+                b[i] = OUT == OUT_BF16 ? bf16_bits_to_f32(bits) : f16_bits_to_f32((uint16_t)bits);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float hi = (float)acc[wo][xo][4 * qq + i], lo = (float)acc[wo][xo + kX][4 * qq + i];
+              o[i] = __builtin_fmaf(__builtin_fmaf(hi, 256.0f, lo), sa, b[i]);
+            }
+            put4<OUT>(g.out, idx, o);
+          } else if constexpr (OUT == OUT_I32) {
+            *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + orow * g.N + col0) =
+                v4i{acc[wo][xo][4 * qq], acc[wo][xo][4 * qq + 1], acc[wo][xo][4 * qq + 2], acc[wo][xo][4 * qq + 3]};
+          } else {
+            const v4f sw = *reinterpret_cast<const v4f*>(sc + (wl / C::kCW) * 64 + wl % C::kCW);
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[wo][xo][4 * qq + i];
+            put4<OUT>(g.out, orow * g.N + col0, o);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <class C, int OUT, int MODE>
+__global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[C::kStages * C::kStageBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sbuf[C::kScaleBufs * C::kScaleBytes];
+  __shared__ int tile_start[kMaxExperts + 1];
+  __shared__ int sched_scratch[2 * kMaxWaves];
+
+  constexpr int kBMt = MODE == GRAD ? C::kBM / 2 : C::kBM;  // routed rows per tile
+  const int lane = threadIdx.x & 63;
+  const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wid / C::WN, wn = wid % C::WN;
+  const int N = g.N, K = g.K, P = g.P, E = g.E;
+  const int cols = MODE == SILU ? N / 2 : MODE == GRAD ? K : N;
+  const int n_tiles = MODE == SILU ? (cols + kBN / 2 - 1) / (kBN / 2) : (cols + kBN - 1) / kBN;
+  const int a_pitch = MODE == GRAD ? plane_pitch(N) : K;
+  const int steps = a_pitch / kRowBytes;
+  sched_build(tile_start, sched_scratch, g.offsets, E, P, kBMt, n_tiles);
+  const int total = __builtin_amdgcn_readfirstlane(tile_start[E]);
+  const int G = gridDim.x;
+  const int first = xcd_logical_id(blockIdx.x, G);
+  if (first >= total) return;
+  const int nq = ((total - first + G - 1) / G) * steps;
+
+  // ---- issue cursor: sources of the next stage to copy.  Wave w copies A
+  // rows [kRW (w % kAWaves), +kRW) and its share of the weight tile.
+  const uint8_t* pa[C::kCopiesA];
+  const uint8_t* pb[C::kCopiesB];
+  const float* psa = g.a_scale;
+  const float* psw = g.a_scale;
+  const int aw = wid % C::kAWaves;
+  const int cch = copy_chunk(lane);
+  int is_item = first, is_step = 0, is_sbuf = 0;
+  auto set_tile = [&](int item) __attribute__((always_inline)) {
+    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
+    int arow[C::kCopiesA];
+#pragma unroll
+    for (int i = 0; i < C::kCopiesA; ++i) {
+      const int r0 = C::kRW * aw + 16 * i;  // A tile row of the copy's first row
+      if constexpr (MODE == GRAD) {
+        // a copy's 16 rows lie in one 32-row operand, hence in one plane
+        const int xo = r0 / 32 % C::XO;
+        const int tok = 16 * C::XO * (r0 / (32 * C::XO)) + 32 * (xo % (C::XO / 2)) + r0 % 32 + (lane >> 2);
+        arow[i] = t.row0 + min(tok, t.rows - 1);
+        pa[i] = g.a + ((int64_t)(xo / (C::XO / 2)) * P + arow[i]) * a_pitch + cch;
+      } else {
+        int r;
+        if (g.a_sorted || g.sorted_ids == nullptr) {
+          r = t.row0 + min(r0 + (lane >> 2), t.rows - 1);
+        } else {
+          // the copy's 16 sorted ids (one 64-byte scalar load when all 16
+          // rows are in the tile); each lane picks its own
+          i32x16_a4 ids;
+          if (r0 + 16 <= t.rows) {
+            ids = ld_uniform16(g.sorted_ids + t.row0 + r0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) ids[k] = ld_uniform(g.sorted_ids, t.row0 + min(r0 + k, t.rows - 1));
+          }
+          int v = ids[0];
+#pragma unroll
+          for (int k = 1; k < 16; ++k) v = (lane >> 2) == k ? ids[k] : v;
+          r = v / g.topk;
+        }
+        arow[i] = (r < 0 || r >= g.rows_a) ? 0 : r;
+        pa[i] = g.a + (int64_t)arow[i] * a_pitch + cch;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C::kCopiesB; ++i) {
+      const int q = C::kCopiesB * wid + i;
+      if constexpr (MODE == GRAD) {
+        // rows n = 4q .. 4q+3 of the stage, 16 chunks of 16 columns each
+        const int n = 4 * q + (lane >> 4);
+        int col = t.nt * kBN + 16 * ((lane & 15) ^ (2 * (n & 7)));
+        if (col >= K) col -= kBN / 2;  // K is a multiple of 128: only the upper half may be past it
+        pb[i] = g.w + ((int64_t)t.e * N + n) * K + col;
+      } else {
+        pb[i] = g.w + ((int64_t)t.e * N + weight_row<C, MODE>(t.nt, 16 * q + (lane >> 2), N)) * K + cch;
+      }
+    }
+    // scales: lane l of the wave's A rows (row kRW aw + l % kRW was gathered by
+    // copy l % kRW / 16, whose lanes 4 (l % 16) .. +3 hold it) and weight rows
+    const int lr = lane % C::kRW, src = 4 * (lr & 15);
+    int s = __shfl(arow[0], src, 64);
+#pragma unroll
+    for (int i = 1; i < C::kCopiesA; ++i) {
+      const int v = __shfl(arow[i], src, 64);
+      s = (lr >> 4) == i ? v : s;
+    }
+    psa = g.a_scale + s;
+    if (MODE != GRAD)
+      psw = g.w_scale + (int64_t)t.e * N + weight_row<C, MODE>(t.nt, C::kCW * wid + lane % C::kCW, N);
+    else
+      psw = psa;
+  };
+  const uint32_t ring_lds = lds_addr(ring), sbuf_lds = lds_addr(sbuf);
+  auto issue = [&](int slot) __attribute__((always_inline)) {
+    const uint32_t base = ring_lds + slot * C::kStageBytes;
+    const int64_t ko = (int64_t)is_step * kRowBytes;
+#pragma unroll
+    for (int i = 0; i < C::kCopiesA; ++i) dma16(pa[i] + ko, base + (C::kCopiesA * aw + i) * 1024);
+    int64_t kb = ko;
+    if (MODE == GRAD) kb = ko * K;
+#pragma unroll
+    for (int i = 0; i < C::kCopiesB; ++i) {
+      const int q = C::kCopiesB * wid + i;
+      int64_t back = 0;
+      // the last stage of N = 64j + 32 ends inside: its rows past N meet zeros
+      // of the planes, so any row's bytes do
+      if (MODE == GRAD && q >= 8 && is_step * kRowBytes + 32 >= N) back = (int64_t)32 * K;
+      dma16(pb[i] + kb - back, base + C::kATile + q * 1024);
+    }
+    if (is_step == 0) {
+      const uint32_t sb = sbuf_lds + is_sbuf * C::kScaleBytes;
+      dma4(psa, sb + wid * 256);
+      dma4(psw, sb + C::kWaves * 256 + wid * 256);
+      is_sbuf = is_sbuf == C::kScaleBufs - 1 ? 0 : is_sbuf + 1;
+    }
+    if (++is_step == steps) {
+      is_step = 0;
+      is_item += G;
+      if (is_item < total) set_tile(is_item);
+    }
+  };
+
+  set_tile(first);
+#pragma nounroll
+  for (int s = 0; s < C::kStages && s < nq; ++s) issue(s);
+
+  v16i acc[C::WO][C::XO];
+#pragma unroll
+  for (int wo = 0; wo < C::WO; ++wo)
+#pragma unroll
+    for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = v16i{};
+
+  int ep_item = first, ep_sbuf = 0;
+  auto finish_tile = [&]() __attribute__((always_inline)) {
+    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, ep_item);
+    epilogue<C, OUT, MODE>(t, reinterpret_cast<const float*>(sbuf + ep_sbuf * C::kScaleBytes), wm, wn, lane, g, acc);
+    wait_vmcnt<0>();  // the stores leave before the next stages are counted
+#pragma unroll
+    for (int wo = 0; wo < C::WO; ++wo)
+#pragma unroll
+      for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = v16i{};
+    ep_item += G;
+    ep_sbuf = ep_sbuf == C::kScaleBufs - 1 ? 0 : ep_sbuf + 1;
+  };
+  // Stage q must have landed: the stages issued after it may stay in flight.
+  // Each is at least kCopies copies of this wave (a tile's first stage has two
+  // more: the wait is then longer than it need be, never shorter).
+  auto stage_start = [&](int q) __attribute__((always_inline)) {
+    const int after = min(nq - 1 - q, q == 0 ? C::kStages - 1 : C::kStages - 2);
+    switch (after) {
+      case 0: wait_vmcnt<0>(); break;
+      case 1: wait_vmcnt<C::kCopies>(); break;
+      case 2: wait_vmcnt<2 * C::kCopies>(); break;
+      case 3: wait_vmcnt<3 * C::kCopies>(); break;
+      case 4: wait_vmcnt<4 * C::kCopies>(); break;
+      default: wait_vmcnt<5 * C::kCopies>(); break;
+    }
+    static_assert(C::kStages <= 6, "wait table");
+    raw_barrier();  // every wave's part of stage q is in LDS; stage q-1 has been read
+    if (q >= 1 && q + C::kStages - 1 < nq) issue((unsigned)(q + C::kStages - 1) % C::kStages);
+    return ring + ((unsigned)q % C::kStages) * C::kStageBytes;
+  };
+  for (int q = 0, st = 0; q < nq; ++q) {
+    const uint8_t* As = stage_start(q);
+    mma<C>(read_frag<C, MODE>(As, wm, wn, lane, 0), acc);
+    mma<C>(read_frag<C, MODE>(As, wm, wn, lane, 1), acc);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage is read before the next barrier frees it
+    if (++st == steps) {
+      st = 0;
+      finish_tile();
+    }
+  }
+}
+
+// ------------------------------------------------------------------ decode
+// Few routed rows per expert: the weight stream is the whole cost.  The wave
+// is the unit of work: item = (at most 8 routed rows of one expert) x (16
+// weight rows; SILU: 8 gate rows and the 8 up rows of the same columns).  Per
+// K group of 128 values (one cache line of a row) a ring slot of the wave
+// holds the 16 weight rows (two whole-line copies of 8 rows, 16-byte piece p
+// of row r at p ^ ((r >> 1) & 7)) and the 8 activation rows (one copy).  The
+// item's scales ride in group 0's slot (one 4-byte-per-lane copy: lanes 0..7
+// the rows', 8..23 the weights').  Two v_mfma_i32_16x16x64_i8 per group take
+// the weights as the 16-row operand and the routed rows as the columns: lane
+// l supplies pieces 2(l/16) and 2(l/16) + 1 of row l % 16, value i of lane l
+// is weight row 4(l/16) + i and routed row l % 16.
+namespace dd {
+constexpr int kM = 8;
+constexpr int kRowsW = 16;
+constexpr int kWaves = 4;                              // waves per workgroup, independent
+constexpr int kDepth = 4;                              // K groups in flight per wave
+constexpr int kW = 0, kX = 2048, kS = 3072;            // slot regions
+constexpr int kSlot = 3328;
+constexpr int kCopies = 3;                             // per K group: 2 weight, 1 activation
+constexpr int kGroupK = 128;
+}  // namespace dd
+
+__device__ __forceinline__ void wait_decode(int n) {  // vmcnt(n * dd::kCopies)
+  static_assert(dd::kDepth == 4, "wait table");
+  if (n <= 0) wait_vmcnt<0>();
+  else if (n == 1) wait_vmcnt<dd::kCopies>();
+  else if (n == 2) wait_vmcnt<2 * dd::kCopies>();
+  else wait_vmcnt<3 * dd::kCopies>();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ v4i mfma_i8_16x16x64(v4i a, v4i b, v4i c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
+template <int OUT, int MODE>
+__global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
+  __shared__ int tile_start[kMaxExperts + 1];
+  __shared__ int sched_scratch[2 * kMaxWaves];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[dd::kWaves][dd::kDepth][dd::kSlot];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = g.N, K = g.K, P = g.P, E = g.E, I = N / 2;
+  const int n_blocks = N / dd::kRowsW;
+  sched_build(tile_start, sched_scratch, g.offsets, E, P, dd::kM, n_blocks);
+  const int total = __builtin_amdgcn_readfirstlane(tile_start[E]);
+  const int active = gridDim.x * dd::kWaves;
+  const int wid = blockIdx.x * dd::kWaves + wv;
+  const int G = K / dd::kGroupK;
+  uint8_t* myring = &ring[wv][0][0];
+  const uint32_t lb = lds_addr(myring);
+  const int l16 = lane & 15, quarter = lane >> 4;
+  const int crow = lane >> 3;  // row of a weight copy, + 8 for the second
+  const int cp0 = ((lane & 7) ^ ((crow >> 1) & 7)) << 4;
+  const int cp1 = ((lane & 7) ^ (((crow + 8) >> 1) & 7)) << 4;
+  const int wkey = (l16 >> 1) & 7;
+  const int wf0 = dd::kW + l16 * 128 + (((2 * quarter) ^ wkey) << 4);
+  const int wf1 = dd::kW + l16 * 128 + (((2 * quarter + 1) ^ wkey) << 4);
+  const int xslot = l16 < dd::kM ? l16 : 0;
+  const int xf = dd::kX + xslot * 128 + ((2 * quarter) << 4);
+
+  for (int item = wid; item < total; item += active) {
+    // m-tile major, then blocks; every field wave-uniform
+    int bl = 0, bh = E - 1;
+    while (bl < bh) {
+      const int mid = (bl + bh + 1) >> 1;
+      if (__builtin_amdgcn_readfirstlane(tile_start[mid]) <= item) bl = mid; else bh = mid - 1;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(bl);
+    const int local = item - __builtin_amdgcn_readfirstlane(tile_start[e]);
+    const int lo = min(max(ld_uniform(g.offsets, e), 0), P);
+    const int hi = min(max(ld_uniform(g.offsets, e + 1), lo), P);
+    const int mt = local / n_blocks;
+    const int nb = local - mt * n_blocks;
+    const int row0 = lo + mt * dd::kM;
+    const int rows = min(dd::kM, hi - row0);
+    int arow[dd::kM];
+#pragma unroll
+    for (int j = 0; j < dd::kM; ++j) {
+      const int sp = row0 + min(j, rows - 1);
+      const int r = (g.a_sorted || g.sorted_ids == nullptr) ? sp : ld_uniform(g.sorted_ids, sp) / g.topk;
+      arow[j] = (r < 0 || r >= g.rows_a) ? 0 : r;
+    }
+    auto wrow = [&](int rb) __attribute__((always_inline)) {
+      return MODE == SILU ? (rb < 8 ? 0 : I) + nb * 8 + (rb & 7) : nb * dd::kRowsW + rb;
+    };
+    const uint8_t* wbase = g.w + (int64_t)e * N * K;
+    const uint8_t* sw0 = wbase + (int64_t)wrow(crow) * K + cp0;
+    const uint8_t* sw1 = wbase + (int64_t)wrow(8 + crow) * K + cp1;
+    // per-lane pick among the wave-uniform rows (a select chain, no indexed
+    // register array)
+    auto pick = [&](int i) __attribute__((always_inline)) {
+      int v = arow[0];
+#pragma unroll
+      for (int j = 1; j < dd::kM; ++j) v = i == j ? arow[j] : v;
+      return v;
+    };
+    const uint8_t* sx = g.a + (int64_t)pick(lane >> 3) * K + ((lane & 7) << 4);
+    const float* ss;
+    if (lane < dd::kM) ss = g.a_scale + pick(lane);
+    else if (lane < dd::kM + dd::kRowsW) ss = g.w_scale + (int64_t)e * N + wrow(lane - dd::kM);
+    else ss = g.a_scale + arow[0];
+    auto issue = [&](int k) __attribute__((always_inline)) {
+      const uint32_t sl = lb + (uint32_t)((k % dd::kDepth) * dd::kSlot);
+      const int64_t ko = (int64_t)k * dd::kGroupK;
+      dma16_nt(sw0 + ko, sl + dd::kW);
+      dma16_nt(sw1 + ko, sl + dd::kW + 1024);
+      dma16(sx + ko, sl + dd::kX);
+      if (k == 0) dma4(ss, sl + dd::kS);
+    };
+    const int npre = G < dd::kDepth ? G : dd::kDepth;
+    for (int k = 0; k < npre; ++k) issue(k);
+    v4i acc = v4i{};
+    float sa = 0.f;
+    v4f sw = v4f{};
+    for (int k = 0; k < G; ++k) {
+      const int after = G - 1 - k;
+      wait_decode(after < dd::kDepth - 1 ? after : dd::kDepth - 1);
+      const uint8_t* sp = myring + (k % dd::kDepth) * dd::kSlot;
+      const v4i w0 = __builtin_bit_cast(v4i, ld16(sp + wf0)), w1 = __builtin_bit_cast(v4i, ld16(sp + wf1));
+      const v4i x0 = __builtin_bit_cast(v4i, ld16(sp + xf)), x1 = __builtin_bit_cast(v4i, ld16(sp + xf + 16));
+      if (k == 0) {
+        const float* s = reinterpret_cast<const float*>(sp + dd::kS);
+        sa = s[xslot];
+        sw = *reinterpret_cast<const v4f*>(s + dd::kM + 4 * quarter);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read; it may be refilled
+      if (k + dd::kDepth < G) issue(k + dd::kDepth);
+      acc = mfma_i8_16x16x64(w0, x0, acc);
+      acc = mfma_i8_16x16x64(w1, x1, acc);
+    }
+    const int64_t orow = row0 + l16;
+    if constexpr (MODE == SILU) {
+      float v[4], u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = sa * sw[i] * (float)acc[i];
+        u[i] = __shfl_xor(v[i], 32, 64);  // quarters 0, 1 hold gates, 2, 3 the ups
+      }
+      if (l16 < rows && quarter < 2) {
+        float o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = silu(v[i]) * u[i];
+        put4<OUT>(g.out, orow * I + nb * 8 + 4 * quarter, o);
+      }
+    } else if (l16 < rows) {
+      const int64_t idx = orow * N + nb * dd::kRowsW + 4 * quarter;
+      if constexpr (OUT == OUT_I32) {
+        *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + idx) = acc;
+      } else {
+        float o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[i];
+        put4<OUT>(g.out, idx, o);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------- gradient's planes
+// d[s][n] = dy[s][n] * w_scale[e][n] as step * (256 hi + lo): step = max |d| /
+// 32512, the code rne(d * (32512 / max)).  One workgroup per row; rows of at
+// most kThreadsD * 8 * kLoadsD values are held in registers, longer ones are
+// read twice.  A row whose largest value is below 2^-100 counts as zero; one
+// that holds an infinity or NaN gets step NaN, so all of its dx is NaN.
+constexpr int kThreadsD = 256;
+
+// Expert of sorted row s, by the whole wave: the number of experts that end
+// at or before it.
+__device__ __forceinline__ int expert_of(const int* __restrict__ offsets, int E, int s, int lane) {
+  int n = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    n += __popcll(__ballot(e < E && offsets[e + 1] <= s));
+  }
+  return min(n, E - 1);
+}
+
+template <int YK, int LOADS>
+__global__ __launch_bounds__(kThreadsD) void grad_planes(const void* __restrict__ dy, const float* __restrict__ w_scale,
+                                                         const int* __restrict__ offsets, int E, int P, int N,
+                                                         uint8_t* __restrict__ planes, float* __restrict__ step) {
+  __shared__ u32 wmax[kThreadsD / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+  const int n = min(max(offsets[E], 0), P), Np = plane_pitch(N);
+  for (int64_t s = blockIdx.x; s < n; s += gridDim.x) {
+    const int e = expert_of(offsets, E, (int)s, lane);
+    const float* ws = w_scale + (int64_t)e * N;
+    const int64_t base = s * N;
+    auto load = [&](int k, float (&d)[8]) __attribute__((always_inline)) {
+      float y[8], c[8];
+      load8<YK, false>(dy, base + k, y);
+      load8<OUT_F32, false>(ws, k, c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = y[j] * c[j];
+    };
+    float d[LOADS ? LOADS : 1][8];
+    u32 m = 0;
+    if constexpr (LOADS > 0) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int k = (i * kThreadsD + tid) * 8;
+        if (k < N) {
+          load(k, d[i]);
+          m = max(m, amax_bits(d[i]));
+        }
+      }
+    } else {
+      for (int k = tid * 8; k < N; k += kThreadsD * 8) {
+        load(k, d[0]);
+        m = max(m, amax_bits(d[0]));
+      }
+    }
+    m = wave_max(m);
+    if (lane == 0) wmax[wid] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreadsD / 64; ++w) m = max(m, wmax[w]);
+    __syncthreads();  // wmax is reused by the next row
+    const Scale c = scale_of(m, 32512.0f, 0x1p-100f);
+    uint8_t* hi = planes + s * Np;
+    uint8_t* lo = hi + (int64_t)P * Np;
+    auto put = [&](int k, const float (&v)[8]) __attribute__((always_inline)) {
+      u32 h[2] = {0, 0}, l[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int q = code_of(v[j], c.recip, 32512.0f);
+        h[j >> 2] |= ((u32)((q + 128) >> 8) & 255u) << (8 * (j & 3));
+        l[j >> 2] |= ((u32)q & 255u) << (8 * (j & 3));
+      }
+      *reinterpret_cast<uint2*>(hi + k) = make_uint2(h[0], h[1]);
+      *reinterpret_cast<uint2*>(lo + k) = make_uint2(l[0], l[1]);
+    };
+    if constexpr (LOADS > 0) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int k = (i * kThreadsD + tid) * 8;
+        if (k < N) put(k, d[i]);
+      }
+    } else {
+      for (int k = tid * 8; k < N; k += kThreadsD * 8) {
+        load(k, d[0]);
+        put(k, d[0]);
+      }
+    }
+    if (tid < (Np - N) / 8) {  // the planes' zeros up to a whole stage
+      *reinterpret_cast<uint2*>(hi + N + 8 * tid) = make_uint2(0, 0);
+      *reinterpret_cast<uint2*>(lo + N + 8 * tid) = make_uint2(0, 0);
+    }
+    if (tid == 0) step[s] = c.scale;
+  }
+}
+
+// ------------------------------------------------------------------ launch
+typedef Cfg<2, 4, 4, 2, 4> Large;   // 256 rows
+typedef Cfg<2, 4, 2, 2, 5> Medium;  // 128 rows
+typedef Cfg<2, 4, 1, 2, 6> Small;   // 64 rows (GRAD: an operand for each plane needs XO >= 2)
+typedef Cfg<1, 8, 2, 1, 6> SmallGrad;
+
+template <class C, int OUT, int MODE>
+hipError_t go_tiles(const Int8Args& g, int num_cus, hipStream_t stream) {
+  const int bm = MODE == GRAD ? C::kBM / 2 : C::kBM;
+  // upper bound on tiles: every expert adds at most one partial m-tile
+  const int64_t mt = (g.P + (int64_t)bm - 1) / bm + std::min(g.E, g.P);
+  const int64_t nt = MODE == SILU ? (g.N / 2 + kBN / 2 - 1) / (kBN / 2) : ((MODE == GRAD ? g.K : g.N) + kBN - 1) / kBN;
+  if (mt * nt == 0) return hipSuccess;
+  const int grid = (int)std::min<int64_t>(mt * nt, num_cus);
+  hipLaunchKernelGGL((int8_tiles<C, OUT, MODE>), dim3(grid), dim3(C::kThreads), 0, stream, g);
+  return hipGetLastError();
+}
+
+template <int OUT, int MODE>
+hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
+  if (g.P == 0) return hipSuccess;
+  const int64_t per = g.P / g.E;
+  if (sched == 1 || (sched == 0 && per < 16)) {
+    hipLaunchKernelGGL((int8_decode<OUT, MODE>), dim3(num_cus * 2), dim3(64 * dd::kWaves), 0, stream, g);
+    return hipGetLastError();
+  }
+  if (per <= 64) return go_tiles<Small, OUT, MODE>(g, num_cus, stream);
+  if (per <= 128) return go_tiles<Medium, OUT, MODE>(g, num_cus, stream);
+  return go_tiles<Large, OUT, MODE>(g, num_cus, stream);
+}
+
+template <int OUT>
+hipError_t go_grad(const Int8Args& g, int num_cus, hipStream_t stream) {
+  const int64_t per = g.P / g.E;
+  if (per <= 32) return go_tiles<SmallGrad, OUT, GRAD>(g, num_cus, stream);
+  if (per <= 64) return go_tiles<Medium, OUT, GRAD>(g, num_cus, stream);
+  return go_tiles<Large, OUT, GRAD>(g, num_cus, stream);
+}
+
+Int8Args int8_args(const GroupedArgs& g, const void* a, const float* a_scale, const int8_t* w, const float* w_scale) {
+  return Int8Args{static_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(w), w_scale, g.offsets,
+                  g.sorted_ids, nullptr, g.out, g.rows_a, g.a_sorted, g.topk, g.E, (int)g.P, g.N, g.K};
+}
+
+}  // namespace
+
+hipError_t launch_gemm_int8(const GroupedArgs& g, const int8_t* a, const float* a_scale, const int8_t* w,
+                            const float* w_scale, hipStream_t stream) {
+  const Int8Args k = int8_args(g, a, a_scale, w, w_scale);
+  if (g.silu_mul) {
+    switch (g.out_kind) {
+      case OUT_F16: return go<OUT_F16, SILU>(k, g.sched, g.num_cus, stream);
+      case OUT_BF16: return go<OUT_BF16, SILU>(k, g.sched, g.num_cus, stream);
+      default: return go<OUT_F32, SILU>(k, g.sched, g.num_cus, stream);
+    }
+  }
+  switch (g.out_kind) {
+    case OUT_F16: return go<OUT_F16, NONE>(k, g.sched, g.num_cus, stream);
+    case OUT_BF16: return go<OUT_BF16, NONE>(k, g.sched, g.num_cus, stream);
+    case OUT_I32: return go<OUT_I32, NONE>(k, g.sched, g.num_cus, stream);
+    default: return go<OUT_F32, NONE>(k, g.sched, g.num_cus, stream);
+  }
+}
+
+// Work items and the stages that one workgroup counts stay below 2^30.
+bool int8_fits(int64_t P, int E, int64_t N, int64_t K) {
+  const int64_t items = (P / dd::kM + E) * (N / dd::kRowsW), tiles = (P / Small::kBM + E) * (N / (kBN / 2) + 1);
+  return items < (1 << 30) && (tiles / 64 + 1) * (K / kRowBytes) < (1 << 30);
+}
+bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K) {
+  const int64_t tiles = (P / (SmallGrad::kBM / 2) + E) * (K / kBN + 1);
+  return tiles < (1 << 30) && (tiles / 64 + 1) * (plane_pitch((int)N) / kRowBytes) < (1 << 30);
+}
+
+size_t int8_bwd_workspace_bytes(int64_t P, int N) { return (size_t)P * (2 * plane_pitch(N) + 4); }
+
+hipError_t launch_gemm_int8_bwd(const GroupedArgs& g, const void* dy, const int8_t* w, const float* w_scale,
+                                const void* base, void* ws, hipStream_t stream) {
+  if (g.P == 0) return hipSuccess;
+  const int P = (int)g.P;
+  uint8_t* planes = static_cast<uint8_t*>(ws);
+  float* step = reinterpret_cast<float*>(planes + 2 * g.P * plane_pitch(g.N));
+  const int grid = std::min(P, g.num_cus * 8);
+  const bool bf = g.out_kind == OUT_BF16;
+#define MOEQ_PLANES(LOADS)                                                                                       \
+  do {                                                                                                           \
+    if (bf)                                                                                                      \
+      hipLaunchKernelGGL((grad_planes<OUT_BF16, LOADS>), dim3(grid), dim3(kThreadsD), 0, stream, dy, w_scale,    \
+                         g.offsets, g.E, P, g.N, planes, step);                                                  \
+    else                                                                                                         \
+      hipLaunchKernelGGL((grad_planes<OUT_F16, LOADS>), dim3(grid), dim3(kThreadsD), 0, stream, dy, w_scale,     \
+                         g.offsets, g.E, P, g.N, planes, step);                                                  \
+  } while (0)
+  if (g.N <= kThreadsD * 8 * 4) MOEQ_PLANES(4);
+  else if (g.N <= kThreadsD * 8 * 16) MOEQ_PLANES(16);
+  else MOEQ_PLANES(0);
+#undef MOEQ_PLANES
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  Int8Args k = int8_args(g, planes, step, w, w_scale);
+  k.base = base;
+  return bf ? go_grad<OUT_BF16>(k, g.num_cus, stream) : go_grad<OUT_F16>(k, g.num_cus, stream);
+}
+
+}  // namespace moeq

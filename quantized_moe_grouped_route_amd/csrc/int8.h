@@ -1,0 +1,58 @@
+// Symmetric 8- and 16-bit codes of fp32 values, shared by the INT8 kernels.
+#pragma once
+
+#include "common.h"
+
+namespace moeq {
+
+typedef int v2i_t __attribute__((ext_vector_type(2)));
+
+// Bytes of one row of a gradient's plane: N up to whole 64-value stages.
+__host__ __device__ __forceinline__ int plane_pitch(int N) { return (N + 63) / 64 * 64; }
+
+// g * sigmoid(g) with the hardware reciprocal (about 1 ulp) in place of an
+// IEEE division, far below the rounding of what it enters.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+__device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
+
+// Largest magnitude as fp32 bits: as integers, an infinity or NaN is above
+// every finite value, so it is never lost in a maximum.
+__device__ __forceinline__ u32 amax_bits(const float (&v)[8]) {
+  u32 m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  return m;
+}
+__device__ __forceinline__ u32 wave_max(u32 m) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = max(m, (u32)__shfl_xor((int)m, o, 64));
+  return m;
+}
+
+// Scale of symmetric codes up to `top` for values of largest magnitude m, and
+// the factor that makes codes of them: each one fp32 division.  m below
+// `tiny`: scale 1, codes 0.  m an infinity or NaN: scale NaN, so what is made
+// of the codes (then without meaning) shows it.
+struct Scale {
+  float scale, recip;
+};
+__device__ __forceinline__ Scale scale_of(u32 m_bits, float top, float tiny) {
+  const float m = __uint_as_float(m_bits);
+  if (m_bits >= 0x7f800000u) return Scale{__uint_as_float(0x7fc00000u), 0.0f};
+  if (m < tiny) return Scale{1.0f, 0.0f};
+  return Scale{m / top, top / m};
+}
+// rne(v * recip) within [-top, top].
+__device__ __forceinline__ int code_of(float v, float recip, float top) {
+  return (int)fminf(fmaxf(__builtin_rintf(v * recip), -top), top);
+}
+
+// int8 codes of 8 values, packed in order.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float recip) {
+  u32 w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j >> 2] |= ((u32)code_of(v[j], recip, 127.0f) & 255u) << (8 * (j & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+}  // namespace moeq

@@ -76,6 +76,31 @@ hipError_t launch_gemm_fp8(const GroupedArgs& g, const uint8_t* a, const float* 
 hipError_t launch_gemm_nvfp4(const GroupedArgs& g, const uint16_t* x, const uint8_t* w,
                              const uint8_t* w_sf, const float* w_gscale, hipStream_t stream);
 
+// W8A8: whether every launch of these sizes fits, the GEMM, and its gradient
+// towards the activations (GroupedArgs: offsets, E, P, N, K, out = dx and its
+// kind, which is dy's; the other fields are not read).
+bool int8_fits(int64_t P, int E, int64_t N, int64_t K);
+bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K);
+hipError_t launch_gemm_int8(const GroupedArgs& g, const int8_t* a, const float* a_scale, const int8_t* w,
+                            const float* w_scale, hipStream_t stream);
+size_t int8_bwd_workspace_bytes(int64_t P, int N);
+hipError_t launch_gemm_int8_bwd(const GroupedArgs& g, const void* dy, const int8_t* w, const float* w_scale,
+                                const void* base, void* ws, hipStream_t stream);
+
+// Per-row symmetric INT8 quantization (x_kind: OutKind of the input).
+hipError_t launch_quant_int8(const void* x, int x_kind, int64_t rows, int K, int8_t* q, float* scale, int num_cus,
+                             hipStream_t stream);
+
+// h = silu(gate) * up of rows [gate | up]; ck, cs: null, or the 8-bit
+// checkpoint.  offsets null: all P rows, else the first offsets[E].  Its
+// gradient reads gu, or the checkpoint where ck is given; h null: not written;
+// dh and dgu null: h alone.
+hipError_t launch_silu_mul(const void* gu, int kind, const int* offsets, int E, int64_t P, int I, void* h, int8_t* ck,
+                           float* cs, int num_cus, hipStream_t stream);
+hipError_t launch_silu_mul_bwd(const void* dh, int kind, const void* gu, const int8_t* ck, const float* cs,
+                               const int* offsets, int E, int64_t P, int I, void* dgu, void* h, int num_cus,
+                               hipStream_t stream);
+
 // Low-rank adapters beside a projection, rows grouped by adapter.
 struct LoraArgs {
   const int* offsets;       // [E+1]

@@ -202,6 +202,23 @@ moeq::LoraArgs lora_args(moeq_dtype dtype, int a_row, const float* scale, const 
   return g;
 }
 
+bool int8_bwd_sizes_ok(int64_t P, int32_t E, int64_t N, int64_t K) {
+  return P >= 0 && P < (int64_t(1) << 31) && E >= 1 && E <= kMaxE && N >= 32 && N < (1 << 17) && N % 32 == 0 &&
+         K >= 128 && K <= (1 << 17) && K % 128 == 0 && moeq::int8_bwd_fits(P, E, N, K);
+}
+
+// Checks shared by moe_silu_mul and its gradient.
+moeq_status check_silu(const char* fn, moeq_dtype dtype, const int32_t* offsets, int32_t E, int64_t P, int64_t I) {
+  if (!float_dtype(dtype)) return fail(MOEQ_EUNSUPPORTED, "%s: dtype %d", fn, dtype);
+  if (offsets && (E < 1 || E > kMaxE)) return fail(MOEQ_EINVAL, "%s: E=%d outside [1, %d]", fn, E, kMaxE);
+  if (P < 0 || P >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: P=%lld out of range", fn, (long long)P);
+  if (I <= 0 || I > (1 << 20)) return fail(MOEQ_EINVAL, "%s: I=%lld out of range", fn, (long long)I);
+  if (I % 8 != 0) return fail(MOEQ_EALIGN, "%s: I=%lld must be a multiple of 8", fn, (long long)I);
+  if (!aligned(offsets, 4)) return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  return MOEQ_OK;
+}
+int64_t checkpoint_blocks(int64_t I) { return (I + MOEQ_CHECKPOINT_BLOCK - 1) / MOEQ_CHECKPOINT_BLOCK; }
+
 }  // namespace
 
 extern "C" {
@@ -561,6 +578,134 @@ moeq_status moe_quantize_int4(const void* x, moeq_dtype x_dtype, int64_t rows, i
   if (rows > 0 && (!x || !q || !scale)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
   return hip_status(moeq::launch_quant_int4(x, (int)x_dtype, rows, (int)K, q, scale, device_cus(), (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, int64_t K, int8_t* q, float* scale,
+                              void* stream) {
+  const char* fn = "moe_quantize_int8";
+  if (rows < 0 || rows >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: rows=%lld out of range", fn, (long long)rows);
+  if (K <= 0 || K > (1 << 24)) return fail(MOEQ_EINVAL, "%s: K=%lld out of range", fn, (long long)K);
+  if (K % 16 != 0) return fail(MOEQ_EALIGN, "%s: K=%lld must be a multiple of 16", fn, (long long)K);
+  if (!float_dtype(x_dtype)) return fail(MOEQ_EUNSUPPORTED, "%s: x dtype %d", fn, x_dtype);
+  if (rows > 0 && (!x || !q || !scale)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  const Span outs[] = {{q, rows * K}, {scale, rows * 4}}, ins[] = {{x, rows * K * float_bytes(x_dtype)}};
+  if (outputs_overlap(outs, ins)) return fail(MOEQ_EINVAL, "%s: an output overlaps x or the other output", fn);
+  return hip_status(moeq::launch_quant_int8(x, (int)x_dtype, rows, (int)K, q, scale, device_cus(), (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t rows_a, moeq_arow a_row, const int8_t* w,
+                               const float* w_scale, const int32_t* expert_offsets, const int32_t* sorted_pair_ids,
+                               int64_t P, int32_t topk, int32_t E, int64_t N, int64_t K, moeq_act act,
+                               moeq_dtype out_dtype, void* out, moeq_sched sched, void* stream) {
+  const char* fn = "grouped_gemm_qint8";
+  moeq_status st = check_grouped(fn, a, rows_a, a_row, w, expert_offsets, P, topk, E, N, K, out, 32);
+  if (st != MOEQ_OK) return st;
+  // products of at most 2^14: K < 2^17 keeps every int32 partial sum below 2^31
+  if (K >= (int64_t(1) << 17))
+    return fail(MOEQ_EINVAL, "%s: K=%lld must be below 131072 (int32 accumulator range)", fn, (long long)K);
+  if (!a_scale || !w_scale) return fail(MOEQ_EINVAL, "%s: null scale pointer", fn);
+  if (!aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(sorted_pair_ids, 4))
+    return fail(MOEQ_EALIGN, "%s: scales and tables must be 4-byte aligned", fn);
+  if (act != MOEQ_ACT_NONE && act != MOEQ_ACT_SILU_MUL) return fail(MOEQ_EUNSUPPORTED, "%s: act %d", fn, act);
+  if (!float_dtype(out_dtype) && out_dtype != MOEQ_I32)
+    return fail(MOEQ_EUNSUPPORTED, "%s: out dtype %d", fn, out_dtype);
+  if (out_dtype == MOEQ_I32 && act != MOEQ_ACT_NONE)
+    return fail(MOEQ_EUNSUPPORTED, "%s: I32 output needs act NONE", fn);
+  if (a_row == MOEQ_AROW_TOKEN && !sorted_pair_ids && rows_a < P)
+    return fail(MOEQ_EINVAL, "%s: identity rows need rows_a >= P", fn);
+  if (sched < MOEQ_SCHED_AUTO || sched > MOEQ_SCHED_PREFILL) return fail(MOEQ_EINVAL, "%s: sched %d", fn, sched);
+  if (!moeq::int8_fits(P, E, N, K))
+    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld are too large for one launch", fn, (long long)P, E,
+                (long long)N, (long long)K);
+  const int64_t cols = act == MOEQ_ACT_SILU_MUL ? N / 2 : N;
+  const Span outs[] = {{out, P * cols * (out_dtype == MOEQ_I32 ? 4 : float_bytes(out_dtype))}},
+             ins[] = {{a, rows_a * K}, {a_scale, rows_a * 4}, {w, E * N * K}, {w_scale, E * N * 4},
+                      {expert_offsets, (int64_t(E) + 1) * 4}, {sorted_pair_ids, P * 4}};
+  if (outputs_overlap(outs, ins)) return fail(MOEQ_EINVAL, "%s: out overlaps an input", fn);
+  moeq::GroupedArgs g = make_args(expert_offsets, sorted_pair_ids, rows_a, a_row, P, topk, E, N, K,
+                                  act == MOEQ_ACT_SILU_MUL, out_dtype, out, sched);
+  return hip_status(moeq::launch_gemm_int8(g, a, a_scale, w, w_scale, (hipStream_t)stream), fn);
+}
+
+size_t grouped_gemm_qint8_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K) {
+  return int8_bwd_sizes_ok(P, E, N, K) ? moeq::int8_bwd_workspace_bytes(P, (int)N) : 0;
+}
+
+moeq_status grouped_gemm_qint8_backward(const void* dy, moeq_dtype dtype, const int8_t* w, const float* w_scale,
+                                        const int32_t* expert_offsets, int64_t P, int32_t E, int64_t N, int64_t K,
+                                        const void* base, void* dx, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  const char* fn = "grouped_gemm_qint8_backward";
+  if (dtype != MOEQ_F16 && dtype != MOEQ_BF16) return fail(MOEQ_EUNSUPPORTED, "%s: dtype %d", fn, dtype);
+  if (E < 1 || E > kMaxE) return fail(MOEQ_EINVAL, "%s: E=%d outside [1, %d]", fn, E, kMaxE);
+  if (P < 0 || P >= (int64_t(1) << 31)) return fail(MOEQ_EINVAL, "%s: P=%lld out of range", fn, (long long)P);
+  // |plane| * |w| <= 2^14: N < 2^17 keeps every int32 partial sum below 2^31
+  if (N <= 0 || K <= 0 || N >= (1 << 17) || K > (1 << 17))
+    return fail(MOEQ_EINVAL, "%s: N=%lld K=%lld out of range", fn, (long long)N, (long long)K);
+  if (K % 128 != 0) return fail(MOEQ_EALIGN, "%s: K=%lld must be a multiple of 128", fn, (long long)K);
+  if (N % 32 != 0) return fail(MOEQ_EALIGN, "%s: N=%lld must be a multiple of 32", fn, (long long)N);
+  if (!int8_bwd_sizes_ok(P, E, N, K))
+    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld are too large for one launch", fn, (long long)P, E,
+                (long long)N, (long long)K);
+  if (!w || !w_scale || !expert_offsets || (P > 0 && (!dy || !dx))) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(base, 16) || !aligned(dx, 16) || !aligned(workspace, 16) ||
+      !aligned(w_scale, 4) || !aligned(expert_offsets, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  const size_t need = moeq::int8_bwd_workspace_bytes(P, (int)N);
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
+  const Span outs[] = {{dx, P * K * 2}, {workspace, (int64_t)need}},
+             ins[] = {{base == dx ? nullptr : base, P * K * 2}, {dy, P * N * 2}, {w, E * N * K}, {w_scale, E * N * 4},
+                      {expert_offsets, (int64_t(E) + 1) * 4}};
+  if (outputs_overlap(outs, ins))
+    return fail(MOEQ_EINVAL, "%s: dx or the workspace overlaps another argument (base may be dx itself)", fn);
+  moeq::GroupedArgs g = make_args(expert_offsets, nullptr, P, MOEQ_AROW_SORTED, P, 1, E, N, K, false, dtype, dx,
+                                  MOEQ_SCHED_AUTO);
+  return hip_status(moeq::launch_gemm_int8_bwd(g, dy, w, w_scale, base, workspace, (hipStream_t)stream), fn);
+}
+
+moeq_status moe_silu_mul(const void* gu, moeq_dtype dtype, const int32_t* expert_offsets, int32_t E, int64_t P,
+                         int64_t I, void* h, int8_t* ck, float* cs, void* stream) {
+  const char* fn = "moe_silu_mul";
+  moeq_status st = check_silu(fn, dtype, expert_offsets, E, P, I);
+  if (st != MOEQ_OK) return st;
+  if ((ck == nullptr) != (cs == nullptr)) return fail(MOEQ_EINVAL, "%s: ck and cs go together", fn);
+  if (P > 0 && (!gu || !h)) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
+  if (!aligned(gu, 16) || !aligned(h, 16) || !aligned(ck, 16) || !aligned(cs, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  const int64_t hb = P * I * float_bytes(dtype);
+  const Span outs[] = {{h, hb}, {ck, 2 * P * I}, {cs, 8 * P * checkpoint_blocks(I)}},
+             ins[] = {{gu, 2 * hb}, {expert_offsets, (int64_t(E) + 1) * 4}};
+  if (outputs_overlap(outs, ins)) return fail(MOEQ_EINVAL, "%s: an output overlaps an input or another output", fn);
+  return hip_status(moeq::launch_silu_mul(gu, (int)dtype, expert_offsets, E, P, (int)I, h, ck, cs, device_cus(),
+                                          (hipStream_t)stream),
+                    fn);
+}
+
+moeq_status moe_silu_mul_backward(const void* dh, moeq_dtype dtype, const void* gu, const int8_t* ck, const float* cs,
+                                  const int32_t* expert_offsets, int32_t E, int64_t P, int64_t I, void* dgu, void* h,
+                                  void* stream) {
+  const char* fn = "moe_silu_mul_backward";
+  moeq_status st = check_silu(fn, dtype, expert_offsets, E, P, I);
+  if (st != MOEQ_OK) return st;
+  if ((ck == nullptr) != (cs == nullptr)) return fail(MOEQ_EINVAL, "%s: ck and cs go together", fn);
+  if (gu && ck) return fail(MOEQ_EINVAL, "%s: gu or its checkpoint, not both", fn);
+  if (P > 0 && (!dh != !dgu || (!dgu && !h) || (!gu && !ck)))
+    return fail(MOEQ_EINVAL, "%s: null pointer (only dh and dgu together, with h)", fn);
+  if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(ck, 16) || !aligned(dgu, 16) || !aligned(h, 16) ||
+      !aligned(cs, 4))
+    return fail(MOEQ_EALIGN, "%s: pointers misaligned", fn);
+  const int64_t hb = P * I * float_bytes(dtype);
+  const Span outs[] = {{dgu, 2 * hb}, {h, hb}},
+             ins[] = {{dh, hb}, {gu == dgu ? nullptr : gu, 2 * hb}, {ck, 2 * P * I},
+                      {cs, 8 * P * checkpoint_blocks(I)}, {expert_offsets, (int64_t(E) + 1) * 4}};
+  if (outputs_overlap(outs, ins))
+    return fail(MOEQ_EINVAL, "%s: an output overlaps an input or the other output (dgu may be gu itself)", fn);
+  return hip_status(moeq::launch_silu_mul_bwd(dh, (int)dtype, gu, ck, cs, expert_offsets, E, P, (int)I, dgu, h,
+                                              device_cus(), (hipStream_t)stream),
                     fn);
 }
 
