@@ -12,6 +12,7 @@
 // the loop, and keep 16 bits of d where a bf16 product would keep 8 after
 // the w_scale product.
 #include <algorithm>
+#include <type_traits>
 
 #include "int8.h"
 #include "kernels.h"
@@ -24,11 +25,11 @@ namespace {
 
 enum Mode { NONE = 0, SILU = 1, GRAD = 2 };
 
-constexpr int kRowBytes = 64;  // K (GRAD: N) values of a row per stage
-constexpr int kBN = 256;       // output columns per tile (weight rows; GRAD: weight columns)
-constexpr int kGroupM = 4;     // m-tiles per n-tile sweep
+constexpr int kRowBytes = 128;  // K (GRAD: N) values of a row per stage: one cache line
+constexpr int kBN = 256;        // output columns per tile (weight rows; GRAD: weight columns)
+constexpr int kGroupM = 4;      // m-tiles per n-tile sweep
 
-// WM x WN waves; a wave owns XO 32-row operands of the A tile and WO 32-wide
+// WM x WN waves; a wave owns XO 16-row operands of the A tile and WO 16-wide
 // operands of the weight tile.  GRAD: the wave's first XO / 2 A operands are
 // the hi planes of its rows, the others the lo planes of the same rows.
 template <int WM_, int WN_, int XO_, int WO_, int STAGES_>
@@ -36,36 +37,33 @@ struct Cfg {
   static constexpr int WM = WM_, WN = WN_, XO = XO_, WO = WO_, kStages = STAGES_;
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
-  static constexpr int kBM = 32 * XO * WM;                          // A tile rows
+  static constexpr int kBM = 16 * XO * WM;                   // A tile rows
   static constexpr int kATile = kBM * kRowBytes;
   static constexpr int kStageBytes = kATile + kBN * kRowBytes;
-  static constexpr int kCopiesA = kBM / 16 > kWaves ? kBM / 16 / kWaves : 1;  // 1 KB copies per wave
-  static constexpr int kCopiesB = 16 / kWaves;
+  static constexpr int kCopiesA = kBM / 8 / kWaves;          // 1 KB copies (8 rows) per wave
+  static constexpr int kCopiesB = kBN / 8 / kWaves;
   static constexpr int kCopies = kCopiesA + kCopiesB;
-  static constexpr int kAWaves = kBM / 16 / kCopiesA;               // waves with A rows of their own
-  static constexpr int kRW = 16 * kCopiesA;                         // A rows per wave
-  static constexpr int kCW = kBN / kWaves;                          // weight-scale columns per wave
-  static constexpr int kScaleBytes = kWaves * 512;                  // [waves][64] row | [waves][64] column scales
-  // Tile t's scales are read at its epilogue, at the latest one stage after
-  // its last one; by then at most kStages later tiles have been issued.
+  static constexpr int kRW = 8 * kCopiesA;                   // A rows per wave
+  static constexpr int kCW = kBN / kWaves;                   // weight-scale columns per wave
+  static constexpr int kScaleBytes = kWaves * 256;           // [waves][32 row | 32 column scales]
+  // Tile t's scales are read at its epilogue, after its last stage; by then
+  // at most kStages later tiles have been issued.
   static constexpr int kScaleBufs = kStages + 1;
-  static constexpr int kWaveCols = 32 * WO;
-  static_assert(WN * kWaveCols == kBN, "waves cover the tile");
-  static_assert(kAWaves <= kWaves && kBM % (16 * kCopiesA) == 0, "copies cover the tile");
+  static constexpr int kWaveCols = 16 * WO;
+  static_assert(WN * kWaveCols == kBN && kCW <= 32 && kRW <= 32, "waves cover the tile");
+  static_assert(kCopiesA * 8 * kWaves == kBM && kCopiesB * 8 * kWaves == kBN, "copies cover the tile");
 };
 
 typedef __attribute__((address_space(4))) const int cint_t;
-typedef int i32x16_a4 __attribute__((ext_vector_type(16), aligned(4)));
-typedef __attribute__((address_space(4))) const i32x16_a4 ci32x16_t;
+typedef int i32x8_a4 __attribute__((ext_vector_type(8), aligned(4)));
+typedef __attribute__((address_space(4))) const i32x8_a4 ci32x8_t;
 // Wave-uniform reads through the constant address space (scalar loads).
 __device__ __forceinline__ int ld_uniform(const int* p, int64_t i) { return ((cint_t*)(p))[i]; }
-__device__ __forceinline__ i32x16_a4 ld_uniform16(const int* p) { return *(ci32x16_t*)(p); }
+__device__ __forceinline__ i32x8_a4 ld_uniform8(const int* p) { return *(ci32x8_t*)(p); }
 
-// LDS rows of 64 bytes: chunk c of row r at position c ^ ((r >> 2) & 3), so
-// that 16 consecutive rows reading one chunk land on 16 bank groups.
-__device__ __forceinline__ int frag_off(int lane, int c) { return ((c ^ ((lane >> 2) & 3)) << 4); }
-// A 1 KB copy moves 16 rows: lane l lands at row l/4, position l%4.
-__device__ __forceinline__ int copy_chunk(int lane) { return ((lane & 3) ^ ((lane >> 4) & 3)) << 4; }
+__device__ __forceinline__ v4i mfma_i8_16x16x64(v4i a, v4i b, v4i c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
 
 struct TileAt {
   int e, row0, rows, nt;
@@ -111,47 +109,32 @@ __device__ __forceinline__ int weight_row(int nt, int rb, int N) {
 
 typedef __attribute__((address_space(3))) v2i_t lds_v2i;
 
+// Operands of one 64-value substep j (two per stage): lane l holds row l % 16
+// and the 16 values of chunk 4j + l / 16 of its row.  LDS rows are 128 bytes,
+// chunk c of row r at c ^ ((r >> 1) & 7): 16 consecutive rows reading one chunk
+// land on 16 bank groups.
 template <class C>
-struct Frag {
-  v4i w[C::WO], x[C::XO];
-};
-
-// Fragments of the 32-value substep j (two per stage): lane half h holds the
-// 16 values of chunk 2j + h of its row.  GRAD: the weight tile is [64 n][256
-// k], chunk c of row n at c ^ 2(n % 8), and a transposing read gives lane i
-// of each 16 column i of the 8 x 16 block whose row i/2, half i%2 it points at.
-template <class C, int MODE>
-__device__ __forceinline__ Frag<C> read_frag(const uint8_t* As, int wm, int wn, int lane, int j) {
-  const uint8_t* Bs = As + C::kATile;
-  const int l32 = lane & 31, off = frag_off(lane, 2 * j + (lane >> 5));
-  Frag<C> f;
-  if constexpr (MODE == GRAD) {
-    const int i = lane & 15;
-    const uint8_t* row = Bs + (32 * j + 16 * (lane >> 5) + (i >> 1)) * kBN + 8 * (i & 1);
-#pragma unroll
-    for (int o = 0; o < C::WO; ++o) {
-      const int c = ((2 * (C::WO * wn + o) + ((lane >> 4) & 1)) ^ (2 * (i >> 1))) << 4;
-      const v2i_t a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + c));
-      const v2i_t b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + 8 * kBN + c));
-      f.w[o] = v4i{a[0], a[1], b[0], b[1]};
-    }
-  } else {
-#pragma unroll
-    for (int o = 0; o < C::WO; ++o)
-      f.w[o] = __builtin_bit_cast(v4i, ld16(Bs + (C::kWaveCols * wn + 32 * o + l32) * kRowBytes + off));
-  }
-#pragma unroll
-  for (int o = 0; o < C::XO; ++o)
-    f.x[o] = __builtin_bit_cast(v4i, ld16(As + (32 * C::XO * wm + 32 * o + l32) * kRowBytes + off));
-  return f;
+__device__ __forceinline__ v4i read_x(const uint8_t* As, int wm, int lane, int j, int o) {
+  const int r = 16 * (C::XO * wm + o) + (lane & 15);
+  return __builtin_bit_cast(v4i, ld16(As + r * kRowBytes + (((4 * j + (lane >> 4)) ^ ((lane >> 1) & 7)) << 4)));
 }
-
-template <class C>
-__device__ __forceinline__ void mma(const Frag<C>& f, v16i (&acc)[C::WO][C::XO]) {
-#pragma unroll
-  for (int wo = 0; wo < C::WO; ++wo)
-#pragma unroll
-    for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = mfma_i8_32x32x32(f.w[wo], f.x[xo], acc[wo][xo]);
+// GRAD: the weight tile is [128 n][256 k], chunk c of row n at c ^ 2(n % 8) ^
+// (n / 16 % 2); a transposing read gives lane i of each 16 column i of the
+// 8 x 16 block whose row i/2, half i%2 it points at.
+template <class C, int MODE>
+__device__ __forceinline__ v4i read_w(const uint8_t* As, int wn, int lane, int j, int o) {
+  const uint8_t* Bs = As + C::kATile;
+  if constexpr (MODE == GRAD) {
+    const int i = lane & 15, g = lane >> 4;
+    const int c = ((C::WO * wn + o) ^ (2 * (i >> 1)) ^ (g & 1)) << 4;
+    const uint8_t* row = Bs + (64 * j + 16 * g + (i >> 1)) * kBN + 8 * (i & 1) + c;
+    const v2i_t a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)row);
+    const v2i_t b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + 8 * kBN));
+    return v4i{a[0], a[1], b[0], b[1]};
+  } else {
+    const int r = C::kWaveCols * wn + 16 * o + (lane & 15);
+    return __builtin_bit_cast(v4i, ld16(Bs + r * kRowBytes + (((4 * j + (lane >> 4)) ^ ((lane >> 1) & 7)) << 4)));
+  }
 }
 
 template <int OUT>
@@ -181,73 +164,65 @@ struct Int8Args {
 };
 
 // Epilogue of one tile: value i of accumulator [wo][xo] in lane l is weight
-// row kWaveCols wn + 32wo + 8(i/4) + 4(l/32) + i%4 of the tile and A row
-// 32(XO wm + xo) + l%32.
+// row kWaveCols wn + 16wo + 4(l/16) + i of the tile and A row 16(XO wm + xo) +
+// l%16.
 template <class C, int OUT, int MODE>
 __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int wm, int wn, int lane, const Int8Args& g,
-                                         const v16i (&acc)[C::WO][C::XO]) {
+                                         const v4i (&acc)[C::WO][C::XO]) {
   constexpr int kX = MODE == GRAD ? C::XO / 2 : C::XO;
-  const int h = lane >> 5, l32 = lane & 31;
-  const float* sc = sb + C::kWaves * 64;
+  const int l16 = lane & 15, m0 = 4 * (lane >> 4);
+  const float* sc = sb + 32;
 #pragma unroll
   for (int xo = 0; xo < kX; ++xo) {
-    const int r = 32 * (kX * wm + xo) + l32;      // row of the tile's routed rows
+    const int r = 16 * (kX * wm + xo) + l16;      // row of the tile's routed rows
     if (r >= t.rows) continue;
-    const int ar = 32 * (C::XO * wm + xo) + l32;  // row of the A tile
+    const int ar = 16 * (C::XO * wm + xo) + l16;  // row of the A tile
     const int64_t orow = t.row0 + r;
     const float sa = sb[(ar / C::kRW) * 64 + ar % C::kRW];
+    if constexpr (MODE == SILU) {
+      const int I = g.N / 2;
 #pragma unroll
-    for (int qq = 0; qq < 4; ++qq) {
-      const int m0 = 8 * qq + 4 * h;  // operand row of values 4qq .. 4qq+3
-      if constexpr (MODE == SILU) {
-        const int I = g.N / 2;
+      for (int wo = 0; wo < C::WO / 2; ++wo) {
+        const int wl = 16 * wo + m0, col0 = t.nt * (kBN / 2) + C::kWaveCols / 2 * wn + wl;
+        if (col0 >= I) continue;
+        const int rg = C::kWaveCols * wn + wl, ru = rg + C::kWaveCols / 2;
+        const v4f sg = *reinterpret_cast<const v4f*>(sc + (rg / C::kCW) * 64 + rg % C::kCW);
+        const v4f su = *reinterpret_cast<const v4f*>(sc + (ru / C::kCW) * 64 + ru % C::kCW);
+        float o[4];
 #pragma unroll
-        for (int wo = 0; wo < C::WO / 2; ++wo) {
-          const int wl = 32 * wo + m0, col0 = t.nt * (kBN / 2) + C::kWaveCols / 2 * wn + wl;
-          if (col0 >= I) continue;
-          const int rg = C::kWaveCols * wn + wl, ru = rg + C::kWaveCols / 2;
-          const v4f sg = *reinterpret_cast<const v4f*>(sc + (rg / C::kCW) * 64 + rg % C::kCW);
-          const v4f su = *reinterpret_cast<const v4f*>(sc + (ru / C::kCW) * 64 + ru % C::kCW);
-          float o[4];
+        for (int i = 0; i < 4; ++i)
+          o[i] = silu(sa * sg[i] * (float)acc[wo][xo][i]) * (sa * su[i] * (float)acc[wo + C::WO / 2][xo][i]);
+        put4<OUT>(g.out, orow * I + col0, o);
+      }
+    } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = silu(sa * sg[i] * (float)acc[wo][xo][4 * qq + i]) *
-                   (sa * su[i] * (float)acc[wo + C::WO / 2][xo][4 * qq + i]);
-          put4<OUT>(g.out, orow * I + col0, o);
-        }
-      } else {
-#pragma unroll
-        for (int wo = 0; wo < C::WO; ++wo) {
-          const int wl = C::kWaveCols * wn + 32 * wo + m0, col0 = t.nt * kBN + wl;
-          if (col0 >= (MODE == GRAD ? g.K : g.N)) continue;
-          if constexpr (MODE == GRAD) {
-            float b[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
-            const int64_t idx = orow * g.K + col0;
-            if (g.base) {
-              const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.base) + idx);
-              const u32 v[2] = {q.x, q.y};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const u32 bits = i & 1 ? v[i >> 1] >> 16 : v[i >> 1] & 0xffffu;
-                b[i] = OUT == OUT_BF16 ? bf16_bits_to_f32(bits) : f16_bits_to_f32((uint16_t)bits);
-              }
-            }
+      for (int wo = 0; wo < C::WO; ++wo) {
+        const int wl = C::kWaveCols * wn + 16 * wo + m0, col0 = t.nt * kBN + wl;
+        if (col0 >= (MODE == GRAD ? g.K : g.N)) continue;
+        if constexpr (MODE == GRAD) {
+          float b[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
+          const int64_t idx = orow * g.K + col0;
+          if (g.base) {
+            const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g.base) + idx);
+            const u32 v[2] = {q.x, q.y};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float hi = (float)acc[wo][xo][4 * qq + i], lo = (float)acc[wo][xo + kX][4 * qq + i];
-              o[i] = __builtin_fmaf(__builtin_fmaf(hi, 256.0f, lo), sa, b[i]);
+              const u32 bits = i & 1 ? v[i >> 1] >> 16 : v[i >> 1] & 0xffffu;
+              b[i] = OUT == OUT_BF16 ? bf16_bits_to_f32(bits) : f16_bits_to_f32((uint16_t)bits);
             }
-            put4<OUT>(g.out, idx, o);
-          } else if constexpr (OUT == OUT_I32) {
-            *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + orow * g.N + col0) =
-                v4i{acc[wo][xo][4 * qq], acc[wo][xo][4 * qq + 1], acc[wo][xo][4 * qq + 2], acc[wo][xo][4 * qq + 3]};
-          } else {
-            const v4f sw = *reinterpret_cast<const v4f*>(sc + (wl / C::kCW) * 64 + wl % C::kCW);
-            float o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[wo][xo][4 * qq + i];
-            put4<OUT>(g.out, orow * g.N + col0, o);
           }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = __builtin_fmaf(__builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + kX][i]), sa, b[i]);
+          put4<OUT>(g.out, idx, o);
+        } else if constexpr (OUT == OUT_I32) {
+          *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + orow * g.N + col0) = acc[wo][xo];
+        } else {
+          const v4f sw = *reinterpret_cast<const v4f*>(sc + (wl / C::kCW) * 64 + wl % C::kCW);
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[wo][xo][i];
+          put4<OUT>(g.out, orow * g.N + col0, o);
         }
       }
     }
@@ -278,47 +253,45 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   const int nq = ((total - first + G - 1) / G) * steps;
 
   // ---- issue cursor: sources of the next stage to copy.  Wave w copies A
-  // rows [kRW (w % kAWaves), +kRW) and its share of the weight tile.
+  // rows [kRW w, +kRW) and weight rows (GRAD: n rows) of its own.
   const uint8_t* pa[C::kCopiesA];
   const uint8_t* pb[C::kCopiesB];
-  const float* psa = g.a_scale;
-  const float* psw = g.a_scale;
-  const int aw = wid % C::kAWaves;
-  const int cch = copy_chunk(lane);
+  const float* psc = g.a_scale;
   int is_item = first, is_step = 0, is_sbuf = 0;
   auto set_tile = [&](int item) __attribute__((always_inline)) {
     const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
     int arow[C::kCopiesA];
 #pragma unroll
     for (int i = 0; i < C::kCopiesA; ++i) {
-      const int r0 = C::kRW * aw + 16 * i;  // A tile row of the copy's first row
+      const int r0 = C::kRW * wid + 8 * i;  // A tile row of the copy's first row
+      const int chunk = dma_chunk(lane, r0 / 8);
       if constexpr (MODE == GRAD) {
-        // a copy's 16 rows lie in one 32-row operand, hence in one plane
-        const int xo = r0 / 32 % C::XO;
-        const int tok = 16 * C::XO * (r0 / (32 * C::XO)) + 32 * (xo % (C::XO / 2)) + r0 % 32 + (lane >> 2);
+        // a copy's 8 rows lie in one 16-row operand, hence in one plane
+        const int xo = r0 / 16 % C::XO;
+        const int tok = 8 * C::XO * (r0 / (16 * C::XO)) + 16 * (xo % (C::XO / 2)) + r0 % 16 + (lane >> 3);
         arow[i] = t.row0 + min(tok, t.rows - 1);
-        pa[i] = g.a + ((int64_t)(xo / (C::XO / 2)) * P + arow[i]) * a_pitch + cch;
+        pa[i] = g.a + ((int64_t)(xo / (C::XO / 2)) * P + arow[i]) * a_pitch + chunk;
       } else {
         int r;
         if (g.a_sorted || g.sorted_ids == nullptr) {
-          r = t.row0 + min(r0 + (lane >> 2), t.rows - 1);
+          r = t.row0 + min(r0 + (lane >> 3), t.rows - 1);
         } else {
-          // the copy's 16 sorted ids (one 64-byte scalar load when all 16
-          // rows are in the tile); each lane picks its own
-          i32x16_a4 ids;
-          if (r0 + 16 <= t.rows) {
-            ids = ld_uniform16(g.sorted_ids + t.row0 + r0);
+          // the copy's 8 sorted ids (one 32-byte scalar load when all 8 rows
+          // are in the tile); each lane picks its own
+          i32x8_a4 ids;
+          if (r0 + 8 <= t.rows) {
+            ids = ld_uniform8(g.sorted_ids + t.row0 + r0);
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) ids[k] = ld_uniform(g.sorted_ids, t.row0 + min(r0 + k, t.rows - 1));
+            for (int k = 0; k < 8; ++k) ids[k] = ld_uniform(g.sorted_ids, t.row0 + min(r0 + k, t.rows - 1));
           }
           int v = ids[0];
 #pragma unroll
-          for (int k = 1; k < 16; ++k) v = (lane >> 2) == k ? ids[k] : v;
+          for (int k = 1; k < 8; ++k) v = (lane >> 3) == k ? ids[k] : v;
           r = v / g.topk;
         }
         arow[i] = (r < 0 || r >= g.rows_a) ? 0 : r;
-        pa[i] = g.a + (int64_t)arow[i] * a_pitch + cch;
+        pa[i] = g.a + (int64_t)arow[i] * a_pitch + chunk;
       }
     }
 #pragma unroll
@@ -327,49 +300,50 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
       if constexpr (MODE == GRAD) {
         // rows n = 4q .. 4q+3 of the stage, 16 chunks of 16 columns each
         const int n = 4 * q + (lane >> 4);
-        int col = t.nt * kBN + 16 * ((lane & 15) ^ (2 * (n & 7)));
+        int col = t.nt * kBN + 16 * ((lane & 15) ^ (2 * (n & 7)) ^ ((n >> 4) & 1));
         if (col >= K) col -= kBN / 2;  // K is a multiple of 128: only the upper half may be past it
         pb[i] = g.w + ((int64_t)t.e * N + n) * K + col;
       } else {
-        pb[i] = g.w + ((int64_t)t.e * N + weight_row<C, MODE>(t.nt, 16 * q + (lane >> 2), N)) * K + cch;
+        pb[i] = g.w + ((int64_t)t.e * N + weight_row<C, MODE>(t.nt, 8 * q + (lane >> 3), N)) * K + dma_chunk(lane, q);
       }
     }
-    // scales: lane l of the wave's A rows (row kRW aw + l % kRW was gathered by
-    // copy l % kRW / 16, whose lanes 4 (l % 16) .. +3 hold it) and weight rows
-    const int lr = lane % C::kRW, src = 4 * (lr & 15);
+    // scales: lanes 0..31 the wave's A rows (row l of them was gathered by
+    // copy l / 8, whose lanes 8 (l % 8) .. +7 hold it), 32..63 its columns
+    const int lr = lane % C::kRW, src = 8 * (lr & 7);
     int s = __shfl(arow[0], src, 64);
 #pragma unroll
     for (int i = 1; i < C::kCopiesA; ++i) {
       const int v = __shfl(arow[i], src, 64);
-      s = (lr >> 4) == i ? v : s;
+      s = (lr >> 3) == i ? v : s;
     }
-    psa = g.a_scale + s;
-    if (MODE != GRAD)
-      psw = g.w_scale + (int64_t)t.e * N + weight_row<C, MODE>(t.nt, C::kCW * wid + lane % C::kCW, N);
-    else
-      psw = psa;
+    psc = MODE != GRAD && lane >= 32
+              ? g.w_scale + (int64_t)t.e * N + weight_row<C, MODE>(t.nt, C::kCW * wid + lane % C::kCW, N)
+              : g.a_scale + s;
   };
   const uint32_t ring_lds = lds_addr(ring), sbuf_lds = lds_addr(sbuf);
-  auto issue = [&](int slot) __attribute__((always_inline)) {
-    const uint32_t base = ring_lds + slot * C::kStageBytes;
+  // Copy i of this wave's share of the cursor's stage, into the slot at `base`.
+  auto copy = [&](uint32_t base, int i) __attribute__((always_inline)) {
     const int64_t ko = (int64_t)is_step * kRowBytes;
-#pragma unroll
-    for (int i = 0; i < C::kCopiesA; ++i) dma16(pa[i] + ko, base + (C::kCopiesA * aw + i) * 1024);
-    int64_t kb = ko;
-    if (MODE == GRAD) kb = ko * K;
-#pragma unroll
-    for (int i = 0; i < C::kCopiesB; ++i) {
-      const int q = C::kCopiesB * wid + i;
-      int64_t back = 0;
-      // the last stage of N = 64j + 32 ends inside: its rows past N meet zeros
-      // of the planes, so any row's bytes do
-      if (MODE == GRAD && q >= 8 && is_step * kRowBytes + 32 >= N) back = (int64_t)32 * K;
-      dma16(pb[i] + kb - back, base + C::kATile + q * 1024);
+    if (i < C::kCopiesA) {
+      dma16(pa[i] + ko, base + (C::kCopiesA * wid + i) * 1024);
+    } else {
+      const int q = C::kCopiesB * wid + i - C::kCopiesA;
+      int64_t kb = ko;
+      if (MODE == GRAD) {
+        kb = ko * K;
+        // rows past N meet zeros of the planes, so any row's bytes do: the
+        // last stage's rows n % 32 are there, N being a multiple of 32
+        if (is_step * kRowBytes + 4 * q >= N) kb -= (int64_t)(4 * q & ~31) * K;
+      }
+      dma16(pb[i - C::kCopiesA] + kb, base + C::kATile + q * 1024);
     }
+  };
+  // After a stage's copies: a tile's scales ride with its first stage, and the
+  // cursor moves on.  Past the last tile it goes over that tile again, into
+  // slots that nobody reads: every wave then waits for constant counts.
+  auto advance = [&]() __attribute__((always_inline)) {
     if (is_step == 0) {
-      const uint32_t sb = sbuf_lds + is_sbuf * C::kScaleBytes;
-      dma4(psa, sb + wid * 256);
-      dma4(psw, sb + C::kWaves * 256 + wid * 256);
+      dma4(psc, sbuf_lds + is_sbuf * C::kScaleBytes + wid * 256);
       is_sbuf = is_sbuf == C::kScaleBufs - 1 ? 0 : is_sbuf + 1;
     }
     if (++is_step == steps) {
@@ -378,56 +352,88 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
       if (is_item < total) set_tile(is_item);
     }
   };
+  // Stage q is there once at most `newer` later stages of this wave's copies
+  // are in flight (a scale copy among them only lengthens the wait) and every
+  // wave has said so; the stage before it has then been read by all.
+  auto arrive = [&](auto newer) __attribute__((always_inline)) {
+    wait_vmcnt<decltype(newer)::value * C::kCopies>();
+    raw_barrier();
+  };
 
   set_tile(first);
 #pragma nounroll
-  for (int s = 0; s < C::kStages && s < nq; ++s) issue(s);
-
-  v16i acc[C::WO][C::XO];
+  for (int s = 0; s < C::kStages; ++s) {
 #pragma unroll
-  for (int wo = 0; wo < C::WO; ++wo)
+    for (int i = 0; i < C::kCopies; ++i) copy(ring_lds + s * C::kStageBytes, i);
+    advance();
+  }
+  arrive(std::integral_constant<int, C::kStages - 1>());
+  const uint8_t* As = ring;
+  v4i x[C::XO], w[C::WO];
 #pragma unroll
-    for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = v16i{};
+  for (int o = 0; o < C::XO; ++o) x[o] = read_x<C>(As, wm, lane, 0, o);
+#pragma unroll
+  for (int o = 0; o < C::WO; ++o) w[o] = read_w<C, MODE>(As, wn, lane, 0, o);
 
-  int ep_item = first, ep_sbuf = 0;
-  auto finish_tile = [&]() __attribute__((always_inline)) {
-    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, ep_item);
-    epilogue<C, OUT, MODE>(t, reinterpret_cast<const float*>(sbuf + ep_sbuf * C::kScaleBytes), wm, wn, lane, g, acc);
-    wait_vmcnt<0>();  // the stores leave before the next stages are counted
+  // Per stage: the 64-value substeps 0 and 1, each WO passes over the A
+  // operands with one weight operand.  An operand's registers take its next
+  // substep's values right after its last use (weights after their pass, A
+  // operands in the last pass), so 48 registers hold the fragments.  The
+  // barrier comes after substep 1's first pass, when all of the stage has been
+  // read: the next stage's reads and the copies into this stage's slot are
+  // spread over the passes that remain.  The order is pinned: left to itself
+  // the compiler gathers the reads, and the matrix cores wait for them.
+  int slot = 0, ep_sbuf = 0;
+  for (int item = first; item < total; item += G) {
+    v4i acc[C::WO][C::XO];
 #pragma unroll
     for (int wo = 0; wo < C::WO; ++wo)
 #pragma unroll
-      for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = v16i{};
-    ep_item += G;
+      for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = v4i{};
+    int st = 0;
+    do {
+#pragma unroll
+      for (int wo = 0; wo < C::WO; ++wo) {
+#pragma unroll
+        for (int xo = 0; xo < C::XO; ++xo) {
+          acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
+          if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 1, xo);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        w[wo] = read_w<C, MODE>(As, wn, lane, 1, wo);
+      }
+#pragma unroll
+      for (int xo = 0; xo < C::XO; ++xo) {
+        acc[0][xo] = mfma_i8_16x16x64(w[0], x[xo], acc[0][xo]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      arrive(std::integral_constant<int, C::kStages - 2>());
+      const uint32_t refill = ring_lds + slot * C::kStageBytes;
+      slot = slot == C::kStages - 1 ? 0 : slot + 1;
+      As = ring + slot * C::kStageBytes;
+      w[0] = read_w<C, MODE>(As, wn, lane, 0, 0);
+      constexpr int kRest = (C::WO - 1) * C::XO;
+#pragma unroll
+      for (int wo = 1; wo < C::WO; ++wo) {
+#pragma unroll
+        for (int xo = 0; xo < C::XO; ++xo) {
+          const int m = (wo - 1) * C::XO + xo;
+          acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
+          if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 0, xo);
+#pragma unroll
+          for (int i = 0; i < C::kCopies; ++i)
+            if (i * kRest / C::kCopies == m) copy(refill, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        w[wo] = read_w<C, MODE>(As, wn, lane, 0, wo);
+      }
+      advance();
+    } while (++st < steps);
+    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
+    epilogue<C, OUT, MODE>(t, reinterpret_cast<const float*>(sbuf + ep_sbuf * C::kScaleBytes), wm, wn, lane, g, acc);
+    wait_vmcnt<0>();  // the stores leave before the next stages are counted
     ep_sbuf = ep_sbuf == C::kScaleBufs - 1 ? 0 : ep_sbuf + 1;
-  };
-  // Stage q must have landed: the stages issued after it may stay in flight.
-  // Each is at least kCopies copies of this wave (a tile's first stage has two
-  // more: the wait is then longer than it need be, never shorter).
-  auto stage_start = [&](int q) __attribute__((always_inline)) {
-    const int after = min(nq - 1 - q, q == 0 ? C::kStages - 1 : C::kStages - 2);
-    switch (after) {
-      case 0: wait_vmcnt<0>(); break;
-      case 1: wait_vmcnt<C::kCopies>(); break;
-      case 2: wait_vmcnt<2 * C::kCopies>(); break;
-      case 3: wait_vmcnt<3 * C::kCopies>(); break;
-      case 4: wait_vmcnt<4 * C::kCopies>(); break;
-      default: wait_vmcnt<5 * C::kCopies>(); break;
-    }
-    static_assert(C::kStages <= 6, "wait table");
-    raw_barrier();  // every wave's part of stage q is in LDS; stage q-1 has been read
-    if (q >= 1 && q + C::kStages - 1 < nq) issue((unsigned)(q + C::kStages - 1) % C::kStages);
-    return ring + ((unsigned)q % C::kStages) * C::kStageBytes;
-  };
-  for (int q = 0, st = 0; q < nq; ++q) {
-    const uint8_t* As = stage_start(q);
-    mma<C>(read_frag<C, MODE>(As, wm, wn, lane, 0), acc);
-    mma<C>(read_frag<C, MODE>(As, wm, wn, lane, 1), acc);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage is read before the next barrier frees it
-    if (++st == steps) {
-      st = 0;
-      finish_tile();
-    }
   }
 }
 
@@ -461,10 +467,6 @@ __device__ __forceinline__ void wait_decode(int n) {  // vmcnt(n * dd::kCopies)
   else if (n == 2) wait_vmcnt<2 * dd::kCopies>();
   else wait_vmcnt<3 * dd::kCopies>();
   asm volatile("" ::: "memory");
-}
-
-__device__ __forceinline__ v4i mfma_i8_16x16x64(v4i a, v4i b, v4i c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
 
 template <int OUT, int MODE>
@@ -686,10 +688,9 @@ __global__ __launch_bounds__(kThreadsD) void grad_planes(const void* __restrict_
 }
 
 // ------------------------------------------------------------------ launch
-typedef Cfg<2, 4, 4, 2, 4> Large;   // 256 rows
-typedef Cfg<2, 4, 2, 2, 5> Medium;  // 128 rows
-typedef Cfg<2, 4, 1, 2, 6> Small;   // 64 rows (GRAD: an operand for each plane needs XO >= 2)
-typedef Cfg<1, 8, 2, 1, 6> SmallGrad;
+typedef Cfg<2, 4, 8, 4, 2> Large;   // 256 A rows
+typedef Cfg<2, 4, 4, 4, 3> Medium;  // 128
+typedef Cfg<1, 8, 4, 2, 3> Small;   // 64
 
 template <class C, int OUT, int MODE>
 hipError_t go_tiles(const Int8Args& g, int num_cus, hipStream_t stream) {
@@ -719,7 +720,7 @@ hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
 template <int OUT>
 hipError_t go_grad(const Int8Args& g, int num_cus, hipStream_t stream) {
   const int64_t per = g.P / g.E;
-  if (per <= 32) return go_tiles<SmallGrad, OUT, GRAD>(g, num_cus, stream);
+  if (per <= 32) return go_tiles<Small, OUT, GRAD>(g, num_cus, stream);
   if (per <= 64) return go_tiles<Medium, OUT, GRAD>(g, num_cus, stream);
   return go_tiles<Large, OUT, GRAD>(g, num_cus, stream);
 }
@@ -755,7 +756,7 @@ bool int8_fits(int64_t P, int E, int64_t N, int64_t K) {
   return items < (1 << 30) && (tiles / 64 + 1) * (K / kRowBytes) < (1 << 30);
 }
 bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K) {
-  const int64_t tiles = (P / (SmallGrad::kBM / 2) + E) * (K / kBN + 1);
+  const int64_t tiles = (P / (Small::kBM / 2) + E) * (K / kBN + 1);
   return tiles < (1 << 30) && (tiles / 64 + 1) * (plane_pitch((int)N) / kRowBytes) < (1 << 30);
 }
 

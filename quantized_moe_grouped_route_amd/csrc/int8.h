@@ -7,8 +7,8 @@ namespace moeq {
 
 typedef int v2i_t __attribute__((ext_vector_type(2)));
 
-// Bytes of one row of a gradient's plane: N up to whole 64-value stages.
-__host__ __device__ __forceinline__ int plane_pitch(int N) { return (N + 63) / 64 * 64; }
+// Bytes of one row of a gradient's plane: N up to whole 128-value stages.
+__host__ __device__ __forceinline__ int plane_pitch(int N) { return (N + 127) / 128 * 128; }
 
 // g * sigmoid(g) with the hardware reciprocal (about 1 ulp) in place of an
 // IEEE division, far below the rounding of what it enters.

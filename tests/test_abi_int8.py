@@ -68,13 +68,13 @@ def _grad(L, **kw):
     (dict(P=-1), mq.EINVAL), (dict(P=2 ** 31), mq.EINVAL), (dict(N=0), mq.EINVAL), (dict(N=131072), mq.EINVAL),
     (dict(N=48), mq.EALIGN), (dict(K=64), mq.EALIGN), (dict(K=131072 + 128), mq.EINVAL), (dict(dy=None), mq.EINVAL),
     (dict(w=None), mq.EINVAL), (dict(sw=None), mq.EINVAL), (dict(off=None), mq.EINVAL), (dict(dx=None), mq.EINVAL),
-    (dict(ws=None), mq.EINVAL), (dict(wsb=16 * (2 * 64 + 4) - 1), mq.EINVAL), (dict(dy=at(0) + 8), mq.EALIGN),
+    (dict(ws=None), mq.EINVAL), (dict(wsb=16 * (2 * 128 + 4) - 1), mq.EINVAL), (dict(dy=at(0) + 8), mq.EALIGN),
     (dict(base=at(4) + 8), mq.EALIGN), (dict(dx=at(5) + 2), mq.EALIGN), (dict(ws=at(6) + 4), mq.EALIGN),
     (dict(sw=at(2) + 2), mq.EALIGN), (dict(off=at(3) + 2), mq.EALIGN), (dict(dx=at(0)), mq.EINVAL),
     (dict(dx=at(1)), mq.EINVAL), (dict(dx=at(2)), mq.EINVAL), (dict(dx=at(3)), mq.EINVAL),
     (dict(dx=at(4) + 16), mq.EINVAL), (dict(dx=at(4) - 16), mq.EINVAL), (dict(ws=at(0)), mq.EINVAL),
     (dict(ws=at(3)), mq.EINVAL), (dict(ws=at(4)), mq.EINVAL), (dict(ws=at(5)), mq.EINVAL),
-    (dict(ws=at(5) - 16 * (2 * 64 + 4) + 16), mq.EINVAL), (dict(P=2 ** 31 - 1, K=131072, wsb=1 << 60), mq.EINVAL),
+    (dict(ws=at(5) - 16 * (2 * 128 + 4) + 16), mq.EINVAL), (dict(P=2 ** 31 - 1, K=131072, wsb=1 << 60), mq.EINVAL),
 ])
 def test_gemm_backward_rejects(L, kw, status):
     assert _grad(L, **kw) == status
@@ -83,8 +83,9 @@ def test_gemm_backward_rejects(L, kw, status):
 
 def test_gemm_backward_workspace_bytes(L):
     f = L.grouped_gemm_qint8_backward_workspace_bytes
-    assert f(16, 4, 64, 128) == 16 * (2 * 64 + 4)
-    assert f(16, 4, 96, 128) == 16 * (2 * 128 + 4)      # rows of whole 64-value stages
+    assert f(16, 4, 64, 128) == 16 * (2 * 128 + 4)      # rows of whole 128-value stages
+    assert f(16, 4, 128, 128) == 16 * (2 * 128 + 4)
+    assert f(16, 4, 160, 128) == 16 * (2 * 256 + 4)
     assert f(0, 4, 64, 128) == 0
     for bad in ((-1, 4, 64, 128), (2 ** 31, 4, 64, 128), (16, 0, 64, 128), (16, 1025, 64, 128), (16, 4, 48, 128),
                 (16, 4, 131072, 128), (16, 4, 64, 64), (16, 4, 64, 131072 + 128), (2 ** 31 - 1, 4, 64, 131072)):
