@@ -30,8 +30,8 @@ constexpr int kBN = 256;        // output columns per tile (weight rows; GRAD: w
 constexpr int kGroupM = 4;      // m-tiles per n-tile sweep
 
 // WM x WN waves; a wave owns XO 16-row operands of the A tile and WO 16-wide
-// operands of the weight tile.  GRAD: the wave's first XO / 2 A operands are
-// the hi planes of its rows, the others the lo planes of the same rows.
+// operands of the weight tile.  GRAD: A operand 2i holds the hi plane of the
+// wave's i-th 16 rows, 2i + 1 the lo plane of the same rows.
 template <int WM_, int WN_, int XO_, int WO_, int STAGES_>
 struct Cfg {
   static constexpr int WM = WM_, WN = WN_, XO = XO_, WO = WO_, kStages = STAGES_;
@@ -166,17 +166,17 @@ struct Int8Args {
 // Epilogue of one tile: value i of accumulator [wo][xo] in lane l is weight
 // row kWaveCols wn + 16wo + 4(l/16) + i of the tile and A row 16(XO wm + xo) +
 // l%16.
-template <class C, int OUT, int MODE>
+template <class C, int OUT, int MODE, int NX>
 __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int wm, int wn, int lane, const Int8Args& g,
-                                         const v4i (&acc)[C::WO][C::XO]) {
-  constexpr int kX = MODE == GRAD ? C::XO / 2 : C::XO;
+                                         const v4i (&acc)[C::WO][NX]) {
+  constexpr int kP = MODE == GRAD ? 2 : 1;  // A operands per 16 routed rows
   const int l16 = lane & 15, m0 = 4 * (lane >> 4);
   const float* sc = sb + 32;
 #pragma unroll
-  for (int xo = 0; xo < kX; ++xo) {
-    const int r = 16 * (kX * wm + xo) + l16;      // row of the tile's routed rows
+  for (int xo = 0; xo < NX; xo += kP) {
+    const int ar = 16 * (C::XO * wm + xo) + l16;                     // row of the A tile
+    const int r = 16 * ((C::XO * wm + xo) / kP) + l16;               // row of the tile's routed rows
     if (r >= t.rows) continue;
-    const int ar = 16 * (C::XO * wm + xo) + l16;  // row of the A tile
     const int64_t orow = t.row0 + r;
     const float sa = sb[(ar / C::kRW) * 64 + ar % C::kRW];
     if constexpr (MODE == SILU) {
@@ -213,7 +213,7 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_fmaf(__builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + kX][i]), sa, b[i]);
+            o[i] = __builtin_fmaf(__builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + 1][i]), sa, b[i]);
           put4<OUT>(g.out, idx, o);
         } else if constexpr (OUT == OUT_I32) {
           *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + orow * g.N + col0) = acc[wo][xo];
@@ -268,9 +268,9 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
       if constexpr (MODE == GRAD) {
         // a copy's 8 rows lie in one 16-row operand, hence in one plane
         const int xo = r0 / 16 % C::XO;
-        const int tok = 8 * C::XO * (r0 / (16 * C::XO)) + 16 * (xo % (C::XO / 2)) + r0 % 16 + (lane >> 3);
+        const int tok = 8 * C::XO * (r0 / (16 * C::XO)) + 16 * (xo / 2) + r0 % 16 + (lane >> 3);
         arow[i] = t.row0 + min(tok, t.rows - 1);
-        pa[i] = g.a + ((int64_t)(xo / (C::XO / 2)) * P + arow[i]) * a_pitch + chunk;
+        pa[i] = g.a + ((int64_t)(xo & 1) * P + arow[i]) * a_pitch + chunk;
       } else {
         int r;
         if (g.a_sorted || g.sorted_ids == nullptr) {
@@ -325,7 +325,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   auto copy = [&](uint32_t base, int i) __attribute__((always_inline)) {
     const int64_t ko = (int64_t)is_step * kRowBytes;
     if (i < C::kCopiesA) {
-      dma16(pa[i] + ko, base + (C::kCopiesA * wid + i) * 1024);
+      dma16(pa[i] + ko, __builtin_amdgcn_readfirstlane(base + (C::kCopiesA * wid + i) * 1024));
     } else {
       const int q = C::kCopiesB * wid + i - C::kCopiesA;
       int64_t kb = ko;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
         // last stage's rows n % 32 are there, N being a multiple of 32
         if (is_step * kRowBytes + 4 * q >= N) kb -= (int64_t)(4 * q & ~31) * K;
       }
-      dma16(pb[i - C::kCopiesA] + kb, base + C::kATile + q * 1024);
+      dma16(pb[i - C::kCopiesA] + kb, __builtin_amdgcn_readfirstlane(base + C::kATile + q * 1024));
     }
   };
   // After a stage's copies: a tile's scales ride with its first stage, and the
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   // slots that nobody reads: every wave then waits for constant counts.
   auto advance = [&]() __attribute__((always_inline)) {
     if (is_step == 0) {
-      dma4(psc, sbuf_lds + is_sbuf * C::kScaleBytes + wid * 256);
+      dma4(psc, __builtin_amdgcn_readfirstlane(sbuf_lds + is_sbuf * C::kScaleBytes + wid * 256));
       is_sbuf = is_sbuf == C::kScaleBufs - 1 ? 0 : is_sbuf + 1;
     }
     if (++is_step == steps) {
@@ -368,13 +368,10 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
     advance();
   }
   arrive(std::integral_constant<int, C::kStages - 1>());
-  const uint8_t* As = ring;
-  v4i x[C::XO], w[C::WO];
-#pragma unroll
-  for (int o = 0; o < C::XO; ++o) x[o] = read_x<C>(As, wm, lane, 0, o);
-#pragma unroll
-  for (int o = 0; o < C::WO; ++o) w[o] = read_w<C, MODE>(As, wn, lane, 0, o);
 
+  // One tile of a wave with NX A operands in use (those of rows past a partial
+  // tile's last are left out: the tile then costs its copies, not its MFMAs).
+  //
   // Per stage: the 64-value substeps 0 and 1, each WO passes over the A
   // operands with one weight operand.  An operand's registers take its next
   // substep's values right after its last use (weights after their pass, A
@@ -384,18 +381,24 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   // spread over the passes that remain.  The order is pinned: left to itself
   // the compiler gathers the reads, and the matrix cores wait for them.
   int slot = 0, ep_sbuf = 0;
-  for (int item = first; item < total; item += G) {
-    v4i acc[C::WO][C::XO];
+  auto run_tile = [&](const TileAt& t, auto operands) __attribute__((always_inline)) {
+    constexpr int NX = decltype(operands)::value, NA = NX ? NX : 1;
+    const uint8_t* As = ring + slot * C::kStageBytes;
+    v4i x[NA], w[C::WO], acc[C::WO][NA];
 #pragma unroll
-    for (int wo = 0; wo < C::WO; ++wo)
+    for (int wo = 0; wo < C::WO; ++wo) {
 #pragma unroll
-      for (int xo = 0; xo < C::XO; ++xo) acc[wo][xo] = v4i{};
+      for (int xo = 0; xo < NX; ++xo) acc[wo][xo] = v4i{};
+      if (NX) w[wo] = read_w<C, MODE>(As, wn, lane, 0, wo);
+    }
+#pragma unroll
+    for (int xo = 0; xo < NX; ++xo) x[xo] = read_x<C>(As, wm, lane, 0, xo);
     int st = 0;
     do {
 #pragma unroll
-      for (int wo = 0; wo < C::WO; ++wo) {
+      for (int wo = 0; wo < (NX ? C::WO : 0); ++wo) {
 #pragma unroll
-        for (int xo = 0; xo < C::XO; ++xo) {
+        for (int xo = 0; xo < NX; ++xo) {
           acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
           if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 1, xo);
           __builtin_amdgcn_sched_barrier(0);
@@ -403,37 +406,52 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
         w[wo] = read_w<C, MODE>(As, wn, lane, 1, wo);
       }
 #pragma unroll
-      for (int xo = 0; xo < C::XO; ++xo) {
+      for (int xo = 0; xo < NX; ++xo) {
         acc[0][xo] = mfma_i8_16x16x64(w[0], x[xo], acc[0][xo]);
         __builtin_amdgcn_sched_barrier(0);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       arrive(std::integral_constant<int, C::kStages - 2>());
-      const uint32_t refill = ring_lds + slot * C::kStageBytes;
+      const uint32_t refill = __builtin_amdgcn_readfirstlane(ring_lds + slot * C::kStageBytes);
       slot = slot == C::kStages - 1 ? 0 : slot + 1;
       As = ring + slot * C::kStageBytes;
-      w[0] = read_w<C, MODE>(As, wn, lane, 0, 0);
-      constexpr int kRest = (C::WO - 1) * C::XO;
+      if constexpr (NX == 0) {
 #pragma unroll
-      for (int wo = 1; wo < C::WO; ++wo) {
+        for (int i = 0; i < C::kCopies; ++i) copy(refill, i);
+      } else {
+        w[0] = read_w<C, MODE>(As, wn, lane, 0, 0);
+        constexpr int kRest = (C::WO - 1) * NX;
 #pragma unroll
-        for (int xo = 0; xo < C::XO; ++xo) {
-          const int m = (wo - 1) * C::XO + xo;
-          acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
-          if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 0, xo);
+        for (int wo = 1; wo < C::WO; ++wo) {
 #pragma unroll
-          for (int i = 0; i < C::kCopies; ++i)
-            if (i * kRest / C::kCopies == m) copy(refill, i);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int xo = 0; xo < NX; ++xo) {
+            acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
+            if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 0, xo);
+#pragma unroll
+            for (int i = 0; i < C::kCopies; ++i)
+              if (i * kRest / C::kCopies == (wo - 1) * NX + xo) copy(refill, i);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          w[wo] = read_w<C, MODE>(As, wn, lane, 0, wo);
         }
-        w[wo] = read_w<C, MODE>(As, wn, lane, 0, wo);
       }
       advance();
     } while (++st < steps);
-    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
-    epilogue<C, OUT, MODE>(t, reinterpret_cast<const float*>(sbuf + ep_sbuf * C::kScaleBytes), wm, wn, lane, g, acc);
+    if constexpr (NX > 0)
+      epilogue<C, OUT, MODE, NX>(t, reinterpret_cast<const float*>(sbuf + ep_sbuf * C::kScaleBytes), wm, wn, lane, g,
+                                 acc);
     wait_vmcnt<0>();  // the stores leave before the next stages are counted
     ep_sbuf = ep_sbuf == C::kScaleBufs - 1 ? 0 : ep_sbuf + 1;
+  };
+  for (int item = first; item < total; item += G) {
+    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
+    const int left = t.rows - kBMt / C::WM * wm;  // routed rows of this wave
+    constexpr int kRows = kBMt / C::WM;
+    if (left > kRows / 2) run_tile(t, std::integral_constant<int, C::XO>());
+    else if (C::XO > 4 && left > kRows / 4) run_tile(t, std::integral_constant<int, C::XO / 2>());
+    else if (C::XO > 4 && left > 0) run_tile(t, std::integral_constant<int, C::XO / 4>());
+    else if (C::XO <= 4 && left > 0) run_tile(t, std::integral_constant<int, C::XO / 2>());
+    else run_tile(t, std::integral_constant<int, 0>());
   }
 }
 
@@ -595,64 +613,77 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
 
 // ------------------------------------------------------- gradient's planes
 // d[s][n] = dy[s][n] * w_scale[e][n] as step * (256 hi + lo): step = max |d| /
-// 32512, the code rne(d * (32512 / max)).  One workgroup per row; rows of at
-// most kThreadsD * 8 * kLoadsD values are held in registers, longer ones are
-// read twice.  A row whose largest value is below 2^-100 counts as zero; one
-// that holds an infinity or NaN gets step NaN, so all of its dx is NaN.
-constexpr int kThreadsD = 256;
-
+// 32512, the code rne(d * (32512 / max)).  WAVES waves work on a row, whose d
+// stays in their registers (LOADS times 8 values a lane; 0: the row is read
+// twice).  A row whose largest value is below 2^-100 counts as zero; one that
+// holds an infinity or NaN gets step NaN, so all of its dx is NaN.
+//
+// HBM-bound: dy is read once, past the caches, and the two planes are written.
 // Expert of sorted row s, by the whole wave: the number of experts that end
-// at or before it.
-__device__ __forceinline__ int expert_of(const int* __restrict__ offsets, int E, int s, int lane) {
+// (ends[e], in LDS) at or before it.
+__device__ __forceinline__ int expert_of(const int* ends, int E, int s, int lane) {
   int n = 0;
   for (int e0 = 0; e0 < E; e0 += 64) {
     const int e = e0 + lane;
-    n += __popcll(__ballot(e < E && offsets[e + 1] <= s));
+    n += __popcll(__ballot(e < E && ends[e] <= s));
   }
   return min(n, E - 1);
 }
 
-template <int YK, int LOADS>
-__global__ __launch_bounds__(kThreadsD) void grad_planes(const void* __restrict__ dy, const float* __restrict__ w_scale,
-                                                         const int* __restrict__ offsets, int E, int P, int N,
-                                                         uint8_t* __restrict__ planes, float* __restrict__ step) {
-  __shared__ u32 wmax[kThreadsD / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
+template <int YK, int WAVES, int LOADS>
+__global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
+    const void* __restrict__ dy, const float* __restrict__ w_scale, const int* __restrict__ offsets, int E, int P, int N,
+    uint8_t* __restrict__ planes, float* __restrict__ step) {
+  constexpr int kRows = WAVES == 1 ? 4 : 1;  // rows of a workgroup at a time
+  constexpr int kT = 64 * WAVES;
+  __shared__ u32 wmax[WAVES];
+  __shared__ int ends[kMaxExperts];
+  // in LDS, so that the search for a row's expert does not wait for dy's loads
+  for (int e = threadIdx.x; e < E; e += blockDim.x) ends[e] = offsets[e + 1];
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, sub = wid / WAVES, tid = threadIdx.x % kT;
   const int n = min(max(offsets[E], 0), P), Np = plane_pitch(N);
-  for (int64_t s = blockIdx.x; s < n; s += gridDim.x) {
-    const int e = expert_of(offsets, E, (int)s, lane);
-    const float* ws = w_scale + (int64_t)e * N;
+  for (int64_t s = (int64_t)blockIdx.x * kRows + sub; s < n; s += (int64_t)gridDim.x * kRows) {
     const int64_t base = s * N;
-    auto load = [&](int k, float (&d)[8]) __attribute__((always_inline)) {
-      float y[8], c[8];
-      load8<YK, false>(dy, base + k, y);
+    float d[LOADS ? LOADS : 1][8];
+    if constexpr (LOADS > 0) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        if ((i * kT + tid) * 8 < N) load8<YK, true>(dy, base + (i * kT + tid) * 8, d[i]);
+    }
+    const float* ws = w_scale + (int64_t)expert_of(ends, E, (int)s, lane) * N;
+    auto scale8 = [&](int k, float (&v)[8]) __attribute__((always_inline)) {
+      float c[8];
       load8<OUT_F32, false>(ws, k, c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = y[j] * c[j];
+      for (int j = 0; j < 8; ++j) v[j] *= c[j];
     };
-    float d[LOADS ? LOADS : 1][8];
     u32 m = 0;
     if constexpr (LOADS > 0) {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int k = (i * kThreadsD + tid) * 8;
+        const int k = (i * kT + tid) * 8;
         if (k < N) {
-          load(k, d[i]);
+          scale8(k, d[i]);
           m = max(m, amax_bits(d[i]));
         }
       }
     } else {
-      for (int k = tid * 8; k < N; k += kThreadsD * 8) {
-        load(k, d[0]);
+      for (int k = tid * 8; k < N; k += kT * 8) {
+        load8<YK, false>(dy, base + k, d[0]);
+        scale8(k, d[0]);
         m = max(m, amax_bits(d[0]));
       }
     }
     m = wave_max(m);
-    if (lane == 0) wmax[wid] = m;
-    __syncthreads();
+    if constexpr (WAVES > 1) {
+      static_assert(kRows == 1, "the rows of a workgroup may end in different rounds: no barrier then");
+      if (lane == 0) wmax[wid] = m;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kThreadsD / 64; ++w) m = max(m, wmax[w]);
-    __syncthreads();  // wmax is reused by the next row
+      for (int w = 0; w < WAVES; ++w) m = max(m, wmax[w]);
+      __syncthreads();  // wmax is reused by the next row
+    }
     const Scale c = scale_of(m, 32512.0f, 0x1p-100f);
     uint8_t* hi = planes + s * Np;
     uint8_t* lo = hi + (int64_t)P * Np;
@@ -670,12 +701,13 @@ __global__ __launch_bounds__(kThreadsD) void grad_planes(const void* __restrict_
     if constexpr (LOADS > 0) {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const int k = (i * kThreadsD + tid) * 8;
+        const int k = (i * kT + tid) * 8;
         if (k < N) put(k, d[i]);
       }
     } else {
-      for (int k = tid * 8; k < N; k += kThreadsD * 8) {
-        load(k, d[0]);
+      for (int k = tid * 8; k < N; k += kT * 8) {
+        load8<YK, false>(dy, base + k, d[0]);
+        scale8(k, d[0]);
         put(k, d[0]);
       }
     }
@@ -692,37 +724,52 @@ typedef Cfg<2, 4, 8, 4, 2> Large;   // 256 A rows
 typedef Cfg<2, 4, 4, 4, 3> Medium;  // 128
 typedef Cfg<1, 8, 4, 2, 3> Small;   // 64
 
+// Columns that one n-tile covers, and n-tiles.
+int64_t n_tiles_of(int mode, int64_t N, int64_t K) {
+  const int64_t cols = mode == SILU ? N / 2 : mode == GRAD ? K : N, w = mode == SILU ? kBN / 2 : kBN;
+  return (cols + w - 1) / w;
+}
+
 template <class C, int OUT, int MODE>
 hipError_t go_tiles(const Int8Args& g, int num_cus, hipStream_t stream) {
   const int bm = MODE == GRAD ? C::kBM / 2 : C::kBM;
   // upper bound on tiles: every expert adds at most one partial m-tile
-  const int64_t mt = (g.P + (int64_t)bm - 1) / bm + std::min(g.E, g.P);
-  const int64_t nt = MODE == SILU ? (g.N / 2 + kBN / 2 - 1) / (kBN / 2) : ((MODE == GRAD ? g.K : g.N) + kBN - 1) / kBN;
-  if (mt * nt == 0) return hipSuccess;
-  const int grid = (int)std::min<int64_t>(mt * nt, num_cus);
+  const int64_t tiles = (((int64_t)g.P + bm - 1) / bm + std::min(g.E, g.P)) * n_tiles_of(MODE, g.N, g.K);
+  const int grid = (int)std::min<int64_t>(tiles, num_cus);
   hipLaunchKernelGGL((int8_tiles<C, OUT, MODE>), dim3(grid), dim3(C::kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
+// The tile height: the least of (tiles a compute unit works through) x (the
+// time of one), with half a partial m-tile for every expert.  Relative times
+// of a tile, measured with 32 experts of 4096 x 4096 and 512 rows each
+// (forward 315, 327 and 445 us for 256, 128 and 64 rows; gradient 588, 648 and
+// 905): 1, 0.54, 0.36.  At 128 rows an expert the forward call takes 155, 139
+// and 159 us, at 16 rows 135, 125 and 124.
 template <int OUT, int MODE>
-hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
-  if (g.P == 0) return hipSuccess;
-  const int64_t per = g.P / g.E;
-  if (sched == 1 || (sched == 0 && per < 16)) {
-    hipLaunchKernelGGL((int8_decode<OUT, MODE>), dim3(num_cus * 2), dim3(64 * dd::kWaves), 0, stream, g);
-    return hipGetLastError();
-  }
-  if (per <= 64) return go_tiles<Small, OUT, MODE>(g, num_cus, stream);
-  if (per <= 128) return go_tiles<Medium, OUT, MODE>(g, num_cus, stream);
+hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
+  const double n_tiles = (double)n_tiles_of(MODE, g.N, g.K), partial = 0.5 * std::min(g.E, g.P);
+  const int planes = MODE == GRAD ? 2 : 1;
+  auto cost = [&](int bm, double one) {
+    return one * std::max(1.0, ((double)g.P * planes / bm + partial) * n_tiles / num_cus);
+  };
+  const double l = cost(Large::kBM, 1.0), m = cost(Medium::kBM, 0.54), s = cost(Small::kBM, 0.36);
+  if (s <= m && s <= l) return go_tiles<Small, OUT, MODE>(g, num_cus, stream);
+  if (m <= l) return go_tiles<Medium, OUT, MODE>(g, num_cus, stream);
   return go_tiles<Large, OUT, MODE>(g, num_cus, stream);
 }
 
-template <int OUT>
-hipError_t go_grad(const Int8Args& g, int num_cus, hipStream_t stream) {
-  const int64_t per = g.P / g.E;
-  if (per <= 32) return go_tiles<Small, OUT, GRAD>(g, num_cus, stream);
-  if (per <= 64) return go_tiles<Medium, OUT, GRAD>(g, num_cus, stream);
-  return go_tiles<Large, OUT, GRAD>(g, num_cus, stream);
+// AUTO streams below 8 rows an expert: with 32 experts of 4096 x 4096, 4 rows
+// each take 95 us streamed and 123 in tiles, 8 rows 118 and 122, 16 rows 197
+// and 124 (a second pass over the weights).
+template <int OUT, int MODE>
+hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
+  if (g.P == 0) return hipSuccess;
+  if (sched == 1 || (sched == 0 && g.P < (int64_t)dd::kM * g.E)) {
+    hipLaunchKernelGGL((int8_decode<OUT, MODE>), dim3(num_cus * 2), dim3(64 * dd::kWaves), 0, stream, g);
+    return hipGetLastError();
+  }
+  return go_prefill<OUT, MODE>(g, num_cus, stream);
 }
 
 Int8Args int8_args(const GroupedArgs& g, const void* a, const float* a_scale, const int8_t* w, const float* w_scale) {
@@ -768,26 +815,28 @@ hipError_t launch_gemm_int8_bwd(const GroupedArgs& g, const void* dy, const int8
   const int P = (int)g.P;
   uint8_t* planes = static_cast<uint8_t*>(ws);
   float* step = reinterpret_cast<float*>(planes + 2 * g.P * plane_pitch(g.N));
-  const int grid = std::min(P, g.num_cus * 8);
   const bool bf = g.out_kind == OUT_BF16;
-#define MOEQ_PLANES(LOADS)                                                                                       \
-  do {                                                                                                           \
-    if (bf)                                                                                                      \
-      hipLaunchKernelGGL((grad_planes<OUT_BF16, LOADS>), dim3(grid), dim3(kThreadsD), 0, stream, dy, w_scale,    \
-                         g.offsets, g.E, P, g.N, planes, step);                                                  \
-    else                                                                                                         \
-      hipLaunchKernelGGL((grad_planes<OUT_F16, LOADS>), dim3(grid), dim3(kThreadsD), 0, stream, dy, w_scale,     \
-                         g.offsets, g.E, P, g.N, planes, step);                                                  \
+#define MOEQ_PLANES(WAVES, LOADS)                                                                                  \
+  do {                                                                                                             \
+    const int rows = WAVES == 1 ? 4 : 1;                                                                           \
+    const dim3 grid(std::min((P + rows - 1) / rows, g.num_cus * 8)), block(64 * WAVES * rows);                     \
+    if (bf)                                                                                                        \
+      hipLaunchKernelGGL((grad_planes<OUT_BF16, WAVES, LOADS>), grid, block, 0, stream, dy, w_scale, g.offsets,    \
+                         g.E, P, g.N, planes, step);                                                               \
+    else                                                                                                           \
+      hipLaunchKernelGGL((grad_planes<OUT_F16, WAVES, LOADS>), grid, block, 0, stream, dy, w_scale, g.offsets,     \
+                         g.E, P, g.N, planes, step);                                                               \
   } while (0)
-  if (g.N <= kThreadsD * 8 * 4) MOEQ_PLANES(4);
-  else if (g.N <= kThreadsD * 8 * 16) MOEQ_PLANES(16);
-  else MOEQ_PLANES(0);
+  if (g.N <= 64 * 8 * 4) MOEQ_PLANES(1, 4);
+  else if (g.N <= 128 * 8 * 8) MOEQ_PLANES(2, 8);
+  else if (g.N <= 512 * 8 * 8) MOEQ_PLANES(8, 8);
+  else MOEQ_PLANES(8, 0);
 #undef MOEQ_PLANES
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   Int8Args k = int8_args(g, planes, step, w, w_scale);
   k.base = base;
-  return bf ? go_grad<OUT_BF16>(k, g.num_cus, stream) : go_grad<OUT_F16>(k, g.num_cus, stream);
+  return bf ? go_prefill<OUT_BF16, GRAD>(k, g.num_cus, stream) : go_prefill<OUT_F16, GRAD>(k, g.num_cus, stream);
 }
 
 }  // namespace moeq
