@@ -487,6 +487,28 @@ __device__ __forceinline__ void wait_decode(int n) {  // vmcnt(n * dd::kCopies)
   asm volatile("" ::: "memory");
 }
 
+// Activation row of sorted position `pos`, one of the 8 from `first` on
+// (wave-uniform): one scalar load of their ids, moved down where it would pass
+// the table's end, and one division.  (Eight loads in turn cost 8 us at the start
+// of every item.)
+__device__ __forceinline__ int act_row(const int* __restrict__ ids, int topk, int64_t rows_a, int P, int first,
+                                       int pos) {
+  int r = pos;
+  if (ids != nullptr) {
+    if (P >= 8) {
+      const int at = min(first, P - 8), k = pos - at;
+      const i32x8_a4 v = ld_uniform8(ids + at);
+      r = v[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) r = k == j ? v[j] : r;
+    } else {
+      r = ids[pos];
+    }
+    r /= topk;
+  }
+  return (r < 0 || r >= rows_a) ? 0 : r;
+}
+
 template <int OUT, int MODE>
 __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
   __shared__ int tile_start[kMaxExperts + 1];
@@ -512,6 +534,7 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
   const int wf1 = dd::kW + l16 * 128 + (((2 * quarter + 1) ^ wkey) << 4);
   const int xslot = l16 < dd::kM ? l16 : 0;
   const int xf = dd::kX + xslot * 128 + ((2 * quarter) << 4);
+  const int* ids = g.a_sorted ? nullptr : g.sorted_ids;
 
   for (int item = wid; item < total; item += active) {
     // m-tile major, then blocks; every field wave-uniform
@@ -528,32 +551,19 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
     const int nb = local - mt * n_blocks;
     const int row0 = lo + mt * dd::kM;
     const int rows = min(dd::kM, hi - row0);
-    int arow[dd::kM];
-#pragma unroll
-    for (int j = 0; j < dd::kM; ++j) {
-      const int sp = row0 + min(j, rows - 1);
-      const int r = (g.a_sorted || g.sorted_ids == nullptr) ? sp : ld_uniform(g.sorted_ids, sp) / g.topk;
-      arow[j] = (r < 0 || r >= g.rows_a) ? 0 : r;
-    }
     auto wrow = [&](int rb) __attribute__((always_inline)) {
       return MODE == SILU ? (rb < 8 ? 0 : I) + nb * 8 + (rb & 7) : nb * dd::kRowsW + rb;
     };
     const uint8_t* wbase = g.w + (int64_t)e * N * K;
     const uint8_t* sw0 = wbase + (int64_t)wrow(crow) * K + cp0;
     const uint8_t* sw1 = wbase + (int64_t)wrow(8 + crow) * K + cp1;
-    // per-lane pick among the wave-uniform rows (a select chain, no indexed
-    // register array)
-    auto pick = [&](int i) __attribute__((always_inline)) {
-      int v = arow[0];
-#pragma unroll
-      for (int j = 1; j < dd::kM; ++j) v = i == j ? arow[j] : v;
-      return v;
-    };
-    const uint8_t* sx = g.a + (int64_t)pick(lane >> 3) * K + ((lane & 7) << 4);
-    const float* ss;
-    if (lane < dd::kM) ss = g.a_scale + pick(lane);
-    else if (lane < dd::kM + dd::kRowsW) ss = g.w_scale + (int64_t)e * N + wrow(lane - dd::kM);
-    else ss = g.a_scale + arow[0];
+    // of the x copy: 8 lanes a row
+    const int xrow = act_row(ids, g.topk, g.rows_a, P, row0, row0 + min(lane >> 3, rows - 1));
+    const uint8_t* sx = g.a + (int64_t)xrow * K + ((lane & 7) << 4);
+    const int srow = __shfl(xrow, 8 * (lane & 7), 64);  // by every lane: it reads lanes on both sides of the select
+    const float* ss = lane >= dd::kM && lane < dd::kM + dd::kRowsW
+                          ? g.w_scale + (int64_t)e * N + wrow(lane - dd::kM)
+                          : g.a_scale + srow;
     auto issue = [&](int k) __attribute__((always_inline)) {
       const uint32_t sl = lb + (uint32_t)((k % dd::kDepth) * dd::kSlot);
       const int64_t ko = (int64_t)k * dd::kGroupK;
