@@ -549,11 +549,11 @@ moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, i
  * MOEQ_EALIGN), K < 131072 so that the int32 accumulator cannot wrap (else
  * MOEQ_EINVAL), a, w and out 16-byte and the scales and tables 4-byte
  * aligned, 1 <= E <= 1024, 1 <= topk <= 64; and out disjoint from the inputs
- * and sizes that one launch can count, (P/8 + E) * N/16 < 2^30 (else
+ * and sizes that one launch can count, (P/16 + E) * N/16 < 2^30 (else
  * MOEQ_EINVAL).
  * Two schedules give identical outputs: MFMA tiles of 64, 128 or 256 rows
  * (PREFILL, by the average rows of an expert), and waves streaming 16 weight
- * rows x at most 8 routed rows (DECODE).  AUTO streams when P < 8 * E.
+ * rows x at most 16 routed rows (DECODE).  AUTO streams when P < 10 * E.
  * ---------------------------------------------------------------------- */
 moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t rows_a, moeq_arow a_row, const int8_t* w,
                                const float* w_scale, const int32_t* expert_offsets, const int32_t* sorted_pair_ids,

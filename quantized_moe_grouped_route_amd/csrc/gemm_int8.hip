@@ -457,33 +457,34 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
 
 // ------------------------------------------------------------------ decode
 // Few routed rows per expert: the weight stream is the whole cost.  The wave
-// is the unit of work: item = (at most 8 routed rows of one expert) x (16
+// is the unit of work: item = (at most 16 routed rows of one expert) x (16
 // weight rows; SILU: 8 gate rows and the 8 up rows of the same columns).  Per
 // K group of 128 values (one cache line of a row) a ring slot of the wave
-// holds the 16 weight rows (two whole-line copies of 8 rows, 16-byte piece p
-// of row r at p ^ ((r >> 1) & 7)) and the 8 activation rows (one copy).  The
-// item's scales ride in group 0's slot (one 4-byte-per-lane copy: lanes 0..7
-// the rows', 8..23 the weights').  Two v_mfma_i32_16x16x64_i8 per group take
-// the weights as the 16-row operand and the routed rows as the columns: lane
-// l supplies pieces 2(l/16) and 2(l/16) + 1 of row l % 16, value i of lane l
-// is weight row 4(l/16) + i and routed row l % 16.
+// holds the 16 weight rows (two whole-line copies of 8 rows) and the activation
+// rows (a copy for each 8 that the item has), 16-byte piece p of row r at p ^
+// ((r >> 1) & 7).  The item's scales ride in group 0's slot (one
+// 4-byte-per-lane copy: lanes 0..15 the rows', 16..31 the weights').  Two
+// v_mfma_i32_16x16x64_i8 per group take the weights as the 16-row operand and
+// the routed rows as the columns: lane l supplies pieces 2(l/16) and 2(l/16) +
+// 1 of row l % 16, value i of lane l is weight row 4(l/16) + i and routed row
+// l % 16.
 namespace dd {
-constexpr int kM = 8;
+constexpr int kM = 16;
 constexpr int kRowsW = 16;
 constexpr int kWaves = 4;                              // waves per workgroup, independent
 constexpr int kDepth = 4;                              // K groups in flight per wave
-constexpr int kW = 0, kX = 2048, kS = 3072;            // slot regions
-constexpr int kSlot = 3328;
-constexpr int kCopies = 3;                             // per K group: 2 weight, 1 activation
+constexpr int kW = 0, kX = 2048, kS = 4096;            // slot regions
+constexpr int kSlot = 4352;
 constexpr int kGroupK = 128;
 }  // namespace dd
 
-__device__ __forceinline__ void wait_decode(int n) {  // vmcnt(n * dd::kCopies)
+template <int COPIES>
+__device__ __forceinline__ void wait_decode(int n) {  // vmcnt(n * COPIES)
   static_assert(dd::kDepth == 4, "wait table");
   if (n <= 0) wait_vmcnt<0>();
-  else if (n == 1) wait_vmcnt<dd::kCopies>();
-  else if (n == 2) wait_vmcnt<2 * dd::kCopies>();
-  else wait_vmcnt<3 * dd::kCopies>();
+  else if (n == 1) wait_vmcnt<COPIES>();
+  else if (n == 2) wait_vmcnt<2 * COPIES>();
+  else wait_vmcnt<3 * COPIES>();
   asm volatile("" ::: "memory");
 }
 
@@ -532,8 +533,6 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
   const int wkey = (l16 >> 1) & 7;
   const int wf0 = dd::kW + l16 * 128 + (((2 * quarter) ^ wkey) << 4);
   const int wf1 = dd::kW + l16 * 128 + (((2 * quarter + 1) ^ wkey) << 4);
-  const int xslot = l16 < dd::kM ? l16 : 0;
-  const int xf = dd::kX + xslot * 128 + ((2 * quarter) << 4);
   const int* ids = g.a_sorted ? nullptr : g.sorted_ids;
 
   for (int item = wid; item < total; item += active) {
@@ -557,67 +556,84 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
     const uint8_t* wbase = g.w + (int64_t)e * N * K;
     const uint8_t* sw0 = wbase + (int64_t)wrow(crow) * K + cp0;
     const uint8_t* sw1 = wbase + (int64_t)wrow(8 + crow) * K + cp1;
-    // of the x copy: 8 lanes a row
-    const int xrow = act_row(ids, g.topk, g.rows_a, P, row0, row0 + min(lane >> 3, rows - 1));
-    const uint8_t* sx = g.a + (int64_t)xrow * K + ((lane & 7) << 4);
-    const int srow = __shfl(xrow, 8 * (lane & 7), 64);  // by every lane: it reads lanes on both sides of the select
-    const float* ss = lane >= dd::kM && lane < dd::kM + dd::kRowsW
-                          ? g.w_scale + (int64_t)e * N + wrow(lane - dd::kM)
-                          : g.a_scale + srow;
-    auto issue = [&](int k) __attribute__((always_inline)) {
-      const uint32_t sl = lb + (uint32_t)((k % dd::kDepth) * dd::kSlot);
-      const int64_t ko = (int64_t)k * dd::kGroupK;
-      dma16_nt(sw0 + ko, sl + dd::kW);
-      dma16_nt(sw1 + ko, sl + dd::kW + 1024);
-      dma16(sx + ko, sl + dd::kX);
-      if (k == 0) dma4(ss, sl + dd::kS);
+    // XC: copies of activation rows, 8 rows each and 8 lanes a row
+    auto run_item = [&](auto copies) __attribute__((always_inline)) {
+      constexpr int XC = decltype(copies)::value;
+      int xrow[XC];
+      const uint8_t* sx[XC];
+#pragma unroll
+      for (int c = 0; c < XC; ++c) {
+        xrow[c] = act_row(ids, g.topk, g.rows_a, P, row0 + 8 * c, row0 + min(8 * c + (lane >> 3), rows - 1));
+        sx[c] = g.a + (int64_t)xrow[c] * K + (((lane & 7) ^ ((4 * c + (lane >> 4)) & 7)) << 4);
+      }
+      // row i's number is in lanes 8 (i % 8) .. +7 of xrow[i / 8]; read by
+      // every lane, as lanes on both sides of the select below hold it
+      const int s0 = __shfl(xrow[0], 8 * (lane & 7), 64), s1 = __shfl(xrow[XC - 1], 8 * (lane & 7), 64);
+      const float* ss = lane >= dd::kM && lane < dd::kM + dd::kRowsW
+                            ? g.w_scale + (int64_t)e * N + wrow(lane - dd::kM)
+                            : g.a_scale + (XC > 1 && lane >= 8 ? s1 : s0);
+      auto issue = [&](int k) __attribute__((always_inline)) {
+        const uint32_t sl = lb + (uint32_t)((k % dd::kDepth) * dd::kSlot);
+        const int64_t ko = (int64_t)k * dd::kGroupK;
+        dma16_nt(sw0 + ko, sl + dd::kW);
+        dma16_nt(sw1 + ko, sl + dd::kW + 1024);
+#pragma unroll
+        for (int c = 0; c < XC; ++c) dma16(sx[c] + ko, sl + dd::kX + 1024 * c);
+        if (k == 0) dma4(ss, sl + dd::kS);
+      };
+      const int npre = G < dd::kDepth ? G : dd::kDepth;
+      for (int k = 0; k < npre; ++k) issue(k);
+      const int xslot = l16 < 8 * XC ? l16 : 0;
+      const int xkey = (xslot >> 1) & 7;
+      const int xf0 = dd::kX + xslot * 128 + (((2 * quarter) ^ xkey) << 4);
+      const int xf1 = dd::kX + xslot * 128 + (((2 * quarter + 1) ^ xkey) << 4);
+      v4i acc = v4i{};
+      float sa = 0.f;
+      v4f sw = v4f{};
+      for (int k = 0; k < G; ++k) {
+        const int after = G - 1 - k;
+        wait_decode<2 + XC>(after < dd::kDepth - 1 ? after : dd::kDepth - 1);
+        const uint8_t* sp = myring + (k % dd::kDepth) * dd::kSlot;
+        const v4i w0 = __builtin_bit_cast(v4i, ld16(sp + wf0)), w1 = __builtin_bit_cast(v4i, ld16(sp + wf1));
+        const v4i x0 = __builtin_bit_cast(v4i, ld16(sp + xf0)), x1 = __builtin_bit_cast(v4i, ld16(sp + xf1));
+        if (k == 0) {
+          const float* s = reinterpret_cast<const float*>(sp + dd::kS);
+          sa = s[xslot];
+          sw = *reinterpret_cast<const v4f*>(s + dd::kM + 4 * quarter);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read; it may be refilled
+        if (k + dd::kDepth < G) issue(k + dd::kDepth);
+        acc = mfma_i8_16x16x64(w0, x0, acc);
+        acc = mfma_i8_16x16x64(w1, x1, acc);
+      }
+      const int64_t orow = row0 + l16;
+      if constexpr (MODE == SILU) {
+        float v[4], u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = sa * sw[i] * (float)acc[i];
+          u[i] = __shfl_xor(v[i], 32, 64);  // quarters 0, 1 hold gates, 2, 3 the ups
+        }
+        if (l16 < rows && quarter < 2) {
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = silu(v[i]) * u[i];
+          put4<OUT>(g.out, orow * I + nb * 8 + 4 * quarter, o);
+        }
+      } else if (l16 < rows) {
+        const int64_t idx = orow * N + nb * dd::kRowsW + 4 * quarter;
+        if constexpr (OUT == OUT_I32) {
+          *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + idx) = acc;
+        } else {
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[i];
+          put4<OUT>(g.out, idx, o);
+        }
+      }
     };
-    const int npre = G < dd::kDepth ? G : dd::kDepth;
-    for (int k = 0; k < npre; ++k) issue(k);
-    v4i acc = v4i{};
-    float sa = 0.f;
-    v4f sw = v4f{};
-    for (int k = 0; k < G; ++k) {
-      const int after = G - 1 - k;
-      wait_decode(after < dd::kDepth - 1 ? after : dd::kDepth - 1);
-      const uint8_t* sp = myring + (k % dd::kDepth) * dd::kSlot;
-      const v4i w0 = __builtin_bit_cast(v4i, ld16(sp + wf0)), w1 = __builtin_bit_cast(v4i, ld16(sp + wf1));
-      const v4i x0 = __builtin_bit_cast(v4i, ld16(sp + xf)), x1 = __builtin_bit_cast(v4i, ld16(sp + xf + 16));
-      if (k == 0) {
-        const float* s = reinterpret_cast<const float*>(sp + dd::kS);
-        sa = s[xslot];
-        sw = *reinterpret_cast<const v4f*>(s + dd::kM + 4 * quarter);
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read; it may be refilled
-      if (k + dd::kDepth < G) issue(k + dd::kDepth);
-      acc = mfma_i8_16x16x64(w0, x0, acc);
-      acc = mfma_i8_16x16x64(w1, x1, acc);
-    }
-    const int64_t orow = row0 + l16;
-    if constexpr (MODE == SILU) {
-      float v[4], u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = sa * sw[i] * (float)acc[i];
-        u[i] = __shfl_xor(v[i], 32, 64);  // quarters 0, 1 hold gates, 2, 3 the ups
-      }
-      if (l16 < rows && quarter < 2) {
-        float o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = silu(v[i]) * u[i];
-        put4<OUT>(g.out, orow * I + nb * 8 + 4 * quarter, o);
-      }
-    } else if (l16 < rows) {
-      const int64_t idx = orow * N + nb * dd::kRowsW + 4 * quarter;
-      if constexpr (OUT == OUT_I32) {
-        *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + idx) = acc;
-      } else {
-        float o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[i];
-        put4<OUT>(g.out, idx, o);
-      }
-    }
+    if (rows > 8) run_item(std::integral_constant<int, 2>());
+    else run_item(std::integral_constant<int, 1>());
   }
 }
 
@@ -769,13 +785,14 @@ hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
   return go_tiles<Large, OUT, MODE>(g, num_cus, stream);
 }
 
-// AUTO streams below 8 rows an expert: with 32 experts of 4096 x 4096, 4 rows
-// each take 95 us streamed and 123 in tiles, 8 rows 118 and 122, 16 rows 197
-// and 124 (a second pass over the weights).
+// AUTO streams below 10 rows an expert: with 32 experts of 4096 x 4096, 4 rows
+// each take 90 us streamed and 123 in tiles, 10 rows 93 and 124, 16 rows 128
+// and 124 (experts past 16 rows stream their weights again); with 256 experts
+// of 2048 x 2048 6 rows take 172 and 185, 10 rows 190 and 188.
 template <int OUT, int MODE>
 hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
   if (g.P == 0) return hipSuccess;
-  if (sched == 1 || (sched == 0 && g.P < (int64_t)dd::kM * g.E)) {
+  if (sched == 1 || (sched == 0 && g.P < (int64_t)10 * g.E)) {
     hipLaunchKernelGGL((int8_decode<OUT, MODE>), dim3(num_cus * 2), dim3(64 * dd::kWaves), 0, stream, g);
     return hipGetLastError();
   }
