@@ -26,7 +26,6 @@ namespace {
 enum Mode { NONE = 0, SILU = 1, GRAD = 2 };
 
 constexpr int kRowBytes = 128;  // K (GRAD: N) values of a row per stage: one cache line
-constexpr int kBN = 256;        // output columns per tile (weight rows; GRAD: weight columns)
 constexpr int kGroupM = 4;      // m-tiles per n-tile sweep
 
 // WM x WN waves; a wave owns XO 16-row operands of the A tile and WO 16-wide
@@ -38,6 +37,7 @@ struct Cfg {
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kBM = 16 * XO * WM;                   // A tile rows
+  static constexpr int kBN = 16 * WO * WN;                   // weight rows of a tile (GRAD: weight columns)
   static constexpr int kATile = kBM * kRowBytes;
   static constexpr int kStageBytes = kATile + kBN * kRowBytes;
   static constexpr int kCopiesA = kBM / 8 / kWaves;          // 1 KB copies (8 rows) per wave
@@ -50,7 +50,9 @@ struct Cfg {
   // at most kStages later tiles have been issued.
   static constexpr int kScaleBufs = kStages + 1;
   static constexpr int kWaveCols = 16 * WO;
-  static_assert(WN * kWaveCols == kBN && kCW <= 32 && kRW <= 32, "waves cover the tile");
+  // Whether both substeps' operands fit in registers beside the accumulators.
+  static constexpr bool kDouble = XO * WO <= 16;
+  static_assert((kBN == 256 || kBN == 128) && kCW <= 32 && kRW <= 32, "scale and weight layouts");
   static_assert(kCopiesA * 8 * kWaves == kBM && kCopiesB * 8 * kWaves == kBN, "copies cover the tile");
 };
 
@@ -99,12 +101,12 @@ __device__ __forceinline__ int weight_row(int nt, int rb, int N) {
   if (MODE == SILU) {
     constexpr int W = C::kWaveCols, H = W / 2;
     const int I = N / 2;
-    int col = nt * (kBN / 2) + H * (rb / W) + rb % H;
-    if (col >= I) col = nt * (kBN / 2);
+    int col = nt * (C::kBN / 2) + H * (rb / W) + rb % H;
+    if (col >= I) col = nt * (C::kBN / 2);
     return (rb / H % 2) * I + col;
   }
-  const int r = nt * kBN + rb;
-  return r < N ? r : nt * kBN;
+  const int r = nt * C::kBN + rb;
+  return r < N ? r : nt * C::kBN;
 }
 
 typedef __attribute__((address_space(3))) v2i_t lds_v2i;
@@ -118,22 +120,48 @@ __device__ __forceinline__ v4i read_x(const uint8_t* As, int wm, int lane, int j
   const int r = 16 * (C::XO * wm + o) + (lane & 15);
   return __builtin_bit_cast(v4i, ld16(As + r * kRowBytes + (((4 * j + (lane >> 4)) ^ ((lane >> 1) & 7)) << 4)));
 }
-// GRAD: the weight tile is [128 n][256 k], chunk c of row n at c ^ 2(n % 8) ^
-// (n / 16 % 2); a transposing read gives lane i of each 16 column i of the
-// 8 x 16 block whose row i/2, half i%2 it points at.
+// GRAD: the weight tile is [128 n][kBN k] and a transposing read gives lane i
+// of each 16 column i of the 8 x 16 block whose row i/2, half i%2 it points at.
+// Chunk c of row n stands at c ^ key(n): the 8 rows of a block, and the blocks
+// 16 rows further down that the next 16 lanes read, on different banks.
+template <class C>
+__device__ __forceinline__ int grad_key(int n) {
+  return C::kBN == 256 ? (2 * (n & 7)) ^ ((n >> 4) & 1) : ((n >> 1) & 3) ^ (((n >> 4) & 1) << 2);
+}
 template <class C, int MODE>
 __device__ __forceinline__ v4i read_w(const uint8_t* As, int wn, int lane, int j, int o) {
   const uint8_t* Bs = As + C::kATile;
   if constexpr (MODE == GRAD) {
     const int i = lane & 15, g = lane >> 4;
-    const int c = ((C::WO * wn + o) ^ (2 * (i >> 1)) ^ (g & 1)) << 4;
-    const uint8_t* row = Bs + (64 * j + 16 * g + (i >> 1)) * kBN + 8 * (i & 1) + c;
+    const int n = 16 * g + (i >> 1);
+    const uint8_t* row = Bs + (64 * j + n) * C::kBN + 8 * (i & 1) + (((C::WO * wn + o) ^ grad_key<C>(n)) << 4);
     const v2i_t a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)row);
-    const v2i_t b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + 8 * kBN));
+    const v2i_t b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(row + 8 * C::kBN));
     return v4i{a[0], a[1], b[0], b[1]};
   } else {
     const int r = C::kWaveCols * wn + 16 * o + (lane & 15);
     return __builtin_bit_cast(v4i, ld16(Bs + r * kRowBytes + (((4 * j + (lane >> 4)) ^ ((lane >> 1) & 7)) << 4)));
+  }
+}
+
+// The WO x NX products of one substep, its reads of another substep's operands
+// (read(0 .. WO + NX - 1)) and copies (copy(0 .. kCopies - 1)) spread over them
+// in a pinned order: the reads over the first half, so that they are there in
+// time.
+template <class C, int NX, class Read, class Copy>
+__device__ __forceinline__ void mma_reading(v4i (&acc)[C::WO][NX ? NX : 1], const v4i (&w)[C::WO],
+                                            const v4i (&x)[NX ? NX : 1], Read read, Copy copy) {
+  constexpr int kM = C::WO * NX, kR = C::WO + NX;
+#pragma unroll
+  for (int m = 0; m < kM; ++m) {
+    acc[m / NX][m % NX] = mfma_i8_16x16x64(w[m / NX], x[m % NX], acc[m / NX][m % NX]);
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+      if (r * (kM / 2) / kR == m) read(r);
+#pragma unroll
+    for (int i = 0; i < C::kCopies; ++i)
+      if (i * kM / C::kCopies == m) copy(i);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -183,7 +211,7 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
       const int I = g.N / 2;
 #pragma unroll
       for (int wo = 0; wo < C::WO / 2; ++wo) {
-        const int wl = 16 * wo + m0, col0 = t.nt * (kBN / 2) + C::kWaveCols / 2 * wn + wl;
+        const int wl = 16 * wo + m0, col0 = t.nt * (C::kBN / 2) + C::kWaveCols / 2 * wn + wl;
         if (col0 >= I) continue;
         const int rg = C::kWaveCols * wn + wl, ru = rg + C::kWaveCols / 2;
         const v4f sg = *reinterpret_cast<const v4f*>(sc + (rg / C::kCW) * 64 + rg % C::kCW);
@@ -197,7 +225,7 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
     } else {
 #pragma unroll
       for (int wo = 0; wo < C::WO; ++wo) {
-        const int wl = C::kWaveCols * wn + 16 * wo + m0, col0 = t.nt * kBN + wl;
+        const int wl = C::kWaveCols * wn + 16 * wo + m0, col0 = t.nt * C::kBN + wl;
         if (col0 >= (MODE == GRAD ? g.K : g.N)) continue;
         if constexpr (MODE == GRAD) {
           float b[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
@@ -242,15 +270,15 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   const int wm = wid / C::WN, wn = wid % C::WN;
   const int N = g.N, K = g.K, P = g.P, E = g.E;
   const int cols = MODE == SILU ? N / 2 : MODE == GRAD ? K : N;
-  const int n_tiles = MODE == SILU ? (cols + kBN / 2 - 1) / (kBN / 2) : (cols + kBN - 1) / kBN;
+  const int n_tiles = MODE == SILU ? (cols + C::kBN / 2 - 1) / (C::kBN / 2) : (cols + C::kBN - 1) / C::kBN;
   const int a_pitch = MODE == GRAD ? plane_pitch(N) : K;
   const int steps = a_pitch / kRowBytes;
+  const bool ragged = N % kRowBytes != 0;  // GRAD: the last stage ends inside
   sched_build(tile_start, sched_scratch, g.offsets, E, P, kBMt, n_tiles);
   const int total = __builtin_amdgcn_readfirstlane(tile_start[E]);
   const int G = gridDim.x;
   const int first = xcd_logical_id(blockIdx.x, G);
   if (first >= total) return;
-  const int nq = ((total - first + G - 1) / G) * steps;
 
   // ---- issue cursor: sources of the next stage to copy.  Wave w copies A
   // rows [kRW w, +kRW) and weight rows (GRAD: n rows) of its own.
@@ -298,10 +326,11 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
     for (int i = 0; i < C::kCopiesB; ++i) {
       const int q = C::kCopiesB * wid + i;
       if constexpr (MODE == GRAD) {
-        // rows n = 4q .. 4q+3 of the stage, 16 chunks of 16 columns each
-        const int n = 4 * q + (lane >> 4);
-        int col = t.nt * kBN + 16 * ((lane & 15) ^ (2 * (n & 7)) ^ ((n >> 4) & 1));
-        if (col >= K) col -= kBN / 2;  // K is a multiple of 128: only the upper half may be past it
+        // kN rows n of the stage, kBN / 16 chunks of 16 columns each
+        constexpr int kChunks = C::kBN / 16, kN = 64 / kChunks;
+        const int n = kN * q + lane / kChunks;
+        int col = t.nt * C::kBN + 16 * ((lane % kChunks) ^ grad_key<C>(n));
+        if (col >= K) col -= 128;  // K is a multiple of 128: only the upper half of 256 may be past it
         pb[i] = g.w + ((int64_t)t.e * N + n) * K + col;
       } else {
         pb[i] = g.w + ((int64_t)t.e * N + weight_row<C, MODE>(t.nt, 8 * q + (lane >> 3), N)) * K + dma_chunk(lane, q);
@@ -321,26 +350,30 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
               : g.a_scale + s;
   };
   const uint32_t ring_lds = lds_addr(ring), sbuf_lds = lds_addr(sbuf);
-  // Copy i of this wave's share of the cursor's stage, into the slot at `base`.
+  // Copy i of this wave's share of the cursor's stage, into the slot at `base`;
+  // its source moves on to the next stage.
+  const int64_t b_step = MODE == GRAD ? (int64_t)kRowBytes * K : kRowBytes;
   auto copy = [&](uint32_t base, int i) __attribute__((always_inline)) {
-    const int64_t ko = (int64_t)is_step * kRowBytes;
     if (i < C::kCopiesA) {
-      dma16(pa[i] + ko, __builtin_amdgcn_readfirstlane(base + (C::kCopiesA * wid + i) * 1024));
+      dma16(pa[i], __builtin_amdgcn_readfirstlane(base + (C::kCopiesA * wid + i) * 1024));
+      pa[i] += kRowBytes;
     } else {
       const int q = C::kCopiesB * wid + i - C::kCopiesA;
-      int64_t kb = ko;
-      if (MODE == GRAD) {
-        kb = ko * K;
+      const uint8_t* src = pb[i - C::kCopiesA];
+      if (MODE == GRAD && ragged && is_step == steps - 1) {
         // rows past N meet zeros of the planes, so any row's bytes do: the
-        // last stage's rows n % 32 are there, N being a multiple of 32
-        if (is_step * kRowBytes + 4 * q >= N) kb -= (int64_t)(4 * q & ~31) * K;
+        // stage's rows n % 32 are there, N being a multiple of 32
+        const int n = 1024 / C::kBN * q;
+        if (is_step * kRowBytes + n >= N) src -= (int64_t)(n & ~31) * K;
       }
-      dma16(pb[i - C::kCopiesA] + kb, __builtin_amdgcn_readfirstlane(base + C::kATile + q * 1024));
+      dma16(src, __builtin_amdgcn_readfirstlane(base + C::kATile + q * 1024));
+      pb[i - C::kCopiesA] += b_step;
     }
   };
   // After a stage's copies: a tile's scales ride with its first stage, and the
   // cursor moves on.  Past the last tile it goes over that tile again, into
   // slots that nobody reads: every wave then waits for constant counts.
+  const int last_item = first + (total - 1 - first) / G * G;
   auto advance = [&]() __attribute__((always_inline)) {
     if (is_step == 0) {
       dma4(psc, __builtin_amdgcn_readfirstlane(sbuf_lds + is_sbuf * C::kScaleBytes + wid * 256));
@@ -349,7 +382,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
     if (++is_step == steps) {
       is_step = 0;
       is_item += G;
-      if (is_item < total) set_tile(is_item);
+      set_tile(min(is_item, last_item));
     }
   };
   // Stage q is there once at most `newer` later stages of this wave's copies
@@ -393,22 +426,30 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
     }
 #pragma unroll
     for (int xo = 0; xo < NX; ++xo) x[xo] = read_x<C>(As, wm, lane, 0, xo);
+    v4i x1[NA], w1[C::WO];  // kDouble
     int st = 0;
     do {
+      if constexpr (C::kDouble) {
+        mma_reading<C, NX>(acc, w, x, [&](int r) __attribute__((always_inline)) {
+          if (r < C::WO) w1[r] = read_w<C, MODE>(As, wn, lane, 1, r);
+          else x1[r - C::WO] = read_x<C>(As, wm, lane, 1, r - C::WO);
+        }, [](int) {});
+      } else {
 #pragma unroll
-      for (int wo = 0; wo < (NX ? C::WO : 0); ++wo) {
+        for (int wo = 0; wo < (NX ? C::WO : 0); ++wo) {
+#pragma unroll
+          for (int xo = 0; xo < NX; ++xo) {
+            acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
+            if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 1, xo);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          w[wo] = read_w<C, MODE>(As, wn, lane, 1, wo);
+        }
 #pragma unroll
         for (int xo = 0; xo < NX; ++xo) {
-          acc[wo][xo] = mfma_i8_16x16x64(w[wo], x[xo], acc[wo][xo]);
-          if (wo == C::WO - 1) x[xo] = read_x<C>(As, wm, lane, 1, xo);
+          acc[0][xo] = mfma_i8_16x16x64(w[0], x[xo], acc[0][xo]);
           __builtin_amdgcn_sched_barrier(0);
         }
-        w[wo] = read_w<C, MODE>(As, wn, lane, 1, wo);
-      }
-#pragma unroll
-      for (int xo = 0; xo < NX; ++xo) {
-        acc[0][xo] = mfma_i8_16x16x64(w[0], x[xo], acc[0][xo]);
-        __builtin_amdgcn_sched_barrier(0);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       arrive(std::integral_constant<int, C::kStages - 2>());
@@ -418,6 +459,11 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
       if constexpr (NX == 0) {
 #pragma unroll
         for (int i = 0; i < C::kCopies; ++i) copy(refill, i);
+      } else if constexpr (C::kDouble) {
+        mma_reading<C, NX>(acc, w1, x1, [&](int r) __attribute__((always_inline)) {
+          if (r < C::WO) w[r] = read_w<C, MODE>(As, wn, lane, 0, r);
+          else x[r - C::WO] = read_x<C>(As, wm, lane, 0, r - C::WO);
+        }, [&](int i) __attribute__((always_inline)) { copy(refill, i); });
       } else {
         w[0] = read_w<C, MODE>(As, wn, lane, 0, 0);
         constexpr int kRest = (C::WO - 1) * NX;
@@ -746,40 +792,47 @@ __global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
 }
 
 // ------------------------------------------------------------------ launch
-typedef Cfg<2, 4, 8, 4, 2> Large;   // 256 A rows
-typedef Cfg<2, 4, 4, 4, 3> Medium;  // 128
-typedef Cfg<1, 8, 4, 2, 3> Small;   // 64
+typedef Cfg<2, 4, 8, 4, 2> Large;   // 256 A rows x 256 columns
+typedef Cfg<2, 4, 4, 4, 3> Medium;  // 128 x 256
+typedef Cfg<1, 8, 4, 2, 3> Small;   // 64 x 256
+typedef Cfg<1, 4, 4, 2, 5> Narrow;  // 64 x 128
 
-// Columns that one n-tile covers, and n-tiles.
-int64_t n_tiles_of(int mode, int64_t N, int64_t K) {
-  const int64_t cols = mode == SILU ? N / 2 : mode == GRAD ? K : N, w = mode == SILU ? kBN / 2 : kBN;
-  return (cols + w - 1) / w;
+int out_cols(const Int8Args& g, int mode) { return mode == SILU ? g.N / 2 : mode == GRAD ? g.K : g.N; }
+
+template <class C, int MODE>
+int64_t n_tiles(const Int8Args& g) {
+  const int w = MODE == SILU ? C::kBN / 2 : C::kBN;
+  return (out_cols(g, MODE) + w - 1) / w;
 }
 
 template <class C, int OUT, int MODE>
 hipError_t go_tiles(const Int8Args& g, int num_cus, hipStream_t stream) {
   const int bm = MODE == GRAD ? C::kBM / 2 : C::kBM;
   // upper bound on tiles: every expert adds at most one partial m-tile
-  const int64_t tiles = (((int64_t)g.P + bm - 1) / bm + std::min(g.E, g.P)) * n_tiles_of(MODE, g.N, g.K);
+  const int64_t tiles = (((int64_t)g.P + bm - 1) / bm + std::min(g.E, g.P)) * n_tiles<C, MODE>(g);
   const int grid = (int)std::min<int64_t>(tiles, num_cus);
   hipLaunchKernelGGL((int8_tiles<C, OUT, MODE>), dim3(grid), dim3(C::kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
-// The tile height: the least of (tiles a compute unit works through) x (the
-// time of one), with half a partial m-tile for every expert.  Relative times
-// of a tile, measured with 32 experts of 4096 x 4096 and 512 rows each
-// (forward 315, 327 and 445 us for 256, 128 and 64 rows; gradient 588, 648 and
-// 905): 1, 0.54, 0.36.  At 128 rows an expert the forward call takes 155, 139
-// and 159 us, at 16 rows 135, 125 and 124.
+// Tiles that a compute unit works through, at the least one, with half a
+// partial m-tile for every expert, times the time of one relative to Large's.
+template <class C, int MODE>
+double cost(const Int8Args& g, int num_cus, double one) {
+  const double mt = (double)g.P * (MODE == GRAD ? 2 : 1) / C::kBM + 0.5 * std::min(g.E, g.P);
+  return one * std::max(1.0, mt * (double)n_tiles<C, MODE>(g) / num_cus);
+}
+
+// The tile of the least cost.  Relative times of a tile, measured with 32
+// experts of 4096 x 4096 and 512 rows each (forward 315, 327 and 445 us for
+// 256, 128 and 64 rows; gradient 588, 648 and 905): 1, 0.54, 0.36.  At 128 rows
+// an expert the forward call takes 155, 139 and 159 us, at 16 rows 135, 125 and
+// 124.
 template <int OUT, int MODE>
 hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
-  const double n_tiles = (double)n_tiles_of(MODE, g.N, g.K), partial = 0.5 * std::min(g.E, g.P);
-  const int planes = MODE == GRAD ? 2 : 1;
-  auto cost = [&](int bm, double one) {
-    return one * std::max(1.0, ((double)g.P * planes / bm + partial) * n_tiles / num_cus);
-  };
-  const double l = cost(Large::kBM, 1.0), m = cost(Medium::kBM, 0.54), s = cost(Small::kBM, 0.36);
+  const double l = cost<Large, MODE>(g, num_cus, 1.0), m = cost<Medium, MODE>(g, num_cus, 0.54),
+               s = cost<Small, MODE>(g, num_cus, 0.36), n = cost<Narrow, MODE>(g, num_cus, 0.22);
+  if (n <= s && n <= m && n <= l) return go_tiles<Narrow, OUT, MODE>(g, num_cus, stream);
   if (s <= m && s <= l) return go_tiles<Small, OUT, MODE>(g, num_cus, stream);
   if (m <= l) return go_tiles<Medium, OUT, MODE>(g, num_cus, stream);
   return go_tiles<Large, OUT, MODE>(g, num_cus, stream);
@@ -788,11 +841,15 @@ hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
 // AUTO streams below 10 rows an expert: with 32 experts of 4096 x 4096, 4 rows
 // each take 90 us streamed and 123 in tiles, 10 rows 93 and 124, 16 rows 128
 // and 124 (experts past 16 rows stream their weights again); with 256 experts
-// of 2048 x 2048 6 rows take 172 and 185, 10 rows 190 and 188.
+// of 2048 x 2048 6 rows take 172 and 185, 10 rows 190 and 188.  And where no
+// wave gets a second item, so that a call is as long as one item: one expert of
+// 4096 x 4096 with 64 rows 11 us streamed and 22 in tiles, with 256 rows 26 and
+// 22.
 template <int OUT, int MODE>
 hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
   if (g.P == 0) return hipSuccess;
-  if (sched == 1 || (sched == 0 && g.P < (int64_t)10 * g.E)) {
+  const int64_t items = (((int64_t)g.P + dd::kM - 1) / dd::kM + std::min(g.E, g.P)) * (g.N / dd::kRowsW);
+  if (sched == 1 || (sched == 0 && (g.P < (int64_t)10 * g.E || items <= (int64_t)num_cus * 2 * dd::kWaves))) {
     hipLaunchKernelGGL((int8_decode<OUT, MODE>), dim3(num_cus * 2), dim3(64 * dd::kWaves), 0, stream, g);
     return hipGetLastError();
   }
@@ -824,13 +881,13 @@ hipError_t launch_gemm_int8(const GroupedArgs& g, const int8_t* a, const float* 
   }
 }
 
-// Work items and the stages that one workgroup counts stay below 2^30.
+// Work items, and the stages that one workgroup counts, stay below 2^30.
 bool int8_fits(int64_t P, int E, int64_t N, int64_t K) {
-  const int64_t items = (P / dd::kM + E) * (N / dd::kRowsW), tiles = (P / Small::kBM + E) * (N / (kBN / 2) + 1);
-  return items < (1 << 30) && (tiles / 64 + 1) * (K / kRowBytes) < (1 << 30);
+  const int64_t items = (P / dd::kM + E) * (N / dd::kRowsW);
+  return items < (1 << 30) && (items / 64 + 1) * (K / kRowBytes) < (1 << 30);
 }
 bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K) {
-  const int64_t tiles = (P / (Small::kBM / 2) + E) * (K / kBN + 1);
+  const int64_t tiles = (P / (Narrow::kBM / 2) + E) * (K / Narrow::kBN);
   return tiles < (1 << 30) && (tiles / 64 + 1) * (plane_pitch((int)N) / kRowBytes) < (1 << 30);
 }
 
