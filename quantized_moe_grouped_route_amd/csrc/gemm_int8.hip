@@ -199,33 +199,41 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
                                          const v4i (&acc)[C::WO][NX]) {
   constexpr int kP = MODE == GRAD ? 2 : 1;  // A operands per 16 routed rows
   const int l16 = lane & 15, m0 = 4 * (lane >> 4);
-  const float* sc = sb + 32;
+  // every scale first: read one by one they cost a trip to LDS per operand
+  v4f sw[C::WO];
+  float sa[NX];
+#pragma unroll
+  for (int wo = 0; wo < C::WO; ++wo) {
+    const int c = C::kWaveCols * wn + 16 * wo + m0;
+    if (MODE != GRAD) sw[wo] = *reinterpret_cast<const v4f*>(sb + 32 + (c / C::kCW) * 64 + c % C::kCW);
+  }
 #pragma unroll
   for (int xo = 0; xo < NX; xo += kP) {
-    const int ar = 16 * (C::XO * wm + xo) + l16;                     // row of the A tile
-    const int r = 16 * ((C::XO * wm + xo) / kP) + l16;               // row of the tile's routed rows
+    const int ar = 16 * (C::XO * wm + xo) + l16;  // row of the A tile
+    sa[xo] = sb[(ar / C::kRW) * 64 + ar % C::kRW];
+  }
+#pragma unroll
+  for (int xo = 0; xo < NX; xo += kP) {
+    const int r = 16 * ((C::XO * wm + xo) / kP) + l16;  // row of the tile's routed rows
     if (r >= t.rows) continue;
     const int64_t orow = t.row0 + r;
-    const float sa = sb[(ar / C::kRW) * 64 + ar % C::kRW];
     if constexpr (MODE == SILU) {
+      constexpr int H = C::WO / 2;
       const int I = g.N / 2;
 #pragma unroll
-      for (int wo = 0; wo < C::WO / 2; ++wo) {
-        const int wl = 16 * wo + m0, col0 = t.nt * (C::kBN / 2) + C::kWaveCols / 2 * wn + wl;
+      for (int wo = 0; wo < H; ++wo) {
+        const int col0 = t.nt * (C::kBN / 2) + C::kWaveCols / 2 * wn + 16 * wo + m0;
         if (col0 >= I) continue;
-        const int rg = C::kWaveCols * wn + wl, ru = rg + C::kWaveCols / 2;
-        const v4f sg = *reinterpret_cast<const v4f*>(sc + (rg / C::kCW) * 64 + rg % C::kCW);
-        const v4f su = *reinterpret_cast<const v4f*>(sc + (ru / C::kCW) * 64 + ru % C::kCW);
         float o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          o[i] = silu(sa * sg[i] * (float)acc[wo][xo][i]) * (sa * su[i] * (float)acc[wo + C::WO / 2][xo][i]);
+          o[i] = silu(sa[xo] * sw[wo][i] * (float)acc[wo][xo][i]) * (sa[xo] * sw[wo + H][i] * (float)acc[wo + H][xo][i]);
         put4<OUT>(g.out, orow * I + col0, o);
       }
     } else {
 #pragma unroll
       for (int wo = 0; wo < C::WO; ++wo) {
-        const int wl = C::kWaveCols * wn + 16 * wo + m0, col0 = t.nt * C::kBN + wl;
+        const int col0 = t.nt * C::kBN + C::kWaveCols * wn + 16 * wo + m0;
         if (col0 >= (MODE == GRAD ? g.K : g.N)) continue;
         if constexpr (MODE == GRAD) {
           float b[4] = {0.f, 0.f, 0.f, 0.f}, o[4];
@@ -241,15 +249,14 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_fmaf(__builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + 1][i]), sa, b[i]);
+            o[i] = __builtin_fmaf(__builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + 1][i]), sa[xo], b[i]);
           put4<OUT>(g.out, idx, o);
         } else if constexpr (OUT == OUT_I32) {
           *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + orow * g.N + col0) = acc[wo][xo];
         } else {
-          const v4f sw = *reinterpret_cast<const v4f*>(sc + (wl / C::kCW) * 64 + wl % C::kCW);
           float o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[wo][xo][i];
+          for (int i = 0; i < 4; ++i) o[i] = sa[xo] * sw[wo][i] * (float)acc[wo][xo][i];
           put4<OUT>(g.out, orow * g.N + col0, o);
         }
       }
