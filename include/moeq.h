@@ -548,9 +548,9 @@ moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, i
  * Requires as grouped_gemm_qint4: K % 128 == 0 and N % 32 == 0 (else
  * MOEQ_EALIGN), K < 131072 so that the int32 accumulator cannot wrap (else
  * MOEQ_EINVAL), a, w and out 16-byte and the scales and tables 4-byte
- * aligned, 1 <= E <= 1024, 1 <= topk <= 64; and out disjoint from the inputs
- * and sizes that one launch can count, (P/16 + E) * N/16 < 2^30 (else
- * MOEQ_EINVAL).
+ * aligned, 1 <= E <= 1024, 1 <= topk <= 64; and rows_a * topk >= P (TOKEN) or
+ * rows_a >= P (SORTED), out disjoint from the inputs, and sizes that one
+ * launch can count, (P/16 + E) * N/16 < 2^30 (else MOEQ_EINVAL).
  * Two schedules give identical outputs: MFMA tiles of 64, 128 or 256 rows
  * (PREFILL, by the average rows of an expert), and waves streaming 16 weight
  * rows x at most 16 routed rows (DECODE).  AUTO streams when P < 10 * E.

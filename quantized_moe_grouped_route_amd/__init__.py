@@ -785,6 +785,8 @@ def _silu_common(rows, cols, expert_offsets, what):
     if expert_offsets is None:
         return I, -(-I // CHECKPOINT_BLOCK), 0
     _need(expert_offsets, "expert_offsets", torch.int32, 1)
+    if expert_offsets.numel() < 2:
+        raise ValueError("expert_offsets must have E+1 entries")
     return I, -(-I // CHECKPOINT_BLOCK), expert_offsets.numel() - 1
 
 

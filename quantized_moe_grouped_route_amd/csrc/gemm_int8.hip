@@ -170,9 +170,11 @@ __device__ __forceinline__ void put4(void* out, int64_t idx, const float (&o)[4]
   typedef typename OutT<OUT>::T T;
   T* dst = static_cast<T*>(out) + idx;
   if constexpr (sizeof(T) == 2) {
-    const u32 lo = (u32)OutT<OUT>::from(o[0]) | ((u32)OutT<OUT>::from(o[1]) << 16);
-    const u32 hi = (u32)OutT<OUT>::from(o[2]) | ((u32)OutT<OUT>::from(o[3]) << 16);
-    *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+    u32 w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = (u32)OutT<OUT>::from(rounded(o[2 * i])) | ((u32)OutT<OUT>::from(rounded(o[2 * i + 1])) << 16);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   } else {
     *reinterpret_cast<v4f*>(dst) = v4f{o[0], o[1], o[2], o[3]};
   }

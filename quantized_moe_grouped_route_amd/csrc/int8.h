@@ -15,6 +15,15 @@ __host__ __device__ __forceinline__ int plane_pitch(int N) { return (N + 127) / 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 __device__ __forceinline__ float silu(float g) { return g * sigmoid(g); }
 
+// The fp32 value itself, rounded.  It keeps the compiler from merging a product
+// with the conversion after it (one rounding where the kernels of other
+// schedules and tile sizes make two): a row's bits then never depend on which
+// of them computed it.
+__device__ __forceinline__ float rounded(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 // Largest magnitude as fp32 bits: as integers, an infinity or NaN is above
 // every finite value, so it is never lost in a maximum.
 __device__ __forceinline__ u32 amax_bits(const float (&v)[8]) {

@@ -601,12 +601,14 @@ moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t ro
                                int64_t P, int32_t topk, int32_t E, int64_t N, int64_t K, moeq_act act,
                                moeq_dtype out_dtype, void* out, moeq_sched sched, void* stream) {
   const char* fn = "grouped_gemm_qint8";
-  moeq_status st = check_grouped(fn, a, rows_a, a_row, w, expert_offsets, P, topk, E, N, K, out, 32);
+  // without rows a, out and a_scale are not read and may be null
+  moeq_status st = check_grouped(fn, P == 0 && !a ? w : a, rows_a, a_row, w, expert_offsets, P, topk, E, N, K,
+                                 P == 0 && !out ? w : out, 32);
   if (st != MOEQ_OK) return st;
   // products of at most 2^14: K < 2^17 keeps every int32 partial sum below 2^31
   if (K >= (int64_t(1) << 17))
     return fail(MOEQ_EINVAL, "%s: K=%lld must be below 131072 (int32 accumulator range)", fn, (long long)K);
-  if (!a_scale || !w_scale) return fail(MOEQ_EINVAL, "%s: null scale pointer", fn);
+  if ((P > 0 && !a_scale) || !w_scale) return fail(MOEQ_EINVAL, "%s: null scale pointer", fn);
   if (!aligned(a_scale, 4) || !aligned(w_scale, 4) || !aligned(sorted_pair_ids, 4))
     return fail(MOEQ_EALIGN, "%s: scales and tables must be 4-byte aligned", fn);
   if (act != MOEQ_ACT_NONE && act != MOEQ_ACT_SILU_MUL) return fail(MOEQ_EUNSUPPORTED, "%s: act %d", fn, act);
@@ -614,8 +616,8 @@ moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t ro
     return fail(MOEQ_EUNSUPPORTED, "%s: out dtype %d", fn, out_dtype);
   if (out_dtype == MOEQ_I32 && act != MOEQ_ACT_NONE)
     return fail(MOEQ_EUNSUPPORTED, "%s: I32 output needs act NONE", fn);
-  if (a_row == MOEQ_AROW_TOKEN && !sorted_pair_ids && rows_a < P)
-    return fail(MOEQ_EINVAL, "%s: identity rows need rows_a >= P", fn);
+  if (a_row == MOEQ_AROW_TOKEN && sorted_pair_ids ? rows_a * topk < P : rows_a < P)
+    return fail(MOEQ_EINVAL, "%s: rows_a=%lld is too few for P=%lld", fn, (long long)rows_a, (long long)P);
   if (sched < MOEQ_SCHED_AUTO || sched > MOEQ_SCHED_PREFILL) return fail(MOEQ_EINVAL, "%s: sched %d", fn, sched);
   if (!moeq::int8_fits(P, E, N, K))
     return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld are too large for one launch", fn, (long long)P, E,

@@ -44,7 +44,8 @@ def _gemm(L, **kw):
     (dict(sa=None), mq.EINVAL), (dict(sw=None), mq.EINVAL), (dict(a=at(0) + 4), mq.EALIGN), (dict(sa=at(1) + 2), mq.EALIGN),
     (dict(srt=at(5) + 1), mq.EALIGN), (dict(out=at(6) + 8), mq.EALIGN), (dict(act=2), mq.EUNSUPPORTED),
     (dict(od=mq.U8), mq.EUNSUPPORTED), (dict(od=mq.I32, act=1), mq.EUNSUPPORTED), (dict(srt=None), mq.EINVAL),
-    (dict(sched=3), mq.EINVAL), (dict(sched=-1), mq.EINVAL), (dict(P=2 ** 30, N=2 ** 20), mq.EINVAL),
+    (dict(sched=3), mq.EINVAL), (dict(sched=-1), mq.EINVAL), (dict(P=2 ** 30, N=2 ** 20, rows=2 ** 30), mq.EINVAL),
+    (dict(rows=7), mq.EINVAL), (dict(arow=1, rows=15), mq.EINVAL), (dict(arow=1, rows=15, srt=None), mq.EINVAL),
     (dict(out=at(0)), mq.EINVAL), (dict(out=at(1)), mq.EINVAL), (dict(out=at(2) + 4 * 64 * 128 - 16), mq.EINVAL),
     (dict(out=at(3)), mq.EINVAL), (dict(out=at(4)), mq.EINVAL), (dict(out=at(5)), mq.EINVAL),
     (dict(out=at(5) - 16 * 64 * 2 + 16), mq.EINVAL), (dict(out=at(5) - 16 * 64 * 4 + 16, od=mq.I32), mq.EINVAL),
@@ -53,6 +54,11 @@ def _gemm(L, **kw):
 def test_gemm_rejects(L, kw, status):
     assert _gemm(L, **kw) == status
     assert b"grouped_gemm_qint8" in L.moeq_last_error()
+
+
+def test_gemm_without_rows_takes_null_rows(L):
+    assert _gemm(L, P=0, rows=0, a=None, sa=None, out=None, srt=None) == mq.OK
+    assert _gemm(L, P=0, rows=0, a=None, sa=None, out=None, srt=None, w=None) == mq.EINVAL
 
 
 def _grad(L, **kw):
@@ -212,6 +218,8 @@ def test_binding_refuses_gemm_backward(L, kw, error, text):
     (lambda: mq.moe_silu_mul(_t(4, 16), checkpoint=True, ck=_t(4, 8, dt=I8)), ValueError, "ck must be"),
     (lambda: mq.moe_silu_mul(_t(4, 272), checkpoint=True, cs=_t(4, 2, dt=F4)), ValueError, "cs must be"),
     (lambda: mq.moe_silu_mul(_t(4, 16), _t(3, dt=torch.int64)), TypeError, "expert_offsets has dtype"),
+    (lambda: mq.moe_silu_mul(_t(4, 16), _t(0, dt=I4)), ValueError, "E\\+1 entries"),
+    (lambda: mq.moe_silu_mul_backward(_t(4, 8), _t(1, dt=I4), gu=_t(4, 16)), ValueError, "E\\+1 entries"),
     (lambda: mq.moe_silu_mul_backward(_t(4, 8)), ValueError, "give gu"),
     (lambda: mq.moe_silu_mul_backward(_t(4, 8), gu=_t(4, 16), ck=_t(4, 16, dt=I8), cs=_t(4, 2, dt=F4)), ValueError, "give gu"),
     (lambda: mq.moe_silu_mul_backward(_t(4, 8), ck=_t(4, 16, dt=I8)), ValueError, "give gu"),

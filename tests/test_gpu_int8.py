@@ -126,6 +126,7 @@ GEMMS = [  # T, k, E, N, K, a_row, kind, skip
     (129, 1, 2, 1056, 384, "token", "one", 0.0),
     (257, 1, 1, 800, 256, "sorted", "one", 0.0),
     (301, 3, 37, 1056, 1152, "sorted", "repeat", 0.2),
+    (40, 2, 1024, 64, 128, "token", "repeat", 0.1),           # the most experts
     (700, 2, 7, 320, 512, "token", "repeat", 0.1),
     (900, 4, 9, 1312, 896, "token", "distinct", 0.05),
 ]
@@ -137,6 +138,7 @@ def test_gemm_every_type_and_schedule(case):
     p = Experts(11, *case)
     r = p.oracle()
     n, I = p.n, p.N // 2
+    seen = {}
     for sched in ("auto", "decode", "prefill"):
         out = torch.full((p.P, p.N), 77, dtype=torch.int32, device="cuda")
         assert p.run(torch.int32, out=out, sched=sched) is out
@@ -150,6 +152,8 @@ def test_gemm_every_type_and_schedule(case):
             ref, g = oracle.silu_gate(r["y"]), np.abs(r["y"][:, :I])
             within(h[:n], ref, half_step(ref, dtype) + (16 + 8 * g) * U * np.abs(ref) + 2.0 ** -118, (sched, dtype, "silu"))
             assert np.all(h[n:] == 7)
+            for x, v in (("y", y), ("h", h[:n])):             # every schedule gives the same bits
+                assert np.array_equal(seen.setdefault((x, dtype), v), v), (sched, dtype, x)
 
 
 def test_gemm_every_row_as_it_is():
@@ -221,6 +225,75 @@ def test_gemm_offsets_past_32_bits():
         within(host(dx[rows]), ref.cpu().numpy(), tol)
 
 
+# Rows of an expert around every tile's height and its halves and quarters; few
+# experts with many rows.  With these widths each tile size of the schedule is
+# the one taken (64 x 128, 64, 128 and 256 x 256).
+MANY = [0, 1, 15, 16, 17, 31, 33, 47, 64, 65, 100, 128, 129, 200, 255, 256, 257, 300, 511, 513, 0, 77]
+FEW = [3000, 257, 1100]
+
+
+def grouped(counts, N, K, seed=14, rows_past=5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    off = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+    n, E = int(off[-1]), len(counts)
+    a = torch.randint(-128, 128, (n + rows_past, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    sa = (torch.rand(n + rows_past, generator=g, device="cuda") + 0.5) / 64
+    sw = (torch.rand(E, N, generator=g, device="cuda") + 0.5) * K ** -0.5 / 64
+    return g, off, off.tolist(), n, a, w, sa, sw
+
+
+@pytest.mark.parametrize("counts,N,K", [(MANY, 288, 128), (MANY, 1024, 384), (MANY, 4096, 256), (FEW, 4096, 256),
+                                        (FEW, 4352, 128)])
+def test_gemm_tiles_of_every_height(counts, N, K):
+    g, off, at, n, a, w, sa, sw = grouped(counts, N, K)
+    order = torch.cat([torch.randperm(n, generator=g, device="cuda"), torch.full((5,), -1, device="cuda")]).int()
+    I = N // 2
+    for srt, topk, a_row in ((None, 1, "sorted"), (order, 1, "token")):
+        acc = torch.full((n + 5, N), 77, dtype=torch.int32, device="cuda")
+        mq.grouped_gemm_qint8(a, sa, w, sw, off, srt, topk, a_row=a_row, out_dtype=torch.int32, out=acc, sched="prefill")
+        h = torch.full((n + 5, I), 7.0, device="cuda")
+        mq.grouped_gemm_qint8(a, sa, w, sw, off, srt, topk, a_row=a_row, act="silu_mul", out_dtype=F32, out=h,
+                              sched="prefill")
+        row = torch.arange(n, device="cuda") if srt is None else srt[:n].long()
+        for e, (lo, hi) in enumerate(zip(at, at[1:])):
+            if hi == lo:
+                continue
+            r = row[lo:hi]
+            ref = a[r].double() @ w[e].double().T.contiguous()
+            assert torch.equal(acc[lo:hi].double(), ref), (a_row, e)
+            y = ref * sa[r].double()[:, None] * sw[e].double()
+            ref = y[:, :I] * torch.sigmoid(y[:, :I]) * y[:, I:]
+            tol = (16 + 8 * y[:, :I].abs()) * U * ref.abs() + U * ref.abs() + 2.0 ** -118
+            assert bool(((h[lo:hi].double() - ref).abs() <= tol).all()), (a_row, e)
+        assert bool((acc[n:] == 77).all()) and bool((h[n:] == 7).all())
+
+
+@pytest.mark.parametrize("counts,N,K", [(MANY, 160, 128), (MANY, 96, 512), (MANY, 288, 2048), (MANY, 128, 1920),
+                                        (FEW, 224, 2048), (FEW, 128, 2176)])
+def test_gradient_tiles_of_every_height(counts, N, K):
+    g, off, at, n, _, w, _, sw = grouped(counts, N, K, 15)
+    dy = torch.randn(n + 5, N, generator=g, device="cuda").to(BF16)
+    base = torch.randn(n + 5, K, generator=g, device="cuda").to(BF16)
+    dx = torch.full((n + 5, K), 7.0, dtype=BF16, device="cuda")
+    mq.grouped_gemm_qint8_backward(dy, w, sw, off, base=base, dx=dx)
+    for e, (lo, hi) in enumerate(zip(at, at[1:])):
+        if hi == lo:
+            continue
+        d, we = dy[lo:hi].double() * sw[e].double(), w[e].double()
+        ref = d @ we + base[lo:hi].double()
+        tol = (ref.abs() * 2.0 ** -8 + 0.51 / 32512 * d.abs().amax(1, keepdim=True) * we.abs().sum(0) +
+               8 * U * (d.abs() @ we.abs()) + U * base[lo:hi].double().abs() + 1e-40)
+        assert bool(((dx[lo:hi].double() - ref).abs() <= tol).all()), e
+    assert bool((dx[n:] == 7).all())
+    # a row's bits do not depend on the rows beside it, which choose the tile
+    lo, hi = at[-2], at[-2] + 3
+    one = torch.zeros_like(off)
+    one[-1] = 3
+    alone = mq.grouped_gemm_qint8_backward(dy[lo:hi].clone(), w, sw, one, base=base[lo:hi].clone())
+    assert torch.equal(alone, dx[lo:hi])
+
+
 # ----------------------------------------------------------------- gradient
 GRADS = [  # T, k, E, N, K, kind, skip
     (1, 1, 1, 32, 128, "distinct", 0.0),
@@ -234,6 +307,7 @@ GRADS = [  # T, k, E, N, K, kind, skip
     (65, 1, 1, 1056, 256, "one", 0.0),
     (128, 1, 1, 96, 1152, "one", 0.0),
     (301, 3, 37, 544, 1152, "repeat", 0.2),
+    (40, 2, 1024, 64, 128, "repeat", 0.1),
     (700, 2, 7, 2080, 384, "repeat", 0.1),
     (900, 4, 9, 8224, 128, "distinct", 0.05),
     (20, 2, 3, 32800, 256, "repeat", 0.1),                    # rows longer than the registers hold
@@ -594,4 +668,22 @@ def test_malformed_tables_touch_nothing_out_of_range():
             assert bool((out[p.P:] == 0).all())
         mq.grouped_gemm_qint8_backward(dy, p.d["w"], p.d["sw"], o)
         mq.moe_silu_mul(gu, o, checkpoint=True)
+    torch.cuda.synchronize()
+
+
+def test_no_rows():
+    z = lambda *s, dt=BF16: torch.zeros(*s, dtype=dt, device="cuda")
+    i4, i8 = torch.int32, torch.int8
+    q, s = mq.quantize_int8_rows(z(0, 64))
+    off, w, sw = z(4, dt=i4), z(3, 64, 128, dt=i8), z(3, 64, dt=F32)
+    for sched in ("auto", "decode", "prefill"):
+        y = mq.grouped_gemm_qint8(z(0, 128, dt=i8), z(0, dt=F32), w, sw, off, z(0, dt=i4), 2, sched=sched)
+        assert y.shape == (0, 64)
+    assert mq.grouped_gemm_qint8_backward(z(0, 64), w, sw, off, base=z(0, 128)).shape == (0, 128)
+    h, ck, cs = mq.moe_silu_mul(z(0, 272), off, checkpoint=True)
+    assert h.shape == (0, 136) and ck.shape == (0, 272) and cs.shape == (0, 4)
+    d, h = mq.moe_silu_mul_backward(z(0, 136), ck=ck, cs=cs, need_h=True)
+    assert d.shape == (0, 272) and h.shape == (0, 136)
+    assert mq.moe_silu_mul_backward(z(0, 136), gu=z(0, 272))[0].shape == (0, 272)
+    assert mq.moe_silu_mul_again(ck, cs).shape == (0, 136)
     torch.cuda.synchronize()
