@@ -8,7 +8,8 @@
 // output bytes.  Rows of up to 16384 elements are held in registers and read
 // once: by one wave each up to 2048, four rows of a workgroup at a time (16384
 // rows of 256 bf16: 7 us, against 19 with a workgroup each), by a workgroup
-// above.  Longer rows are read twice.
+// above (16384 rows of 14336 f16, 705 MB: 125 us, 5.6 TB/s).  Longer rows are
+// read twice.
 #include <algorithm>
 
 #include "int8.h"
