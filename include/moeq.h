@@ -553,7 +553,8 @@ moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, i
  * launch can count, (P/16 + E) * N/16 < 2^30 (else MOEQ_EINVAL).
  * Two schedules give identical outputs: MFMA tiles of 64, 128 or 256 rows
  * (PREFILL, by the average rows of an expert), and waves streaming 16 weight
- * rows x at most 16 routed rows (DECODE).  AUTO streams when P < 10 * E.
+ * rows x at most 16 routed rows (DECODE).  AUTO streams when P < 10 * E, and
+ * where every wave of the GPU gets at most one such item.
  * ---------------------------------------------------------------------- */
 moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t rows_a, moeq_arow a_row, const int8_t* w,
                                const float* w_scale, const int32_t* expert_offsets, const int32_t* sorted_pair_ids,
