@@ -398,8 +398,18 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
     }
     if (++is_step == steps) {
       is_step = 0;
-      is_item += G;
-      set_tile(min(is_item, last_item));
+      if (C::kBN == 128 && is_item >= last_item) {
+        // the same sources without a look-up, in the tile of short calls: 7.4 us
+        // for 8.5 with 128 rows and 4 experts of 256 x 256 (the branch costs
+        // long calls 4 % in Large, 0.5 % in Medium)
+#pragma unroll
+        for (int i = 0; i < C::kCopiesA; ++i) pa[i] -= a_pitch;
+#pragma unroll
+        for (int i = 0; i < C::kCopiesB; ++i) pb[i] -= steps * b_step;
+      } else {
+        is_item += G;
+        set_tile(min(is_item, last_item));
+      }
     }
   };
   // Stage q is there once at most `newer` later stages of this wave's copies
