@@ -282,6 +282,14 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   __shared__ int sched_scratch[2 * kMaxWaves];
 
   constexpr int kBMt = MODE == GRAD ? C::kBM / 2 : C::kBM;  // routed rows per tile
+  // The dies start their sums an eighth of K apart (exact sums: any order gives
+  // the same bits).  Starting together they all read the same columns of rows K
+  // apart, on the same few memory channels where K is a power of two: 32 experts
+  // of 4096 x 4096 with 64 rows each take 131 us, staggered 111; 8 of 8192 x
+  // 8192 126, 99; K = 1536, 7168 and 14336 the same within 2 %.  Large's calls
+  // are not held by the channels (no gain), the gradient's go down the rows
+  // (1 to 2 % slower).
+  constexpr bool kStagger = MODE != GRAD && C::kDouble;
   const int lane = threadIdx.x & 63;
   const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wid / C::WN, wn = wid % C::WN;
@@ -303,6 +311,11 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   const uint8_t* pb[C::kCopiesB];
   const float* psc = g.a_scale;
   int is_item = first, is_step = 0, is_sbuf = 0;
+  // kStagger: where the tiles' sums start, and the sources' move to their next
+  // stage (at the last one back to stage 0)
+  const int phase = kStagger ? (int)((blockIdx.x & 7) * steps) >> 3 : 0;
+  int is_pos = phase;
+  int64_t move = kStagger && phase == steps - 1 ? kRowBytes - K : kRowBytes;
   auto set_tile = [&](int item) __attribute__((always_inline)) {
     const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
     int arow[C::kCopiesA];
@@ -336,7 +349,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
           r = v / g.topk;
         }
         arow[i] = (r < 0 || r >= g.rows_a) ? 0 : r;
-        pa[i] = g.a + (int64_t)arow[i] * a_pitch + chunk;
+        pa[i] = g.a + (int64_t)arow[i] * a_pitch + chunk + phase * kRowBytes;
       }
     }
 #pragma unroll
@@ -350,7 +363,8 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
         if (col >= K) col -= 128;  // K is a multiple of 128: only the upper half of 256 may be past it
         pb[i] = g.w + ((int64_t)t.e * N + n) * K + col;
       } else {
-        pb[i] = g.w + ((int64_t)t.e * N + weight_row<C, MODE>(t.nt, 8 * q + (lane >> 3), N)) * K + dma_chunk(lane, q);
+        pb[i] = g.w + ((int64_t)t.e * N + weight_row<C, MODE>(t.nt, 8 * q + (lane >> 3), N)) * K + dma_chunk(lane, q) +
+                phase * kRowBytes;
       }
     }
     // scales: lanes 0..31 the wave's A rows (row l of them was gathered by
@@ -373,7 +387,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   auto copy = [&](uint32_t base, int i) __attribute__((always_inline)) {
     if (i < C::kCopiesA) {
       dma16(pa[i], __builtin_amdgcn_readfirstlane(base + (C::kCopiesA * wid + i) * 1024));
-      pa[i] += kRowBytes;
+      pa[i] += kStagger ? move : kRowBytes;
     } else {
       const int q = C::kCopiesB * wid + i - C::kCopiesA;
       const uint8_t* src = pb[i - C::kCopiesA];
@@ -384,7 +398,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
         if (is_step * kRowBytes + n >= N) src -= (int64_t)(n & ~31) * K;
       }
       dma16(src, __builtin_amdgcn_readfirstlane(base + C::kATile + q * 1024));
-      pb[i - C::kCopiesA] += b_step;
+      pb[i - C::kCopiesA] += kStagger ? move : b_step;
     }
   };
   // After a stage's copies: a tile's scales ride with its first stage, and the
@@ -396,16 +410,22 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
       dma4(psc, __builtin_amdgcn_readfirstlane(sbuf_lds + is_sbuf * C::kScaleBytes + wid * 256));
       is_sbuf = is_sbuf == C::kScaleBufs - 1 ? 0 : is_sbuf + 1;
     }
+    if constexpr (kStagger) {
+      is_pos = is_pos == steps - 1 ? 0 : is_pos + 1;
+      move = is_pos == steps - 1 ? kRowBytes - K : kRowBytes;
+    }
     if (++is_step == steps) {
       is_step = 0;
       if (C::kBN == 128 && is_item >= last_item) {
         // the same sources without a look-up, in the tile of short calls: 7.4 us
         // for 8.5 with 128 rows and 4 experts of 256 x 256 (the branch costs
         // long calls 4 % in Large, 0.5 % in Medium)
+        if constexpr (!kStagger) {  // (kStagger: they are back by themselves)
 #pragma unroll
-        for (int i = 0; i < C::kCopiesA; ++i) pa[i] -= a_pitch;
+          for (int i = 0; i < C::kCopiesA; ++i) pa[i] -= a_pitch;
 #pragma unroll
-        for (int i = 0; i < C::kCopiesB; ++i) pb[i] -= steps * b_step;
+          for (int i = 0; i < C::kCopiesB; ++i) pb[i] -= steps * b_step;
+        }
       } else {
         is_item += G;
         set_tile(min(is_item, last_item));
@@ -610,6 +630,12 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
   const int wf0 = dd::kW + l16 * 128 + (((2 * quarter) ^ wkey) << 4);
   const int wf1 = dd::kW + l16 * 128 + (((2 * quarter + 1) ^ wkey) << 4);
   const int* ids = g.a_sorted ? nullptr : g.sorted_ids;
+  // Where K is a power of two, 64 neighbouring waves start their (exact) sums at
+  // different groups of it: together they would read the same columns of rows K
+  // apart, on the same few memory channels.  8 rows an expert: 32 experts of 4096
+  // x 4096 94 us and 85 staggered, 8 of 8192 x 8192 94 and 85; other K lose by
+  // it, 64 of 4096 x 7168 284 and 288, 16 of 4096 x 14336 142 and 146.
+  const int phase = (K & (K - 1)) == 0 ? (wid & 63) * G >> 6 : 0;
 
   for (int item = wid; item < total; item += active) {
     // m-tile major, then blocks; every field wave-uniform
@@ -650,7 +676,8 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
                             : g.a_scale + (XC > 1 && lane >= 8 ? s1 : s0);
       auto issue = [&](int k) __attribute__((always_inline)) {
         const uint32_t sl = lb + (uint32_t)((k % dd::kDepth) * dd::kSlot);
-        const int64_t ko = (int64_t)k * dd::kGroupK;
+        const int kk = k + phase;
+        const int64_t ko = (int64_t)(kk < G ? kk : kk - G) * dd::kGroupK;
         dma16_nt(sw0 + ko, sl + dd::kW);
         dma16_nt(sw1 + ko, sl + dd::kW + 1024);
 #pragma unroll
@@ -858,10 +885,10 @@ double cost(const Int8Args& g, int num_cus, double one) {
 }
 
 // The tile of the least cost.  Relative times of a tile, measured with 32
-// experts of 4096 x 4096 and 512 rows each (forward 315, 327 and 445 us for
+// experts of 4096 x 4096 and 512 rows each (forward 310, 322 and 431 us for
 // 256, 128 and 64 rows; gradient 588, 648 and 905): 1, 0.54, 0.36.  At 128 rows
-// an expert the forward call takes 155, 139 and 159 us, at 16 rows 135, 125 and
-// 124.
+// an expert the forward call takes 156, 140 and 153 us, at 16 rows 134, 104 and
+// 103.
 template <int OUT, int MODE>
 hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
   const double l = cost<Large, MODE>(g, num_cus, 1.0), m = cost<Medium, MODE>(g, num_cus, 0.54),
@@ -873,12 +900,12 @@ hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
 }
 
 // AUTO streams below 10 rows an expert: with 32 experts of 4096 x 4096, 4 rows
-// each take 90 us streamed and 123 in tiles, 10 rows 93 and 124, 16 rows 128
-// and 124 (experts past 16 rows stream their weights again); with 256 experts
-// of 2048 x 2048 6 rows take 172 and 185, 10 rows 190 and 188.  And where no
-// wave gets a second item, so that a call is as long as one item: one expert of
-// 4096 x 4096 with 64 rows 11 us streamed and 22 in tiles, with 256 rows 26 and
-// 22.
+// each take 85 us streamed and 103 in tiles, 10 rows 86 and 100, 12 rows 102 and
+// 101, 16 rows 125 and 101 (experts past 16 rows stream their weights again);
+// with 256 experts of 2048 x 2048 6 rows take 170 and 183, 10 rows 190 and 187.
+// And where no wave gets a second item, so that a call is as long as one item:
+// one expert of 4096 x 4096 with 64 rows 11 us streamed and 22 in tiles, with 256
+// rows 26 and 22.
 template <int OUT, int MODE>
 hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
   if (g.P == 0) return hipSuccess;

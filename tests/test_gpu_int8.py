@@ -170,6 +170,27 @@ def test_gemm_every_row_as_it_is():
     assert torch.equal(got, ref)
 
 
+@pytest.mark.parametrize("counts", [(1, 0, 9), (70, 3, 130), (300, 0, 500)])
+@pytest.mark.parametrize("K", [128, 256, 1024, 1152, 4096])
+def test_gemm_sums_that_start_anywhere(K, counts):
+    # workgroups and waves start their sums over K at places of their own: enough of them for
+    # every place, K of one stage and more, powers of two and not
+    g = torch.Generator(device="cuda").manual_seed(K + counts[0])
+    P, N, E = sum(counts), 4096, len(counts)
+    code = lambda *s: torch.randint(-128, 128, s, dtype=torch.int8, device="cuda", generator=g)
+    a, w = code(P, K), code(E, N, K)
+    one = [torch.ones(s, device="cuda") for s in ((P,), (E, N))]
+    ends = np.cumsum((0,) + counts)
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    # float64 products of integers below 2^53 are exact
+    want = torch.cat([a[lo:hi].double() @ w[e].double().T.contiguous()
+                      for e, (lo, hi) in enumerate(zip(ends, ends[1:]))]).int()
+    for sched in ("decode", "prefill"):
+        for _ in range(2):
+            got = mq.grouped_gemm_qint8(a, one[0], w, one[1], off, None, 1, out_dtype=torch.int32, sched=sched)
+            assert torch.equal(got, want), sched
+
+
 def test_gemm_the_largest_sums_and_scales():
     # every code -128: the int32 sums' largest, K = 131072 - 128; and scales at the ends of fp32
     K, N, P = 131072 - 128, 64, 40
