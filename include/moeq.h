@@ -566,11 +566,11 @@ moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t ro
  * towards its activations, straight through their quantization; the weights
  * are frozen:
  *   dx[s][:] = base[s][:] + sum_n dy[s][n] * w_scale[e][n] * w[e][n][:]
- * for every sorted row s < expert_offsets[E] of expert e.  d = dy * w_scale
- * enters as 16-bit fixed point of its row, to half a step of max_n |d| / 32512
- * (rows whose largest |d| is below 2^-100 count as zero); the sums over n are
- * exact integers, joined in fp32 and rounded once.  A row whose d holds an
- * infinity or NaN gives a row of NaN.  Equal inputs give equal bits.
+ * for every sorted row s < expert_offsets[E] of expert e.  d = dy * w_scale, one
+ * fp32 product, enters as 24-bit fixed point of its row, to half a step of
+ * max_n |d| / 8355711 (rows whose largest |d| is below 2^-100 count as zero); the
+ * sums over n are exact integers, joined in fp32 and rounded once.  A row whose d
+ * holds an infinity or NaN gives a row of NaN.  Equal inputs give equal bits.
  *
  *   dtype  F16 | BF16: the type of dy, base and dx
  *   dy     [P][N] in SORTED order;  w, w_scale, expert_offsets as above
@@ -579,8 +579,10 @@ moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t ro
  *   dx     [P][K] in SORTED order, whatever a_row was (moe_permute_backward
  *          sums TOKEN rows; rows past expert_offsets[E] are not written)
  *   workspace  grouped_gemm_qint8_backward_workspace_bytes(P, E, N, K) bytes,
- *          contents on entry ignored.  Calls that may overlap in time need
- *          their own.
+ *          contents on entry ignored.  With these the rows are taken in two
+ *          parts, of two launches each; P * (3 * N' + 4) bytes, N' being N up to
+ *          a multiple of 128, take them at once, and more are not used.  The
+ *          results are the same.  Calls that may overlap in time need their own.
  * Requires K % 128 == 0 and N % 32 == 0 (else MOEQ_EALIGN), N < 131072 and
  * K <= 131072, 1 <= E <= 1024, P < 2^31, 16-byte aligned pointers (4-byte for
  * the table and w_scale), outputs disjoint from the inputs and each other, and

@@ -739,8 +739,11 @@ def grouped_gemm_qint8(a, a_scale, w, w_scale, expert_offsets, sorted_pair_ids, 
     return out
 
 
-def qint8_backward_workspace_bytes(P: int, E: int, N: int, K: int) -> int:
-    return int(lib().grouped_gemm_qint8_backward_workspace_bytes(P, E, N, K))
+def qint8_backward_workspace_bytes(P: int, E: int, N: int, K: int, *, at_once: bool = False) -> int:
+    """The least workspace of grouped_gemm_qint8_backward, which then takes its
+    rows in two parts; at_once: room for all of them, half as much again."""
+    least = int(lib().grouped_gemm_qint8_backward_workspace_bytes(P, E, N, K))
+    return P * (3 * (-(-N // 128) * 128) + 4) if at_once and least else least
 
 
 def grouped_gemm_qint8_backward(dy, w, w_scale, expert_offsets, *, base=None, dx=None, workspace=None):
@@ -753,8 +756,9 @@ def grouped_gemm_qint8_backward(dy, w, w_scale, expert_offsets, *, base=None, dx
     another part of the same gradient, such as grouped_lora_backward's dx.
     Returns dx [P][K] in sorted order, rows past expert_offsets[E] not written;
     moe_permute_backward sums it over each token's slots.  The products see
-    16 bits of dy * w_scale relative to its row's largest.  workspace: uint8,
-    qint8_backward_workspace_bytes(P, E, N, K)."""
+    24 bits of dy * w_scale relative to its row's largest.  workspace: uint8,
+    qint8_backward_workspace_bytes(P, E, N, K) at least; with at_once=True's all
+    rows are taken at once, in half the launches.  The results are the same."""
     _need(dy, "dy", _HALVES, 2)
     E, N, K = _int8_weights(w, w_scale, expert_offsets)
     P, dt = dy.shape[0], dy.dtype
@@ -764,7 +768,7 @@ def grouped_gemm_qint8_backward(dy, w, w_scale, expert_offsets, *, base=None, dx
         base = _fit(base, "base", (P, K), dt, dy)
     dx = _fit(dx, "dx", (P, K), dt, dy)
     if workspace is None:
-        wsb = qint8_backward_workspace_bytes(P, E, N, K)
+        wsb = qint8_backward_workspace_bytes(P, E, N, K, at_once=True)
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dy.device)
     else:
         _need(workspace, "workspace")

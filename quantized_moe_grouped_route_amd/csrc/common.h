@@ -135,19 +135,19 @@ __device__ __forceinline__ float load_as_f32<OUT_F32>(const void* p, int64_t i) 
 //
 // The table lives in LDS: tile_start[e] = first item of expert e,
 // tile_start[E] = total.  Built by one workgroup-wide scan.
-// Rows [lo, hi) of expert e, clamped to [0, P] so that a malformed offsets
-// table can never address past the P output rows.
+// Rows [lo, hi) of expert e among the P sorted rows from `first` on, clamped to
+// [0, P] so that a malformed offsets table can never address past them.
 __device__ __forceinline__ void expert_range(const int* __restrict__ offsets, int e, int P, int& lo,
-                                             int& hi) {
-  lo = min(max(offsets[e], 0), P);
-  hi = min(max(offsets[e + 1], lo), P);
+                                             int& hi, int first = 0) {
+  lo = min(max(offsets[e], first) - first, P);
+  hi = max(min(max(offsets[e + 1], first) - first, P), lo);
 }
 
 // Builds tile_start in LDS.  Needs blockDim.x threads, E+1 ints of LDS in
 // `tile_start` and 2*kMaxWaves ints in `scratch`.  Ends with a barrier.
 constexpr int kMaxWaves = 16;
 __device__ inline void sched_build(int* tile_start, int* scratch, const int* __restrict__ offsets,
-                                   int E, int P, int bm, int n_tiles) {
+                                   int E, int P, int bm, int n_tiles, int first = 0) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int lane = tid & 63, wid = tid >> 6, nw = nt >> 6;
   // Each thread owns a contiguous run of experts.
@@ -156,7 +156,7 @@ __device__ inline void sched_build(int* tile_start, int* scratch, const int* __r
   int local = 0;
   for (int e = e0; e < e1; ++e) {
     int lo, hi;
-    expert_range(offsets, e, P, lo, hi);
+    expert_range(offsets, e, P, lo, hi, first);
     const int m = hi - lo;
     local += m > 0 ? ((m + bm - 1) / bm) * n_tiles : 0;
   }
@@ -182,7 +182,7 @@ __device__ inline void sched_build(int* tile_start, int* scratch, const int* __r
   for (int e = e0; e < e1; ++e) {
     tile_start[e] = run;
     int lo, hi;
-    expert_range(offsets, e, P, lo, hi);
+    expert_range(offsets, e, P, lo, hi, first);
     const int m = hi - lo;
     run += m > 0 ? ((m + bm - 1) / bm) * n_tiles : 0;
   }

@@ -5,18 +5,21 @@
 //           y = a_scale * w_scale * acc, optionally silu(gate) * up.
 // Gradient: dx[s][k] = sum_n dy[s][n] w_scale[e][n] w[e][n][k]  (+ base)
 // The int8 MFMA takes w as it is stored in both.  For the gradient a first
-// kernel writes d = dy * w_scale as 16-bit fixed point of its row's largest
-// value, d = step (256 hi + lo) with |256 hi + lo| <= 32512, in two int8
-// planes; both planes' products with w are exact int32 sums, joined in fp32.
-// Two int8 MFMAs take as long as one bf16 MFMA, need no conversion of w in
-// the loop, and keep 16 bits of d where a bf16 product would keep 8 after
-// the w_scale product.
+// kernel writes d = dy * w_scale, an fp32 value, as 24-bit fixed point of its
+// row's largest value, d = step (65536 hi + 256 mid + lo) with a code of at most
+// 8355711, in three int8 planes; the planes' products with w are exact int32
+// sums, joined in fp32.  So the sums lose no more than fp32 products and sums
+// would: d is off by 2^-24 of its row's largest, its own fp32 rounding there.
+// Two planes (16 bits) would be half again as fast, but where one column is 100
+// times the others they lose more than f16's own rounding.  Three int8 MFMAs
+// take as long as one and a half bf16 MFMAs and need no conversion of w in the
+// loop; d's 24 bits would take three bf16 operands.
 //
-// Measured, 8 experts, 16384 rows, f16: gate+up 4096 -> 28672 with SiLU 1.58 ms
-// (2.44 POP/s; the MFMAs alone take 1.15 ms at the clock that they are left), its
-// gradient 3.67 ms with the planes' 0.41.  256 experts, 32768 rows under Zipf,
-// gradient 7168 -> 2048, bf16: 1.52 ms, 8.6 GB read past the L2s at 6.4 TB/s.  8
-// tokens to 8 of 256 experts, 7168 -> 4096: 243 us, the weights at 7.0 TB/s.
+// Measured, 8 experts, 16384 rows, f16: gate+up 4096 -> 28672 with SiLU 1.58-1.71
+// ms (2.26-2.44 POP/s; the MFMAs alone take 1.15 ms at the clock that they are
+// left), its gradient 5.51 ms with the planes' 0.49 (two planes: 3.68).  256
+// experts, 32768 rows under Zipf, gradient 7168 -> 2048, bf16: 1.91 ms with the
+// planes' 0.25 (two planes: 1.54).  8 tokens to 8 of 256 experts, 7168 -> 4096: 243 us, the weights at 7.0 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -34,9 +37,11 @@ enum Mode { NONE = 0, SILU = 1, GRAD = 2 };
 constexpr int kRowBytes = 128;  // K (GRAD: N) values of a row per stage: one cache line
 constexpr int kGroupM = 4;      // m-tiles per n-tile sweep
 
+constexpr int kPlanes = 3;      // int8 digits of a gradient's value: hi, mid, lo
+
 // WM x WN waves; a wave owns XO 16-row operands of the A tile and WO 16-wide
-// operands of the weight tile.  GRAD: A operand 2i holds the hi plane of the
-// wave's i-th 16 rows, 2i + 1 the lo plane of the same rows.
+// operands of the weight tile.  GRAD: A operands 3i, 3i + 1, 3i + 2 of a wave
+// hold the hi, mid and lo plane of its i-th 16 rows.
 template <int WM_, int WN_, int XO_, int WO_, int STAGES_>
 struct Cfg {
   static constexpr int WM = WM_, WN = WN_, XO = XO_, WO = WO_, kStages = STAGES_;
@@ -44,9 +49,11 @@ struct Cfg {
   static constexpr int kThreads = 64 * kWaves;
   static constexpr int kBM = 16 * XO * WM;                   // A tile rows
   static constexpr int kBN = 16 * WO * WN;                   // weight rows of a tile (GRAD: weight columns)
-  static constexpr int kATile = kBM * kRowBytes;
+  // 1 KB copies (8 rows) per wave, the same for every wave: a tile of 96 rows
+  // and 8 waves has 32 rows more that nobody reads
+  static constexpr int kCopiesA = (kBM / 8 + kWaves - 1) / kWaves;
+  static constexpr int kATile = kCopiesA * 8 * kWaves * kRowBytes;
   static constexpr int kStageBytes = kATile + kBN * kRowBytes;
-  static constexpr int kCopiesA = kBM / 8 / kWaves;          // 1 KB copies (8 rows) per wave
   static constexpr int kCopiesB = kBN / 8 / kWaves;
   static constexpr int kCopies = kCopiesA + kCopiesB;
   static constexpr int kRW = 8 * kCopiesA;                   // A rows per wave
@@ -59,7 +66,7 @@ struct Cfg {
   // Whether both substeps' operands fit in registers beside the accumulators.
   static constexpr bool kDouble = XO * WO <= 16;
   static_assert((kBN == 256 || kBN == 128) && kCW <= 32 && kRW <= 32, "scale and weight layouts");
-  static_assert(kCopiesA * 8 * kWaves == kBM && kCopiesB * 8 * kWaves == kBN, "copies cover the tile");
+  static_assert(kBM % 8 == 0 && kCopiesB * 8 * kWaves == kBN, "copies cover the tile");
 };
 
 typedef __attribute__((address_space(4))) const int cint_t;
@@ -80,9 +87,10 @@ struct TileAt {
 // Work item -> tile, wave-uniform: expert-major, and inside an expert
 // kGroupM m-tiles are visited for each n-tile before the next n-tile (1, 2, 4, 8
 // of them: 1.73, 1.65, 1.62, 1.66 ms for the Mixtral-sized product above, when
-// it took 1.62; 1.59, 1.56, 1.56, 1.54 for the gradient under Zipf).
+// it took 1.62; 1.59, 1.56, 1.56, 1.54 for the gradient under Zipf, when it had
+// two planes).
 __device__ __forceinline__ TileAt tile_at(const int* tile_start, const int* __restrict__ offsets, int E, int P,
-                                          int bm, int n_tiles, int item) {
+                                          int first, int bm, int n_tiles, int item) {
   int bl = 0, bh = E - 1;
   while (bl < bh) {
     const int mid = (bl + bh + 1) >> 1;
@@ -90,8 +98,8 @@ __device__ __forceinline__ TileAt tile_at(const int* tile_start, const int* __re
   }
   const int e = __builtin_amdgcn_readfirstlane(bl);
   const int local = item - __builtin_amdgcn_readfirstlane(tile_start[e]);
-  const int lo = min(max(ld_uniform(offsets, e), 0), P);
-  const int hi = min(max(ld_uniform(offsets, e + 1), lo), P);
+  const int lo = min(max(ld_uniform(offsets, e), first) - first, P);
+  const int hi = max(min(max(ld_uniform(offsets, e + 1), first) - first, P), lo);
   const int m = hi - lo;
   const int mtiles = (m + bm - 1) / bm;
   const int group = local / (kGroupM * n_tiles);
@@ -189,7 +197,7 @@ __device__ __forceinline__ void put4(void* out, int64_t idx, const float (&o)[4]
 }
 
 struct Int8Args {
-  const uint8_t* a;        // activations, or the hi | lo planes of d
+  const uint8_t* a;        // activations, or the planes of d
   const float* a_scale;    // per activation row, or step per sorted row
   const uint8_t* w;
   const float* w_scale;    // not read by GRAD
@@ -199,6 +207,7 @@ struct Int8Args {
   void* out;
   int64_t rows_a;
   int a_sorted, topk, E, P, N, K;
+  int first;               // sorted row that a, base and out begin at (GRAD: of a round of rows)
 };
 
 // Epilogue of one tile: value i of accumulator [wo][xo] in lane l is weight
@@ -207,7 +216,7 @@ struct Int8Args {
 template <class C, int OUT, int MODE, int NX>
 __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int wm, int wn, int lane, const Int8Args& g,
                                          const v4i (&acc)[C::WO][NX]) {
-  constexpr int kP = MODE == GRAD ? 2 : 1;  // A operands per 16 routed rows
+  constexpr int kP = MODE == GRAD ? kPlanes : 1;  // A operands per 16 routed rows
   const int l16 = lane & 15, m0 = 4 * (lane >> 4);
   // every scale first: read one by one they cost a trip to LDS per operand
   v4f sw[C::WO];
@@ -258,8 +267,10 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = __builtin_fmaf(__builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + 1][i]), sa[xo], b[i]);
+          for (int i = 0; i < 4; ++i) {
+            const float hm = __builtin_fmaf((float)acc[wo][xo][i], 256.0f, (float)acc[wo][xo + 1][i]);
+            o[i] = __builtin_fmaf(__builtin_fmaf(hm, 256.0f, (float)acc[wo][xo + 2][i]), sa[xo], b[i]);
+          }
           put4<OUT>(g.out, idx, o);
         } else if constexpr (OUT == OUT_I32) {
           *reinterpret_cast<v4i*>(static_cast<int*>(g.out) + orow * g.N + col0) = acc[wo][xo];
@@ -281,7 +292,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   __shared__ int tile_start[kMaxExperts + 1];
   __shared__ int sched_scratch[2 * kMaxWaves];
 
-  constexpr int kBMt = MODE == GRAD ? C::kBM / 2 : C::kBM;  // routed rows per tile
+  constexpr int kBMt = MODE == GRAD ? C::kBM / kPlanes : C::kBM;  // routed rows per tile
   // The dies start their sums an eighth of K apart (exact sums: any order gives
   // the same bits).  Starting together they all read the same columns of rows K
   // apart, on the same few memory channels where K is a power of two: 32 experts
@@ -299,7 +310,8 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   const int a_pitch = MODE == GRAD ? plane_pitch(N) : K;
   const int steps = a_pitch / kRowBytes;
   const bool ragged = N % kRowBytes != 0;  // GRAD: the last stage ends inside
-  sched_build(tile_start, sched_scratch, g.offsets, E, P, kBMt, n_tiles);
+  const int row_base = MODE == GRAD ? g.first : 0;
+  sched_build(tile_start, sched_scratch, g.offsets, E, P, kBMt, n_tiles, row_base);
   const int total = __builtin_amdgcn_readfirstlane(tile_start[E]);
   const int G = gridDim.x;
   const int first = xcd_logical_id(blockIdx.x, G);
@@ -317,7 +329,7 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
   int is_pos = phase;
   int64_t move = kStagger && phase == steps - 1 ? kRowBytes - K : kRowBytes;
   auto set_tile = [&](int item) __attribute__((always_inline)) {
-    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
+    const TileAt t = tile_at(tile_start, g.offsets, E, P, row_base, kBMt, n_tiles, item);
     int arow[C::kCopiesA];
 #pragma unroll
     for (int i = 0; i < C::kCopiesA; ++i) {
@@ -325,10 +337,10 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
       const int chunk = dma_chunk(lane, r0 / 8);
       if constexpr (MODE == GRAD) {
         // a copy's 8 rows lie in one 16-row operand, hence in one plane
-        const int xo = r0 / 16 % C::XO;
-        const int tok = 8 * C::XO * (r0 / (16 * C::XO)) + 16 * (xo / 2) + r0 % 16 + (lane >> 3);
-        arow[i] = t.row0 + min(tok, t.rows - 1);
-        pa[i] = g.a + ((int64_t)(xo & 1) * P + arow[i]) * a_pitch + chunk;
+        static_assert(C::XO == 2 * kPlanes, "a wave owns two groups of 16 rows");
+        const int op = r0 / 16;
+        arow[i] = t.row0 + min(16 * (op / kPlanes) + r0 % 16 + (lane >> 3), t.rows - 1);
+        pa[i] = g.a + ((int64_t)(op % kPlanes) * P + arow[i]) * a_pitch + chunk;
       } else {
         int r;
         if (g.a_sorted || g.sorted_ids == nullptr) {
@@ -539,10 +551,14 @@ __global__ __launch_bounds__(C::kThreads, 1) void int8_tiles(Int8Args g) {
     ep_sbuf = ep_sbuf == C::kScaleBufs - 1 ? 0 : ep_sbuf + 1;
   };
   for (int item = first; item < total; item += G) {
-    const TileAt t = tile_at(tile_start, g.offsets, E, P, kBMt, n_tiles, item);
+    const TileAt t = tile_at(tile_start, g.offsets, E, P, row_base, kBMt, n_tiles, item);
     const int left = t.rows - kBMt / C::WM * wm;  // routed rows of this wave
     constexpr int kRows = kBMt / C::WM;
-    if (left > kRows / 2) run_tile(t, std::integral_constant<int, C::XO>());
+    if constexpr (MODE == GRAD) {
+      if (left > kRows / 2) run_tile(t, std::integral_constant<int, C::XO>());
+      else if (left > 0) run_tile(t, std::integral_constant<int, kPlanes>());
+      else run_tile(t, std::integral_constant<int, 0>());
+    } else if (left > kRows / 2) run_tile(t, std::integral_constant<int, C::XO>());
     else if (C::XO > 4 && left > kRows / 4) run_tile(t, std::integral_constant<int, C::XO / 2>());
     else if (C::XO > 4 && left > 0) run_tile(t, std::integral_constant<int, C::XO / 4>());
     else if (C::XO <= 4 && left > 0) run_tile(t, std::integral_constant<int, C::XO / 2>());
@@ -741,16 +757,18 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
 }
 
 // ------------------------------------------------------- gradient's planes
-// d[s][n] = dy[s][n] * w_scale[e][n] as step * (256 hi + lo): step = max |d| /
-// 32512, the code rne(d * (32512 / max)).  WAVES waves work on a row, whose d
-// stays in their registers (LOADS times 8 values a lane; 0: the row is read
-// twice).  A row whose largest value is below 2^-100 counts as zero; one that
-// holds an infinity or NaN gets step NaN, so all of its dx is NaN.
+// d[s][n] = dy[s][n] * w_scale[e][n] as step * (65536 hi + 256 mid + lo): step =
+// max |d| / 8355711, the code rne(d * (8355711 / max)), its digits from -128 to
+// 127.  WAVES waves work on a row, whose d stays in their registers (LOADS times
+// 8 values a lane; 0: the row is read twice).  A row whose largest value is below
+// 2^-100 counts as zero; one that holds an infinity or NaN gets step NaN, so all
+// of its dx is NaN.  The rows are those from `first` on, at most P of them; dy,
+// the planes and step begin at the first.
 //
-// HBM-bound: dy is read once, past the caches, and the two planes are written,
-// 16384 rows of 28672 (1.88 GB) in 394-422 us, 4.6 TB/s, 32768 rows of 7168 (0.94
-// GB) in 213-225.  Waves a row: 8 for rows of 28672 (16: 437 us, 4: 480), 2 for
-// rows of 7168 (1: 311, 4: 251).
+// HBM-bound: dy is read once, past the caches, and the three planes are written,
+// 16384 rows of 28672 (2.35 GB) in 489-494 us, 4.8 TB/s, 32768 rows of 7168 (1.17
+// GB) in 248-254.  Waves a row, timed with two planes (394-422 and 213-225 us): 8
+// for rows of 28672 (16: 437, 4: 480), 2 for rows of 7168 (1: 311, 4: 251).
 
 // Expert of sorted row s, by the whole wave: the number of experts that end
 // (ends[e], in LDS) at or before it.
@@ -763,10 +781,13 @@ __device__ __forceinline__ int expert_of(const int* ends, int E, int s, int lane
   return min(n, E - 1);
 }
 
+// The largest code: digits 127, 127, 127.
+constexpr float kTopCode = 127 * 65536 + 127 * 256 + 127;
+
 template <int YK, int WAVES, int LOADS>
 __global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
-    const void* __restrict__ dy, const float* __restrict__ w_scale, const int* __restrict__ offsets, int E, int P, int N,
-    uint8_t* __restrict__ planes, float* __restrict__ step) {
+    const void* __restrict__ dy, const float* __restrict__ w_scale, const int* __restrict__ offsets, int E, int first, int P,
+    int N, uint8_t* __restrict__ planes, float* __restrict__ step) {
   constexpr int kRows = WAVES == 1 ? 4 : 1;  // rows of a workgroup at a time
   constexpr int kT = 64 * WAVES;
   __shared__ u32 wmax[WAVES];
@@ -775,7 +796,7 @@ __global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
   for (int e = threadIdx.x; e < E; e += blockDim.x) ends[e] = offsets[e + 1];
   __syncthreads();
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6, sub = wid / WAVES, tid = threadIdx.x % kT;
-  const int n = min(max(offsets[E], 0), P), Np = plane_pitch(N);
+  const int n = min(max(offsets[E], first) - first, P), Np = plane_pitch(N);
   for (int64_t s = (int64_t)blockIdx.x * kRows + sub; s < n; s += (int64_t)gridDim.x * kRows) {
     const int64_t base = s * N;
     float d[LOADS ? LOADS : 1][8];
@@ -784,7 +805,7 @@ __global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
       for (int i = 0; i < LOADS; ++i)
         if ((i * kT + tid) * 8 < N) load8<YK, true>(dy, base + (i * kT + tid) * 8, d[i]);
     }
-    const float* ws = w_scale + (int64_t)expert_of(ends, E, (int)s, lane) * N;
+    const float* ws = w_scale + (int64_t)expert_of(ends, E, first + (int)s, lane) * N;
     auto scale8 = [&](int k, float (&v)[8]) __attribute__((always_inline)) {
       float c[8];
       load8<OUT_F32, false>(ws, k, c);
@@ -817,19 +838,20 @@ __global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
       for (int w = 0; w < WAVES; ++w) m = max(m, wmax[w]);
       __syncthreads();  // wmax is reused by the next row
     }
-    const Scale c = scale_of(m, 32512.0f, 0x1p-100f);
-    uint8_t* hi = planes + s * Np;
-    uint8_t* lo = hi + (int64_t)P * Np;
+    const Scale c = scale_of(m, kTopCode, 0x1p-100f);
+    uint8_t* row = planes + s * Np;
+    const int64_t plane = (int64_t)P * Np;
     auto put = [&](int k, const float (&v)[8]) __attribute__((always_inline)) {
-      u32 h[2] = {0, 0}, l[2] = {0, 0};
+      u32 w[kPlanes][2] = {};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int q = code_of(v[j], c.recip, 32512.0f);
-        h[j >> 2] |= ((u32)((q + 128) >> 8) & 255u) << (8 * (j & 3));
-        l[j >> 2] |= ((u32)q & 255u) << (8 * (j & 3));
+        const int q = code_of(v[j], c.recip, kTopCode);
+        w[0][j >> 2] |= ((u32)((q + 0x8080) >> 16) & 255u) << (8 * (j & 3));
+        w[1][j >> 2] |= ((u32)((q + 0x80) >> 8) & 255u) << (8 * (j & 3));
+        w[2][j >> 2] |= ((u32)q & 255u) << (8 * (j & 3));
       }
-      *reinterpret_cast<uint2*>(hi + k) = make_uint2(h[0], h[1]);
-      *reinterpret_cast<uint2*>(lo + k) = make_uint2(l[0], l[1]);
+#pragma unroll
+      for (int p = 0; p < kPlanes; ++p) *reinterpret_cast<uint2*>(row + p * plane + k) = make_uint2(w[p][0], w[p][1]);
     };
     if constexpr (LOADS > 0) {
 #pragma unroll
@@ -845,18 +867,25 @@ __global__ __launch_bounds__(64 * (WAVES == 1 ? 4 : WAVES)) void grad_planes(
       }
     }
     if (tid < (Np - N) / 8) {  // the planes' zeros up to a whole stage
-      *reinterpret_cast<uint2*>(hi + N + 8 * tid) = make_uint2(0, 0);
-      *reinterpret_cast<uint2*>(lo + N + 8 * tid) = make_uint2(0, 0);
+#pragma unroll
+      for (int p = 0; p < kPlanes; ++p) *reinterpret_cast<uint2*>(row + p * plane + N + 8 * tid) = make_uint2(0, 0);
     }
     if (tid == 0) step[s] = c.scale;
   }
 }
 
 // ------------------------------------------------------------------ launch
-typedef Cfg<2, 4, 8, 4, 2> Large;   // 256 A rows x 256 columns
-typedef Cfg<2, 4, 4, 4, 3> Medium;  // 128 x 256
-typedef Cfg<1, 8, 4, 2, 3> Small;   // 64 x 256
-typedef Cfg<1, 4, 4, 2, 5> Narrow;  // 64 x 128
+struct Forward {
+  typedef Cfg<2, 4, 8, 4, 2> Large;   // 256 rows x 256 columns
+  typedef Cfg<2, 4, 4, 4, 3> Medium;  // 128 x 256
+  typedef Cfg<1, 8, 4, 2, 3> Small;   // 64 x 256
+  typedef Cfg<1, 4, 4, 2, 5> Narrow;  // 64 x 128
+};
+struct Gradient {                     // three A rows for a routed row
+  typedef Cfg<2, 4, 6, 4, 2> Large;   // 64 routed rows x 256 columns
+  typedef Cfg<1, 8, 6, 2, 3> Small;   // 32 x 256
+  typedef Cfg<1, 4, 6, 2, 5> Narrow;  // 32 x 128
+};
 
 int out_cols(const Int8Args& g, int mode) { return mode == SILU ? g.N / 2 : mode == GRAD ? g.K : g.N; }
 
@@ -868,7 +897,7 @@ int64_t n_tiles(const Int8Args& g) {
 
 template <class C, int OUT, int MODE>
 hipError_t go_tiles(const Int8Args& g, int num_cus, hipStream_t stream) {
-  const int bm = MODE == GRAD ? C::kBM / 2 : C::kBM;
+  const int bm = MODE == GRAD ? C::kBM / kPlanes : C::kBM;
   // upper bound on tiles: every expert adds at most one partial m-tile
   const int64_t tiles = (((int64_t)g.P + bm - 1) / bm + std::min(g.E, g.P)) * n_tiles<C, MODE>(g);
   const int grid = (int)std::min<int64_t>(tiles, num_cus);
@@ -880,23 +909,38 @@ hipError_t go_tiles(const Int8Args& g, int num_cus, hipStream_t stream) {
 // partial m-tile for every expert, times the time of one relative to Large's.
 template <class C, int MODE>
 double cost(const Int8Args& g, int num_cus, double one) {
-  const double mt = (double)g.P * (MODE == GRAD ? 2 : 1) / C::kBM + 0.5 * std::min(g.E, g.P);
+  const double mt = (double)g.P * (MODE == GRAD ? kPlanes : 1) / C::kBM + 0.5 * std::min(g.E, g.P);
   return one * std::max(1.0, mt * (double)n_tiles<C, MODE>(g) / num_cus);
 }
 
 // The tile of the least cost.  Relative times of a tile, measured with 32
-// experts of 4096 x 4096 and 512 rows each (forward 310, 322 and 431 us for
-// 256, 128 and 64 rows; gradient 588, 648 and 905): 1, 0.54, 0.36.  At 128 rows
-// an expert the forward call takes 156, 140 and 153 us, at 16 rows 134, 104 and
-// 103.
+// experts of 4096 x 4096 and 512 rows each (310, 322 and 431 us for 256, 128 and
+// 64 rows): 1, 0.54, 0.36.  At 128 rows an expert the call takes 156, 140 and 153
+// us, at 16 rows 134, 104 and 103.
 template <int OUT, int MODE>
 hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
-  const double l = cost<Large, MODE>(g, num_cus, 1.0), m = cost<Medium, MODE>(g, num_cus, 0.54),
-               s = cost<Small, MODE>(g, num_cus, 0.36), n = cost<Narrow, MODE>(g, num_cus, 0.22);
-  if (n <= s && n <= m && n <= l) return go_tiles<Narrow, OUT, MODE>(g, num_cus, stream);
-  if (s <= m && s <= l) return go_tiles<Small, OUT, MODE>(g, num_cus, stream);
-  if (m <= l) return go_tiles<Medium, OUT, MODE>(g, num_cus, stream);
-  return go_tiles<Large, OUT, MODE>(g, num_cus, stream);
+  typedef Forward F;
+  const double l = cost<F::Large, MODE>(g, num_cus, 1.0), m = cost<F::Medium, MODE>(g, num_cus, 0.54),
+               s = cost<F::Small, MODE>(g, num_cus, 0.36), n = cost<F::Narrow, MODE>(g, num_cus, 0.22);
+  if (n <= s && n <= m && n <= l) return go_tiles<F::Narrow, OUT, MODE>(g, num_cus, stream);
+  if (s <= m && s <= l) return go_tiles<F::Small, OUT, MODE>(g, num_cus, stream);
+  if (m <= l) return go_tiles<F::Medium, OUT, MODE>(g, num_cus, stream);
+  return go_tiles<F::Large, OUT, MODE>(g, num_cus, stream);
+}
+
+// The gradient's tile, as above.  32 experts of 4096 x 4096, bf16, each tile
+// forced, 64 x 256, 32 x 256 and 32 x 128, us with the planes: 512 rows each 848,
+// 1025 and 1243, 128 rows 267, 304 and 372, 64 rows 202, 191 and 215, 16 rows 124,
+// 115 and 131; so 1, 0.62 and 0.37.  4 of 256 x 256 with 256 rows: 14.3, 13.6 and
+// 12.1.
+template <int OUT>
+hipError_t go_gradient(const Int8Args& g, int num_cus, hipStream_t stream) {
+  typedef Gradient B;
+  const double l = cost<B::Large, GRAD>(g, num_cus, 1.0), s = cost<B::Small, GRAD>(g, num_cus, 0.62),
+               n = cost<B::Narrow, GRAD>(g, num_cus, 0.37);
+  if (n <= s && n <= l) return go_tiles<B::Narrow, OUT, GRAD>(g, num_cus, stream);
+  if (s <= l) return go_tiles<B::Small, OUT, GRAD>(g, num_cus, stream);
+  return go_tiles<B::Large, OUT, GRAD>(g, num_cus, stream);
 }
 
 // AUTO streams below 10 rows an expert: with 32 experts of 4096 x 4096, 4 rows
@@ -919,7 +963,7 @@ hipError_t go(const Int8Args& g, int sched, int num_cus, hipStream_t stream) {
 
 Int8Args int8_args(const GroupedArgs& g, const void* a, const float* a_scale, const int8_t* w, const float* w_scale) {
   return Int8Args{static_cast<const uint8_t*>(a), a_scale, reinterpret_cast<const uint8_t*>(w), w_scale, g.offsets,
-                  g.sorted_ids, nullptr, g.out, g.rows_a, g.a_sorted, g.topk, g.E, (int)g.P, g.N, g.K};
+                  g.sorted_ids, nullptr, g.out, g.rows_a, g.a_sorted, g.topk, g.E, (int)g.P, g.N, g.K, 0};
 }
 
 }  // namespace
@@ -948,40 +992,57 @@ bool int8_fits(int64_t P, int E, int64_t N, int64_t K) {
   return items < (1 << 30) && (items / 64 + 1) * (K / kRowBytes) < (1 << 30);
 }
 bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K) {
-  const int64_t tiles = (P / (Narrow::kBM / 2) + E) * (K / Narrow::kBN);
+  typedef Gradient::Narrow C;
+  const int64_t tiles = (P / (C::kBM / kPlanes) + E) * (K / C::kBN);
   return tiles < (1 << 30) && (tiles / 64 + 1) * (plane_pitch((int)N) / kRowBytes) < (1 << 30);
 }
 
-size_t int8_bwd_workspace_bytes(int64_t P, int N) { return (size_t)P * (2 * plane_pitch(N) + 4); }
+// Bytes of the workspace that one row takes: its planes and its step.
+static int64_t row_bytes(int N) { return kPlanes * plane_pitch(N) + 4; }
 
+size_t int8_bwd_workspace_bytes(int64_t P, int N) {
+  return P == 0 ? 0 : (size_t)std::max(P * (2 * plane_pitch(N) + 4), row_bytes(N));
+}
+size_t int8_bwd_workspace_most(int64_t P, int N) { return (size_t)(P * row_bytes(N)); }
+
+// One plane and one tile launch for as many rows as the workspace holds: all of
+// them, or, with the least workspace, two thirds of them and then the rest.
 hipError_t launch_gemm_int8_bwd(const GroupedArgs& g, const void* dy, const int8_t* w, const float* w_scale,
-                                const void* base, void* ws, hipStream_t stream) {
-  if (g.P == 0) return hipSuccess;
-  const int P = (int)g.P;
-  uint8_t* planes = static_cast<uint8_t*>(ws);
-  float* step = reinterpret_cast<float*>(planes + 2 * g.P * plane_pitch(g.N));
+                                const void* base, void* ws, size_t ws_bytes, hipStream_t stream) {
   const bool bf = g.out_kind == OUT_BF16;
+  const int64_t room = std::min<int64_t>(ws_bytes / row_bytes(g.N), g.P);
+  uint8_t* planes = static_cast<uint8_t*>(ws);
+  float* step = reinterpret_cast<float*>(planes + kPlanes * room * plane_pitch(g.N));
+  for (int64_t first = 0; first < g.P; first += room) {
+    const int P = (int)std::min(room, g.P - first);
+    const uint16_t* y = static_cast<const uint16_t*>(dy) + first * g.N;
 #define MOEQ_PLANES(WAVES, LOADS)                                                                                  \
   do {                                                                                                             \
     const int rows = WAVES == 1 ? 4 : 1;                                                                           \
     const dim3 grid(std::min((P + rows - 1) / rows, g.num_cus * 8)), block(64 * WAVES * rows);                     \
     if (bf)                                                                                                        \
-      hipLaunchKernelGGL((grad_planes<OUT_BF16, WAVES, LOADS>), grid, block, 0, stream, dy, w_scale, g.offsets,    \
-                         g.E, P, g.N, planes, step);                                                               \
+      hipLaunchKernelGGL((grad_planes<OUT_BF16, WAVES, LOADS>), grid, block, 0, stream, y, w_scale, g.offsets,     \
+                         g.E, (int)first, P, g.N, planes, step);                                                   \
     else                                                                                                           \
-      hipLaunchKernelGGL((grad_planes<OUT_F16, WAVES, LOADS>), grid, block, 0, stream, dy, w_scale, g.offsets,     \
-                         g.E, P, g.N, planes, step);                                                               \
+      hipLaunchKernelGGL((grad_planes<OUT_F16, WAVES, LOADS>), grid, block, 0, stream, y, w_scale, g.offsets,      \
+                         g.E, (int)first, P, g.N, planes, step);                                                   \
   } while (0)
-  if (g.N <= 64 * 8 * 4) MOEQ_PLANES(1, 4);
-  else if (g.N <= 128 * 8 * 8) MOEQ_PLANES(2, 8);
-  else if (g.N <= 512 * 8 * 8) MOEQ_PLANES(8, 8);
-  else MOEQ_PLANES(8, 0);
+    if (g.N <= 64 * 8 * 4) MOEQ_PLANES(1, 4);
+    else if (g.N <= 128 * 8 * 8) MOEQ_PLANES(2, 8);
+    else if (g.N <= 512 * 8 * 8) MOEQ_PLANES(8, 8);
+    else MOEQ_PLANES(8, 0);
 #undef MOEQ_PLANES
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  Int8Args k = int8_args(g, planes, step, w, w_scale);
-  k.base = base;
-  return bf ? go_prefill<OUT_BF16, GRAD>(k, g.num_cus, stream) : go_prefill<OUT_F16, GRAD>(k, g.num_cus, stream);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    Int8Args k = int8_args(g, planes, step, w, w_scale);
+    k.P = P;
+    k.first = (int)first;
+    k.base = base ? static_cast<const uint16_t*>(base) + first * g.K : nullptr;
+    k.out = static_cast<uint16_t*>(g.out) + first * g.K;
+    e = bf ? go_gradient<OUT_BF16>(k, g.num_cus, stream) : go_gradient<OUT_F16>(k, g.num_cus, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moeq

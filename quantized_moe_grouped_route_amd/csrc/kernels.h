@@ -83,9 +83,11 @@ bool int8_fits(int64_t P, int E, int64_t N, int64_t K);
 bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K);
 hipError_t launch_gemm_int8(const GroupedArgs& g, const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, hipStream_t stream);
+// The least workspace, and the one beyond which more is not used.
 size_t int8_bwd_workspace_bytes(int64_t P, int N);
+size_t int8_bwd_workspace_most(int64_t P, int N);
 hipError_t launch_gemm_int8_bwd(const GroupedArgs& g, const void* dy, const int8_t* w, const float* w_scale,
-                                const void* base, void* ws, hipStream_t stream);
+                                const void* base, void* ws, size_t ws_bytes, hipStream_t stream);
 
 // Per-row symmetric INT8 quantization (x_kind: OutKind of the input).
 hipError_t launch_quant_int8(const void* x, int x_kind, int64_t rows, int K, int8_t* q, float* scale, int num_cus,

@@ -6,6 +6,7 @@
 // reported as status codes because the boundary is C.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -659,14 +660,15 @@ moeq_status grouped_gemm_qint8_backward(const void* dy, moeq_dtype dtype, const 
   const size_t need = moeq::int8_bwd_workspace_bytes(P, (int)N);
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(MOEQ_EINVAL, "%s: workspace of %zu bytes needed, %zu given", fn, need, workspace_bytes);
-  const Span outs[] = {{dx, P * K * 2}, {workspace, (int64_t)need}},
+  const size_t used = std::min(workspace_bytes, moeq::int8_bwd_workspace_most(P, (int)N));
+  const Span outs[] = {{dx, P * K * 2}, {workspace, (int64_t)used}},
              ins[] = {{base == dx ? nullptr : base, P * K * 2}, {dy, P * N * 2}, {w, E * N * K}, {w_scale, E * N * 4},
                       {expert_offsets, (int64_t(E) + 1) * 4}};
   if (outputs_overlap(outs, ins))
     return fail(MOEQ_EINVAL, "%s: dx or the workspace overlaps another argument (base may be dx itself)", fn);
   moeq::GroupedArgs g = make_args(expert_offsets, nullptr, P, MOEQ_AROW_SORTED, P, 1, E, N, K, false, dtype, dx,
                                   MOEQ_SCHED_AUTO);
-  return hip_status(moeq::launch_gemm_int8_bwd(g, dy, w, w_scale, base, workspace, (hipStream_t)stream), fn);
+  return hip_status(moeq::launch_gemm_int8_bwd(g, dy, w, w_scale, base, workspace, used, (hipStream_t)stream), fn);
 }
 
 moeq_status moe_silu_mul(const void* gu, moeq_dtype dtype, const int32_t* expert_offsets, int32_t E, int64_t P,
