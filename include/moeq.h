@@ -603,7 +603,7 @@ moeq_status grouped_gemm_qint8_backward(const void* dy, moeq_dtype dtype, const 
  * moe_silu_mul - the gated activation of rows [gate | up] by itself, for
  * projections whose columns change before it (grouped_lora beside gate+up):
  *   h[s][i] = silu(gu[s][i]) * gu[s][I + i]
- * in fp32, rounded once, with an optional 8-bit checkpoint of gu, which
+ * in fp32, rounded once (F32 rows: to 8 * 2^-24 of h at every gate), with an optional 8-bit checkpoint of gu, which
  * moe_silu_mul_backward reads in its place.
  *
  *   gu     [P][2I] dtype (F16 | BF16 | F32);  h [P][I] dtype

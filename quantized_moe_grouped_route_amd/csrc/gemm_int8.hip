@@ -246,7 +246,7 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
         float o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          o[i] = silu(sa[xo] * sw[wo][i] * (float)acc[wo][xo][i]) * (sa[xo] * sw[wo + H][i] * (float)acc[wo + H][xo][i]);
+          o[i] = silu<OUT>(sa[xo] * sw[wo][i] * (float)acc[wo][xo][i]) * (sa[xo] * sw[wo + H][i] * (float)acc[wo + H][xo][i]);
         put4<OUT>(g.out, orow * I + col0, o);
       }
     } else {
@@ -736,7 +736,7 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
         if (l16 < rows && quarter < 2) {
           float o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = silu(v[i]) * u[i];
+          for (int i = 0; i < 4; ++i) o[i] = silu<OUT>(v[i]) * u[i];
           put4<OUT>(g.out, orow * I + nb * 8 + 4 * quarter, o);
         }
       } else if (l16 < rows) {

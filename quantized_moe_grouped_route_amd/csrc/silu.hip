@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kThreadsS) void silu_mul_rows(const void* __restric
       load8<XK, NT>(gu, at + I, u);
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = rounded(silu(g[j]) * u[j]);
+      for (int j = 0; j < 8; ++j) o[j] = rounded(silu<XK>(g[j]) * u[j]);
       store8<XK, NT>(h, p.row * I + p.col, o);
     }
     if constexpr (SAVE) {
@@ -126,8 +126,9 @@ __global__ __launch_bounds__(kThreadsS) void silu_mul_grad(const void* __restric
     float a[8], b[8], o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float s = sigmoid(g[j]), t = g[j] * s;
-      a[j] = rounded(d[j] * u[j] * __builtin_fmaf(t, 1.0f - s, s));
+      const Sigmoid q = sigmoid<XK>(g[j]);
+      const float t = g[j] * q.s;
+      a[j] = rounded(d[j] * u[j] * __builtin_fmaf(t, q.c, q.s));
       b[j] = rounded(d[j] * t);
       o[j] = rounded(t * u[j]);
     }
