@@ -544,7 +544,8 @@ moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, i
  *                F16 | BF16 | F32: a_scale[r] * w_scale[e][n] * acc
  *                I32: the raw accumulator acc (act NONE only), bit-exact
  * Computed exactly in integers, every code from -128 to 127, then scaled in
- * fp32 and rounded to nearest even.
+ * fp32, by w_scale first, and rounded to nearest even.  w_scale below 2^96 in
+ * magnitude cannot overflow there, whatever a_scale is.
  * Requires as grouped_gemm_qint4: K % 128 == 0 and N % 32 == 0 (else
  * MOEQ_EALIGN), K < 131072 so that the int32 accumulator cannot wrap (else
  * MOEQ_EINVAL), a, w and out 16-byte and the scales and tables 4-byte

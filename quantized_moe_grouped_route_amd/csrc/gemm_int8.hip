@@ -210,6 +210,14 @@ struct Int8Args {
   int first;               // sorted row that a, base and out begin at (GRAD: of a round of rows)
 };
 
+// An accumulator with its scales.  The weight's goes first: an accumulator is zero
+// or at least 1 and below 2^31, so that only a w_scale past 2^96 can leave fp32's
+// range before the result does, whatever a_scale is.  (a_scale * w_scale first
+// made NaN of accumulators of zero, and lost the bits of small products.)
+__device__ __forceinline__ float scaled(int acc, float w_scale, float a_scale) {
+  return a_scale * (w_scale * (float)acc);
+}
+
 // Epilogue of one tile: value i of accumulator [wo][xo] in lane l is weight
 // row kWaveCols wn + 16wo + 4(l/16) + i of the tile and A row 16(XO wm + xo) +
 // l%16.
@@ -246,7 +254,7 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
         float o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          o[i] = silu<OUT>(sa[xo] * sw[wo][i] * (float)acc[wo][xo][i]) * (sa[xo] * sw[wo + H][i] * (float)acc[wo + H][xo][i]);
+          o[i] = silu<OUT>(scaled(acc[wo][xo][i], sw[wo][i], sa[xo])) * scaled(acc[wo + H][xo][i], sw[wo + H][i], sa[xo]);
         put4<OUT>(g.out, orow * I + col0, o);
       }
     } else {
@@ -277,7 +285,7 @@ __device__ __forceinline__ void epilogue(const TileAt& t, const float* sb, int w
         } else {
           float o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = sa[xo] * sw[wo][i] * (float)acc[wo][xo][i];
+          for (int i = 0; i < 4; ++i) o[i] = scaled(acc[wo][xo][i], sw[wo][i], sa[xo]);
           put4<OUT>(g.out, orow * g.N + col0, o);
         }
       }
@@ -730,7 +738,7 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
         float v[4], u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[i] = sa * sw[i] * (float)acc[i];
+          v[i] = scaled(acc[i], sw[i], sa);
           u[i] = __shfl_xor(v[i], 32, 64);  // quarters 0, 1 hold gates, 2, 3 the ups
         }
         if (l16 < rows && quarter < 2) {
@@ -746,7 +754,7 @@ __global__ __launch_bounds__(64 * dd::kWaves) void int8_decode(Int8Args g) {
         } else {
           float o[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = sa * sw[i] * (float)acc[i];
+          for (int i = 0; i < 4; ++i) o[i] = scaled(acc[i], sw[i], sa);
           put4<OUT>(g.out, idx, o);
         }
       }

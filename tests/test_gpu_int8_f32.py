@@ -1,4 +1,5 @@
-"""SiLU·up of f32 rows keeps f32's bits, whatever the gate.
+"""SiLU·up of f32 rows keeps f32's bits, whatever the gate, and the gated or plain
+product its range, whatever the scales.
 
 With u = 2^-24: exp(-|g|) to 1 ulp, 2 u; the sum, the reciprocal and the product
 by exp, 1 u each: sig(g) and sig(-g) to 5 u (2 u of exp count by at most 1/2 in
@@ -84,3 +85,33 @@ def test_gated_gemm_of_large_gates(sched):
     h = host(p.run(F32, act="silu_mul", sched=sched))[:p.n]
     floor = 2.0 ** -148 * (1 + np.abs(g)) * (1 + np.abs(y[:, 272:]))
     within(h, ref, half_step(ref, F32) + (8 + 3 * (1 + np.abs(g) * c) + 3) * U * np.abs(ref) + floor)
+
+
+@pytest.mark.parametrize("sched", ["decode", "prefill"])
+@pytest.mark.parametrize("rows", [5, 70])
+def test_scales_whose_product_leaves_the_range(rows, sched):
+    # powers of two, so that every result within the range is exact
+    N, K = 64, 128
+    a = torch.full((rows, K), 64, dtype=torch.int8, device="cuda")
+    a[1] = 0                                                  # a row of zeros: zeros, whatever its scale
+    w = torch.full((1, N, K), 64, dtype=torch.int8, device="cuda")
+    w[0, 3::4] = 0                                            # and so are columns of zeros
+    acc = 64.0 * 64 * K                                       # 2^19
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    for ea, ew in ((120, 90), (127, 95), (121, -148), (-130, -20), (-149, 95), (100, -149), (-60, -80)):
+        # ea, ew at the ends: a_scale * w_scale leaves the range, or keeps no bits
+        sa = torch.full((rows,), 2.0 ** ea, dtype=torch.float64).float().cuda()
+        sw = torch.full((1, N), 2.0 ** ew, dtype=torch.float64).float().cuda()
+        exact = acc * 2.0 ** ea * 2.0 ** ew
+        want = np.full((rows, N), np.float32(exact) if exact < 2.0 ** 128 else np.float32("inf"), np.float32)
+        want[1], want[:, 3::4] = 0, 0
+        y = mq.grouped_gemm_qint8(a, sa, w, sw, off, None, 1, out_dtype=F32, sched=sched)
+        assert np.array_equal(y.cpu().numpy(), want), (ea, ew)
+        # gates of zero beside any scale: zero; ups of zero too, where the gate is finite
+        g = mq.grouped_gemm_qint8(a, sa, w, sw, off, None, 1, act="silu_mul", out_dtype=F32, sched=sched).cpu().numpy()
+        assert not g[1].any()
+        if np.isfinite(want).all():
+            v = want.astype(np.float64)
+            assert not g[:, 3::4].any()
+            ref = oracle.silu_gate(v)
+            within(g.astype(np.float64), ref, half_step(ref, F32) + 20 * U * np.abs(ref) + 2.0 ** -148 * (1 + np.abs(v[:, 32:])))
