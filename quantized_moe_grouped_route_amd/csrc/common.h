@@ -143,6 +143,9 @@ __device__ __forceinline__ void expert_range(const int* __restrict__ offsets, in
   hi = max(min(max(offsets[e + 1], first) - first, P), lo);
 }
 
+// Tiles of bm rows that m rows take.  Unsigned, as m + bm - 1 can pass 2^31.
+__device__ __forceinline__ int tiles_of(int m, int bm) { return (int)(((u32)m + (u32)bm - 1) / (u32)bm); }
+
 // Builds tile_start in LDS.  Needs blockDim.x threads, E+1 ints of LDS in
 // `tile_start` and 2*kMaxWaves ints in `scratch`.  Ends with a barrier.
 constexpr int kMaxWaves = 16;
@@ -158,7 +161,7 @@ __device__ inline void sched_build(int* tile_start, int* scratch, const int* __r
     int lo, hi;
     expert_range(offsets, e, P, lo, hi, first);
     const int m = hi - lo;
-    local += m > 0 ? ((m + bm - 1) / bm) * n_tiles : 0;
+    local += m > 0 ? tiles_of(m, bm) * n_tiles : 0;
   }
   // Inclusive scan of `local` across the workgroup.
   int incl = local;
@@ -184,7 +187,7 @@ __device__ inline void sched_build(int* tile_start, int* scratch, const int* __r
     int lo, hi;
     expert_range(offsets, e, P, lo, hi, first);
     const int m = hi - lo;
-    run += m > 0 ? ((m + bm - 1) / bm) * n_tiles : 0;
+    run += m > 0 ? tiles_of(m, bm) * n_tiles : 0;
   }
   if (tid == nt - 1) tile_start[E] = run;
   __syncthreads();
@@ -214,7 +217,7 @@ __device__ __forceinline__ Tile sched_tile(const int* tile_start, const int* __r
   int lo, hi;
   expert_range(offsets, e, P, lo, hi);
   const int m = hi - lo;
-  const int mtiles = (m + bm - 1) / bm;
+  const int mtiles = tiles_of(m, bm);
   const int group = local / (GROUP_M * n_tiles);
   const int in_group = local - group * GROUP_M * n_tiles;
   const int gm = min(GROUP_M, mtiles - group * GROUP_M);

@@ -104,7 +104,7 @@ __device__ __forceinline__ Tile4 tile_of(const int* tile_start, const int* __res
   const int lo = min(max(ld_uniform_i32(offsets, e), 0), P);
   const int hi = min(max(ld_uniform_i32(offsets, e + 1), lo), P);
   const int m = hi - lo;
-  const int mtiles = (m + kBM - 1) / kBM;
+  const int mtiles = tiles_of(m, kBM);
   const int group = local / (kGroupM * n_tiles);
   const int in_group = local - group * kGroupM * n_tiles;
   const int gm = min(kGroupM, mtiles - group * kGroupM);

@@ -101,7 +101,7 @@ __device__ __forceinline__ TileAt tile_at(const int* tile_start, const int* __re
   const int lo = min(max(ld_uniform(offsets, e), first) - first, P);
   const int hi = max(min(max(ld_uniform(offsets, e + 1), first) - first, P), lo);
   const int m = hi - lo;
-  const int mtiles = (m + bm - 1) / bm;
+  const int mtiles = tiles_of(m, bm);
   const int group = local / (kGroupM * n_tiles);
   const int in_group = local - group * kGroupM * n_tiles;
   const int gm = min(kGroupM, mtiles - group * kGroupM);
@@ -1026,8 +1026,8 @@ hipError_t launch_gemm_int8_bwd(const GroupedArgs& g, const void* dy, const int8
     const uint16_t* y = static_cast<const uint16_t*>(dy) + first * g.N;
 #define MOEQ_PLANES(WAVES, LOADS)                                                                                  \
   do {                                                                                                             \
-    const int rows = WAVES == 1 ? 4 : 1;                                                                           \
-    const dim3 grid(std::min((P + rows - 1) / rows, g.num_cus * 8)), block(64 * WAVES * rows);                     \
+    const int64_t rows = WAVES == 1 ? 4 : 1;                                                                       \
+    const dim3 grid((int)std::min<int64_t>((P + rows - 1) / rows, g.num_cus * 8)), block(64 * WAVES * rows);       \
     if (bf)                                                                                                        \
       hipLaunchKernelGGL((grad_planes<OUT_BF16, WAVES, LOADS>), grid, block, 0, stream, y, w_scale, g.offsets,     \
                          g.E, (int)first, P, g.N, planes, step);                                                   \
