@@ -587,7 +587,7 @@ moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t ro
  * Requires K % 128 == 0 and N % 32 == 0 (else MOEQ_EALIGN), N < 131072 and
  * K <= 131072, 1 <= E <= 1024, P < 2^31, 16-byte aligned pointers (4-byte for
  * the table and w_scale), outputs disjoint from the inputs and each other, and
- * sizes that one launch can count (else MOEQ_EINVAL).  The workspace size of
+ * sizes that one launch can count, (P/32 + E) * K/128 < 2^30 (else MOEQ_EINVAL).  The workspace size of
  * arguments outside these ranges is 0.
  * ---------------------------------------------------------------------- */
 size_t grouped_gemm_qint8_backward_workspace_bytes(int64_t P, int32_t E, int64_t N, int64_t K); /* host */

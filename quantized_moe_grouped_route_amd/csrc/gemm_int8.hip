@@ -994,15 +994,14 @@ hipError_t launch_gemm_int8(const GroupedArgs& g, const int8_t* a, const float* 
   }
 }
 
-// Work items, and the stages that one workgroup counts, stay below 2^30.
-bool int8_fits(int64_t P, int E, int64_t N, int64_t K) {
-  const int64_t items = (P / dd::kM + E) * (N / dd::kRowsW);
-  return items < (1 << 30) && (items / 64 + 1) * (K / kRowBytes) < (1 << 30);
+// Work items are counted in 32 bits.  Every expert adds at most one partial item,
+// and the tiles are fewer than the streamed items (GRAD: than the narrow tiles).
+bool int8_fits(int64_t P, int E, int64_t N) {
+  return (P / dd::kM + E) * (N / dd::kRowsW) < (1 << 30);
 }
-bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K) {
+bool int8_bwd_fits(int64_t P, int E, int64_t K) {
   typedef Gradient::Narrow C;
-  const int64_t tiles = (P / (C::kBM / kPlanes) + E) * (K / C::kBN);
-  return tiles < (1 << 30) && (tiles / 64 + 1) * (plane_pitch((int)N) / kRowBytes) < (1 << 30);
+  return (P / (C::kBM / kPlanes) + E) * (K / C::kBN) < (1 << 30);
 }
 
 // Bytes of the workspace that one row takes: its planes and its step.

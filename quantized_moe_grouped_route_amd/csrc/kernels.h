@@ -79,8 +79,8 @@ hipError_t launch_gemm_nvfp4(const GroupedArgs& g, const uint16_t* x, const uint
 // W8A8: whether every launch of these sizes fits, the GEMM, and its gradient
 // towards the activations (GroupedArgs: offsets, E, P, N, K, out = dx and its
 // kind, which is dy's; the other fields are not read).
-bool int8_fits(int64_t P, int E, int64_t N, int64_t K);
-bool int8_bwd_fits(int64_t P, int E, int64_t N, int64_t K);
+bool int8_fits(int64_t P, int E, int64_t N);
+bool int8_bwd_fits(int64_t P, int E, int64_t K);
 hipError_t launch_gemm_int8(const GroupedArgs& g, const int8_t* a, const float* a_scale, const int8_t* w,
                             const float* w_scale, hipStream_t stream);
 // The least workspace, and the one beyond which more is not used.

@@ -205,7 +205,7 @@ moeq::LoraArgs lora_args(moeq_dtype dtype, int a_row, const float* scale, const 
 
 bool int8_bwd_sizes_ok(int64_t P, int32_t E, int64_t N, int64_t K) {
   return P >= 0 && P < (int64_t(1) << 31) && E >= 1 && E <= kMaxE && N >= 32 && N < (1 << 17) && N % 32 == 0 &&
-         K >= 128 && K <= (1 << 17) && K % 128 == 0 && moeq::int8_bwd_fits(P, E, N, K);
+         K >= 128 && K <= (1 << 17) && K % 128 == 0 && moeq::int8_bwd_fits(P, E, K);
 }
 
 // Checks shared by moe_silu_mul and its gradient.
@@ -620,9 +620,9 @@ moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t ro
   if (a_row == MOEQ_AROW_TOKEN && sorted_pair_ids ? rows_a * topk < P : rows_a < P)
     return fail(MOEQ_EINVAL, "%s: rows_a=%lld is too few for P=%lld", fn, (long long)rows_a, (long long)P);
   if (sched < MOEQ_SCHED_AUTO || sched > MOEQ_SCHED_PREFILL) return fail(MOEQ_EINVAL, "%s: sched %d", fn, sched);
-  if (!moeq::int8_fits(P, E, N, K))
-    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld are too large for one launch", fn, (long long)P, E,
-                (long long)N, (long long)K);
+  if (!moeq::int8_fits(P, E, N))
+    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld are too large for one launch", fn, (long long)P, E,
+                (long long)N);
   const int64_t cols = act == MOEQ_ACT_SILU_MUL ? N / 2 : N;
   const Span outs[] = {{out, P * cols * (out_dtype == MOEQ_I32 ? 4 : float_bytes(out_dtype))}},
              ins[] = {{a, rows_a * K}, {a_scale, rows_a * 4}, {w, E * N * K}, {w_scale, E * N * 4},
@@ -651,8 +651,8 @@ moeq_status grouped_gemm_qint8_backward(const void* dy, moeq_dtype dtype, const 
   if (K % 128 != 0) return fail(MOEQ_EALIGN, "%s: K=%lld must be a multiple of 128", fn, (long long)K);
   if (N % 32 != 0) return fail(MOEQ_EALIGN, "%s: N=%lld must be a multiple of 32", fn, (long long)N);
   if (!int8_bwd_sizes_ok(P, E, N, K))
-    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, N=%lld, K=%lld are too large for one launch", fn, (long long)P, E,
-                (long long)N, (long long)K);
+    return fail(MOEQ_EINVAL, "%s: P=%lld, E=%d, K=%lld are too large for one launch", fn, (long long)P, E,
+                (long long)K);
   if (!w || !w_scale || !expert_offsets || (P > 0 && (!dy || !dx))) return fail(MOEQ_EINVAL, "%s: null pointer", fn);
   if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(base, 16) || !aligned(dx, 16) || !aligned(workspace, 16) ||
       !aligned(w_scale, 4) || !aligned(expert_offsets, 4))
