@@ -553,9 +553,11 @@ moeq_status moe_quantize_int8(const void* x, moeq_dtype x_dtype, int64_t rows, i
  * rows_a >= P (SORTED), out disjoint from the inputs, and sizes that one
  * launch can count, (P/16 + E) * N/16 < 2^30 (else MOEQ_EINVAL).
  * Two schedules give identical outputs: MFMA tiles of 64, 128 or 256 rows
- * (PREFILL, by the average rows of an expert), and waves streaming 16 weight
+ * by 128 or 256 columns (PREFILL: the size of the least estimated cost by P, E,
+ * N and the number of compute units), and waves streaming 16 weight
  * rows x at most 16 routed rows (DECODE).  AUTO streams when P < 10 * E, and
- * where every wave of the GPU gets at most one such item.
+ * where every wave of the GPU gets at most one such item; it cannot see skewed
+ * routing, under which PREFILL is faster from fewer rows on.
  * ---------------------------------------------------------------------- */
 moeq_status grouped_gemm_qint8(const int8_t* a, const float* a_scale, int64_t rows_a, moeq_arow a_row, const int8_t* w,
                                const float* w_scale, const int32_t* expert_offsets, const int32_t* sorted_pair_ids,

@@ -17,9 +17,11 @@
 //
 // Measured, 8 experts, 16384 rows, f16: gate+up 4096 -> 28672 with SiLU 1.58-1.71
 // ms (2.26-2.44 POP/s; the MFMAs alone take 1.15 ms at the clock that they are
-// left), its gradient 5.51 ms with the planes' 0.49 (two planes: 3.68).  256
-// experts, 32768 rows under Zipf, gradient 7168 -> 2048, bf16: 1.91 ms with the
-// planes' 0.25 (two planes: 1.54).  8 tokens to 8 of 256 experts, 7168 -> 4096: 243 us, the weights at 7.0 TB/s.
+// left), its gradient 5.51-5.58 ms with the planes' 0.49 (two planes: 3.67-3.77).
+// 256 experts, 32768 rows under Zipf, gradient 7168 -> 2048, bf16: 1.90-1.92 ms
+// with the planes' 0.25 (two planes: 1.54-1.59), 7.6 GB read past the L2s at 4.5
+// TB/s.  8 tokens to 8 of 256 experts, 7168 -> 4096: 241-253 us, the weights at 6.7
+// to 7.0 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -921,10 +923,12 @@ double cost(const Int8Args& g, int num_cus, double one) {
   return one * std::max(1.0, mt * (double)n_tiles<C, MODE>(g) / num_cus);
 }
 
-// The tile of the least cost.  Relative times of a tile, measured with 32
-// experts of 4096 x 4096 and 512 rows each (310, 322 and 431 us for 256, 128 and
-// 64 rows): 1, 0.54, 0.36.  At 128 rows an expert the call takes 156, 140 and 153
-// us, at 16 rows 134, 104 and 103.
+// The tile of the least cost.  Relative times of a tile: 1, 0.54, 0.36, 0.22, from
+// 32 experts of 4096 x 4096, bf16, each tile forced, 256, 128 and 64 rows x 256 and
+// 64 x 128, us: 512 rows each 315, 319, 430 and 520, 128 rows 155, 139, 153 and
+// 171, 64 rows 143, 112, 120 and 125, 16 rows 134, 104, 103 and 103 (by the rule
+// 512 rows take 128-row tiles, 64 rows 64-row ones).  4 of 256 x 256 with 256 rows:
+// 18.6, 12.8, 10.3 and 9.2.
 template <int OUT, int MODE>
 hipError_t go_prefill(const Int8Args& g, int num_cus, hipStream_t stream) {
   typedef Forward F;
@@ -951,10 +955,15 @@ hipError_t go_gradient(const Int8Args& g, int num_cus, hipStream_t stream) {
   return go_tiles<B::Large, OUT, GRAD>(g, num_cus, stream);
 }
 
-// AUTO streams below 10 rows an expert: with 32 experts of 4096 x 4096, 4 rows
-// each take 85 us streamed and 103 in tiles, 10 rows 86 and 100, 12 rows 102 and
-// 101, 16 rows 125 and 101 (experts past 16 rows stream their weights again);
-// with 256 experts of 2048 x 2048 6 rows take 170 and 183, 10 rows 190 and 187.
+// AUTO streams below 10 rows an expert on average: with 32 experts of 4096 x 4096,
+// 4 rows each take 83 us streamed and 102 in tiles, 8 rows 84 and 102, 10 rows 87
+// and 100, 12 rows 107 and 101, 16 rows 125 and 100 (experts past 16 rows stream
+// their weights again); with 256 experts of 2048 x 2048 8 rows take 180 and 185, 10
+// rows 191 and 187.  The counts are on the device, so the rule cannot see skewed
+// routing, where the large experts' weights stream more than once: under Zipf 4
+// rows an expert take 67 and 88 us with the 32 experts, 8 rows 97 and 97; with the
+// 256, 129 and 134, 187 and 163.  A caller that knows of stronger skew asks for
+// PREFILL.
 // And where no wave gets a second item, so that a call is as long as one item:
 // one expert of 4096 x 4096 with 64 rows 11 us streamed and 22 in tiles, with 256
 // rows 26 and 22.
